@@ -261,6 +261,136 @@ tg_status_t tg_gemm_sp24(int32_t in_dtype, const void* Ac, const void* E, const 
                          int64_t ldac, int64_t lde, int64_t ldb, int64_t ldc,
                          const tg_epilogue_ex_t* epi, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit weights with group scales: C = out(act(A · W^T + bias) + R).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * tg_gemm_w4 — the product of the rows of A with a weight held in 4-bit
+ * integer codes, with a scale and, where given, a zero point for each group
+ * of `group` consecutive k of a row, asynchronous on `stream`:
+ *
+ *   code(n, k)  byte Bq[n*ldbq + k/2], low nibble for even k, high nibble for
+ *               odd k: 0..15.  One row of packed codes per column n of C (the
+ *               [out][in] orientation of a linear layer's weight);
+ *   s(g, n)     Bscale[g*ldbs + n], of type in_dtype, g = k / group;
+ *   z(g, n)     the low four bits of Bzero[g*ldbz + n], or 8 if Bzero is NULL;
+ *   W[n][k]     = (code(n, k) - z(k/group, n)) · s(k/group, n);
+ *   C[m][n]     = out(act(sum_k A[m][k]·W[n][k] + bias[n]) + R[m][n])
+ *
+ * with the epilogue of tg_gemm_ex (fp32 sums, one rounding at the end).
+ *
+ * in_dtype  TG_DTYPE_F16 or TG_DTYPE_BF16: the type of A, Bscale and R.
+ * group     32, 64 or 128; K need not be a multiple of it (the last group is
+ *           then shorter).
+ * A         device, row-major M×K, row stride lda ≥ K, 2-byte aligned.
+ * Bq        device, N rows of ceil(K/2) bytes, row stride ldbq ≥ ceil(K/2);
+ *           16-byte aligned, ldbq a multiple of 16 (else TG_ERR_MISALIGNED).
+ *           A spare high nibble (odd K) is ignored.
+ * Bscale    device, ceil(K/group) rows of N, row stride ldbs ≥ N; 16-byte
+ *           aligned, ldbs a multiple of 8 (else TG_ERR_MISALIGNED).
+ * Bzero     device, ceil(K/group) rows of N bytes, row stride ldbz ≥ N, 16-byte
+ *           aligned, ldbz a multiple of 16 (else TG_ERR_MISALIGNED); or NULL.
+ * C, ldc, epi, stream  as tg_gemm_ex.
+ * Few rows: the codes are streamed once, no weight is rounded (the group sums
+ *           of A·(code - z) are scaled in fp32).
+ * Many rows: W is decoded once to in_dtype (each weight rounded) into a
+ *           buffer of K × roundup(N, 8) elements that belongs to the (device,
+ *           stream), is grown on demand and kept until process exit, and the
+ *           dense GEMM runs on it.  The first call of a size on a stream has to
+ *           come before any capture (else TG_ERR_NO_MEMORY).
+ * K == 0:   C = out(act(bias) + R); A, Bq, Bscale and Bzero may be NULL.
+ * Errors:   TG_ERR_INVALID_VALUE for an unknown type, activation or group, a
+ *           size out of range, a stride below its row, a NULL pointer where one
+ *           is needed; TG_ERR_MISALIGNED as above; all before anything is
+ *           enqueued.  Otherwise as tg_gemm_ex.
+ */
+tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* Bq, const void* Bscale,
+                       const void* Bzero, void* C, int64_t M, int64_t N, int64_t K,
+                       int32_t group, int64_t lda, int64_t ldbq, int64_t ldbs, int64_t ldbz,
+                       int64_t ldc, const tg_epilogue_ex_t* epi, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The norms after and before a block, with its gate and residual scale.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * What the forward and the backward call share.  Per row (rms over the
+ * row's `cols` values, everything in fp32, each output rounded once):
+ *
+ *   o = x / sqrt(mean(x²) + eps) · post_weight     (post_weight NULL: o = x)
+ *   y = residual + scale · gate ⊙ o                (residual NULL: 0, gate NULL: 1)
+ *   h = y / sqrt(mean(y²) + eps) · pre_weight      (from y before it is rounded)
+ *
+ * x, gate and h are of type `dtype`; residual and y of `stream_dtype`, which is
+ * the same type or TG_DTYPE_F32.  The weights are fp32, `cols` values each.
+ * The gate has gate_rows rows, a divisor of `rows`: row i of x takes row
+ * i / (rows / gate_rows) of it (1: one for all, rows: one for each).
+ * Matrices are row-major with any stride of at least cols elements, aligned to
+ * their element.
+ */
+typedef struct {
+    int32_t dtype;            /* tg_dtype_t of x, gate, h and their gradients       */
+    int32_t stream_dtype;     /* tg_dtype_t of residual, y and their gradients      */
+    int64_t rows, cols;       /* rows in [0, 2^31 - 1], cols in [0, 32768]          */
+    const void* x;            /* device, the block's output                         */
+    int64_t ldx;
+    const void* residual;     /* device, or NULL                                    */
+    int64_t ldr;
+    const float* post_weight; /* device, or NULL: no norm after the block           */
+    const void* gate;         /* device, or NULL                                    */
+    int64_t ldg;
+    int64_t gate_rows;        /* used when gate is not NULL                         */
+    const float* pre_weight;  /* device, or NULL: no norm before the next block     */
+    float scale, eps;         /* eps ≥ 0                                            */
+} tg_norm_t;
+
+/*
+ * tg_norm_residual — y and h above, asynchronous on `stream`.
+ * y may be NULL (not written) and may be the residual's own buffer (same
+ * pointer and stride); any other overlap is undefined.  h is given exactly when
+ * pre_weight is.  rows == 0 or cols == 0: nothing is done.
+ * Errors: TG_ERR_INVALID_VALUE for an unknown type, a size out of range, a
+ * stride below cols, gate_rows that do not divide rows, a NULL x, h without
+ * pre_weight or the reverse, a negative or NaN eps; TG_ERR_MISALIGNED; all
+ * before anything is enqueued.  TG_ERR_LAUNCH if a launch fails.
+ */
+tg_status_t tg_norm_residual(const tg_norm_t* n, void* y, int64_t ldy, void* h, int64_t ldh,
+                             void* stream);
+
+/* The gradients that come in and go out; any of them may be NULL: no gradient
+ * (zero) for an input, not wanted for an output. */
+typedef struct {
+    const void* dy;      /* device, rows × cols of stream_dtype                     */
+    int64_t lddy;
+    const void* dh;      /* device, rows × cols of dtype; needs pre_weight          */
+    int64_t lddh;
+    void* dx;            /* device, rows × cols of dtype                            */
+    int64_t lddx;
+    void* dresidual;     /* device, rows × cols of stream_dtype                     */
+    int64_t lddr;
+    void* dgate;         /* device, gate_rows × cols of dtype; needs gate           */
+    int64_t lddg;
+    float* dpost_weight; /* device, cols values; needs post_weight                  */
+    float* dpre_weight;  /* device, cols values; needs pre_weight                   */
+} tg_norm_grad_t;
+
+/*
+ * tg_norm_residual_backward — the gradients of the call that tg_norm_residual
+ * makes with the same `n`, asynchronous on `stream`.  The statistics are made
+ * again from x and residual (not y): nothing is kept by the forward call, whose
+ * inputs have to be unchanged (no y in the residual's place).
+ * Sums over rows are taken in fp32 in a fixed order: the same call gives the
+ * same bits.  Outputs are written, not added to; they overlap no input and not
+ * one another.  rows == 0: the weights' and the gate's gradients are zero.
+ * The shares of the column sums lie in a workspace that belongs to the (device,
+ * stream), is grown on demand and kept until process exit; the first call of a
+ * size on a stream has to come before any capture (else TG_ERR_NO_MEMORY).
+ * Errors: as tg_norm_residual; TG_ERR_INVALID_VALUE for a gradient without what
+ * it needs.
+ */
+tg_status_t tg_norm_residual_backward(const tg_norm_t* n, const tg_norm_grad_t* g, void* stream);
+
 /*
  * tg_sync_status — wait for `stream`, then report (and clear) a device-side
  * timeout recorded by any libtgemm kernel on the current device since the

@@ -1,7 +1,8 @@
 """Python binding for libtgemm (dense FP16 GEMM on GB300, sm_103a).
 
-Argument marshalling only: every step of C = epi(A·B) runs in the CUDA
-kernels of ``libtgemm.so``, called through its C ABI (``include/tgemm.h``).
+Argument marshalling only: every step of C = epi(A·B), of the products with
+4-bit weights and of the norms around a block runs in the CUDA kernels of
+``libtgemm.so``, called through its C ABI (``include/tgemm.h``).
 PyTorch is used for device memory and streams.  There is no fallback: if the
 shared library is missing, the first call raises ImportError.
 
@@ -12,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtgemm.so")
@@ -42,7 +44,7 @@ EXPORTS = (
     "tg_tile_coord", "tg_ring_bytes", "tg_debug_set_wait_timeout_ns", "tg_debug_inject",
     "tg_gemm_f16_noalloc", "tg_gemm_bf16", "tg_gemm_ex", "tg_gemm_mxfp4", "tg_gemm_sp24",
     "tg_gemm_f16_host", "tg_plan_f16_limits", "tg_device_limits", "tg_debug_last_launch",
-    "tg_debug_map_cache_stats",
+    "tg_debug_map_cache_stats", "tg_gemm_w4", "tg_norm_residual", "tg_norm_residual_backward",
 )
 
 #: bytes of the library's fixed scratch array used by tg_gemm_f16_noalloc
@@ -69,6 +71,29 @@ class tg_epilogue_ex_t(ctypes.Structure):
     _fields_ = [
         ("activation", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
         ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+    ]
+
+
+class tg_norm_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("post_weight", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_rows", ctypes.c_int64),
+        ("pre_weight", ctypes.c_void_p), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+    ]
+
+
+class tg_norm_grad_t(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+        ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+        ("dresidual", ctypes.c_void_p), ("lddr", ctypes.c_int64),
+        ("dgate", ctypes.c_void_p), ("lddg", ctypes.c_int64),
+        ("dpost_weight", ctypes.c_void_p), ("dpre_weight", ctypes.c_void_p),
     ]
 
 
@@ -103,6 +128,15 @@ def _L():
     lib.tg_gemm_sp24.argtypes = [ctypes.c_int32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                  _i64, _i64, _i64, ctypes.POINTER(tg_epilogue_ex_t), _vp]
     lib.tg_gemm_sp24.restype = ctypes.c_int
+    lib.tg_gemm_w4.argtypes = [ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                               ctypes.c_int32, _i64, _i64, _i64, _i64, _i64,
+                               ctypes.POINTER(tg_epilogue_ex_t), _vp]
+    lib.tg_gemm_w4.restype = ctypes.c_int
+    lib.tg_norm_residual.argtypes = [ctypes.POINTER(tg_norm_t), _vp, _i64, _vp, _i64, _vp]
+    lib.tg_norm_residual.restype = ctypes.c_int
+    lib.tg_norm_residual_backward.argtypes = [ctypes.POINTER(tg_norm_t),
+                                              ctypes.POINTER(tg_norm_grad_t), _vp]
+    lib.tg_norm_residual_backward.restype = ctypes.c_int
     lib.tg_sync_status.argtypes = [_vp]
     lib.tg_sync_status.restype = ctypes.c_int
     lib.tg_status_string.argtypes = [ctypes.c_int]
@@ -186,6 +220,27 @@ def tg_gemm_sp24(in_dtype: int, Ac: int, E: int, B: int, C: int, M: int, N: int,
     metadata words E), integer device pointers; returns the status code."""
     return _L().tg_gemm_sp24(in_dtype, Ac, E, B, C, M, N, K, ldac, lde, ldb, ldc,
                              ctypes.byref(epi) if epi is not None else None, stream or None)
+
+
+def tg_gemm_w4(in_dtype: int, A: int, Bq: int, Bscale: int, Bzero: int | None, C: int, M: int,
+               N: int, K: int, group: int, lda: int, ldbq: int, ldbs: int, ldbz: int, ldc: int,
+               epi: tg_epilogue_ex_t | None, stream: int | None) -> int:
+    """C = out(act(A·W^T + bias) + R) with W in 4-bit codes and group scales,
+    integer device pointers; returns the status code."""
+    return _L().tg_gemm_w4(in_dtype, A, Bq, Bscale, Bzero or None, C, M, N, K, group, lda, ldbq,
+                           ldbs, ldbz, ldc, ctypes.byref(epi) if epi is not None else None,
+                           stream or None)
+
+
+def tg_norm_residual(n: tg_norm_t, y: int | None, ldy: int, h: int | None, ldh: int,
+                     stream: int | None) -> int:
+    """The norms around a block with integer device pointers; returns the status code."""
+    return _L().tg_norm_residual(ctypes.byref(n), y or None, ldy, h or None, ldh, stream or None)
+
+
+def tg_norm_residual_backward(n: tg_norm_t, g: tg_norm_grad_t, stream: int | None) -> int:
+    """Their gradient with integer device pointers; returns the status code."""
+    return _L().tg_norm_residual_backward(ctypes.byref(n), ctypes.byref(g), stream or None)
 
 
 def tg_sync_status(stream: int | None) -> int:
@@ -462,6 +517,255 @@ def gemm_sp24(ac, e, b, relu: bool = False, out=None, stream=None, *, bias=None,
     if st != TG_OK:
         raise TgemmError(st, "tg_gemm_sp24")
     return out
+
+
+def _on_stream(device, stream, used, body):
+    """``body(raw stream)`` with ``device`` current, its allocations made on the
+    stream that it launches on.  ``used``: the caller's tensors, kept from reuse
+    until that stream is done with them where it is not the current one."""
+    import torch
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(device):
+            return body(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            made = body(stream.cuda_stream)
+        if here.cuda_stream != stream.cuda_stream:
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
+            for t in made if isinstance(made, tuple) else (made,):
+                if t is not None:
+                    t.record_stream(here)
+    return made
+
+
+def _check_rows(t, name: str, rows: int, cols: int, dtype, device):
+    """A rows × cols tensor of ``dtype`` with unit column stride, on ``device``."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.device != device:
+        raise ValueError(f"{name} must be {rows}×{cols} on {device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+
+
+def _check_vector(t, name: str, size: int, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 1 \
+            or t.shape[0] != size or t.device != device or (size > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {size} elements")
+
+
+def gemm_w4(a, bq, bscale, N: int, group: int, relu: bool = False, out=None, stream=None, *,
+            bzero=None, bias=None, residual=None, out_dtype=None):
+    """C = out(act(a @ W.T + bias) + residual) with the weight W (N × K) in
+    4-bit codes: W[n][k] = (code[n][k] - zero[k // group][n]) · scale[k // group][n].
+
+    a: CUDA float16 or bfloat16 tensor M×K (row-major).  bq: CUDA uint8 tensor
+    of N rows of packed codes along k, low nibble first (row stride a multiple
+    of 16 bytes, at least ceil(K/2)).  group: 32, 64 or 128.  bscale: tensor of
+    a's dtype, ceil(K/group) rows of N scales (row stride a multiple of 8).
+    bzero: optional uint8 tensor of ceil(K/group) rows of N zero points 0..15
+    (row stride a multiple of 16); without it every zero point is 8.  bias,
+    residual, out_dtype, out and stream as for ``gemm``.
+    """
+    import torch
+    _check_operand(a, "a")
+    M, K = a.shape
+    dtype, device = a.dtype, a.device
+    if not a.is_cuda:
+        raise ValueError("a must be a CUDA tensor")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    groups = (K + group - 1) // group
+    for t, name, kind, rows, width in ((bq, "bq", torch.uint8, N, (K + 1) // 2),
+                                       (bscale, "bscale", dtype, groups, N),
+                                       (bzero, "bzero", torch.uint8, groups, N)):
+        if t is None and name == "bzero":
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != kind or t.dim() != 2:
+            raise TypeError(f"{name} must be a 2-D {kind} tensor")
+        if t.shape[0] != rows or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be {rows} rows of at least {width}, row-major")
+        if t.device != device:
+            raise ValueError(f"{name} must be on a's device")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else dtype
+    if out_dtype not in (dtype, torch.float32):
+        raise TypeError(f"out_dtype must be {dtype} or torch.float32, got {out_dtype}")
+    if out is not None:
+        _check_rows(out, "out", M, N, out_dtype, device)
+    if bias is not None:
+        _check_vector(bias, "bias", N, device)
+    if residual is not None:
+        _check_rows(residual, "residual", M, N, dtype, device)
+    code = TG_DTYPE_BF16 if dtype == torch.bfloat16 else TG_DTYPE_F16
+
+    def up16(t):  # the row stride; a single row's is never used
+        return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+    def body(s):
+        c = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
+        epi = tg_epilogue_ex_t(
+            TG_EPI_RELU if relu else TG_EPI_NONE,
+            TG_DTYPE_F32 if out_dtype == torch.float32 else code,
+            bias.data_ptr() if bias is not None else None,
+            residual.data_ptr() if residual is not None else None,
+            _ld(residual) if residual is not None else 0)
+        st = _L().tg_gemm_w4(
+            code, a.data_ptr(), bq.data_ptr(), bscale.data_ptr(),
+            bzero.data_ptr() if bzero is not None else None, c.data_ptr(), M, N, K, group,
+            _ld(a), up16(bq), up16(bscale), up16(bzero) if bzero is not None else 0, _ld(c),
+            ctypes.byref(epi), s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_gemm_w4")
+        return c
+
+    return _on_stream(device, stream, (a, bq, bscale, bzero, bias, residual, out), body)
+
+
+def _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps):
+    """Checks and packs what the norms and their gradient share."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    codes = {torch.float16: TG_DTYPE_F16, torch.bfloat16: TG_DTYPE_BF16,
+             torch.float32: TG_DTYPE_F32}
+    if x.dtype not in codes:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
+    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be a 2-D row-major CUDA tensor (unit column stride)")
+    rows, cols = x.shape
+    device = x.device
+    if cols > 32768:
+        raise ValueError(f"x must have at most 32768 columns, got {cols}")
+    kind = x.dtype
+    if residual is not None:
+        kind = residual.dtype if isinstance(residual, torch.Tensor) else None
+        if kind not in (x.dtype, torch.float32):
+            raise TypeError(f"residual must be a {x.dtype} or float32 tensor")
+        _check_rows(residual, "residual", rows, cols, kind, device)
+    if post_weight is not None:
+        _check_vector(post_weight, "post_weight", cols, device)
+    if pre_weight is not None:
+        _check_vector(pre_weight, "pre_weight", cols, device)
+    gate_rows, ldg = 0, 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor) or gate.dtype != x.dtype:
+            raise TypeError(f"gate must be a {x.dtype} tensor")
+        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
+        if gate.dim() not in (1, 2) or gate.shape[-1] != cols or gate.device != device \
+                or (cols > 1 and gate.stride(-1) != 1):
+            raise ValueError(f"gate must be {cols} values, or rows of {cols}, on x's device")
+        if gate_rows < 1 or (rows > 0 and (gate_rows > rows or rows % gate_rows)):
+            raise ValueError(f"the gate's {gate_rows} rows must divide x's {rows}")
+        ldg = _ld(gate) if gate.dim() == 2 else cols
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    n = tg_norm_t(codes[x.dtype], codes[kind], rows, cols, x.data_ptr(), _ld(x),
+                  residual.data_ptr() if residual is not None else None,
+                  _ld(residual) if residual is not None else 0,
+                  post_weight.data_ptr() if post_weight is not None else None,
+                  gate.data_ptr() if gate is not None else None, ldg, gate_rows,
+                  pre_weight.data_ptr() if pre_weight is not None else None, scale, eps)
+    return n, rows, cols, kind
+
+
+def norm_residual(x, residual=None, *, post_weight=None, gate=None, scale: float = 1.0,
+                  pre_weight=None, eps: float = 1e-6, out=None, normed=None, stream=None):
+    """The norms after and before a block with its gate and residual scale:
+
+        y = residual + scale · gate ⊙ rms(x)·post_weight,   h = rms(y)·pre_weight
+
+    with rms(v) = v / sqrt(mean(v²) + eps) over each row.  Returns (y, h).
+
+    x: CUDA float16, bfloat16 or float32 tensor of rows × cols (the block's
+    output).  residual: optional tensor of x's dtype or float32; y has its dtype.
+    post_weight, pre_weight: optional float32 vectors of cols; without
+    post_weight x is taken as it is, without pre_weight h is None.  gate:
+    optional tensor of x's dtype, cols values for all rows or G rows of them,
+    each for rows / G consecutive rows of x.  y is written to ``out`` (which may
+    be ``residual`` itself) and h to ``normed`` where given.  Runs on ``stream``
+    (default: torch's current stream of x's device).
+    """
+    import torch
+    n, rows, cols, kind = _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps)
+    device = x.device
+    if out is not None:
+        _check_rows(out, "out", rows, cols, kind, device)
+    if normed is not None:
+        if pre_weight is None:
+            raise ValueError("normed needs pre_weight")
+        _check_rows(normed, "normed", rows, cols, x.dtype, device)
+
+    def body(s):
+        y = torch.empty((rows, cols), dtype=kind, device=device) if out is None else out
+        h = normed
+        if h is None and pre_weight is not None:
+            h = torch.empty((rows, cols), dtype=x.dtype, device=device)
+        st = _L().tg_norm_residual(
+            ctypes.byref(n), y.data_ptr(), _ld(y), h.data_ptr() if h is not None else None,
+            _ld(h) if h is not None else 0, s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_norm_residual")
+        return y, h
+
+    return _on_stream(device, stream, (x, residual, post_weight, gate, pre_weight, out, normed),
+                      body)
+
+
+class NormGrads(NamedTuple):
+    """Gradients of ``norm_residual``; None for an input that was not given."""
+    x: object
+    residual: object
+    gate: object
+    post_weight: object
+    pre_weight: object
+
+
+def norm_residual_backward(dy, dh, x, residual=None, *, post_weight=None, gate=None,
+                           scale: float = 1.0, pre_weight=None, eps: float = 1e-6, stream=None):
+    """The gradients of ``norm_residual`` called with the same arguments, given
+    dy and dh, the gradients of its two results (either may be None: zero).
+
+    dy has residual's dtype, dh x's.  Returns NormGrads, each gradient with its
+    input's dtype and shape.  x and residual are those of the forward call: no
+    ``out`` may have been written over them.
+    """
+    import torch
+    n, rows, cols, kind = _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps)
+    device = x.device
+    if dy is not None:
+        _check_rows(dy, "dy", rows, cols, kind, device)
+    if dh is not None:
+        if pre_weight is None:
+            raise ValueError("dh needs pre_weight")
+        _check_rows(dh, "dh", rows, cols, x.dtype, device)
+
+    def body(s):
+        def like(t):
+            return torch.empty(t.shape, dtype=t.dtype, device=device) if t is not None else None
+
+        def at(t):
+            return t.data_ptr() if t is not None else None
+
+        grads = NormGrads(like(x), like(residual), like(gate), like(post_weight),
+                          like(pre_weight))
+        g = tg_norm_grad_t(at(dy), _ld(dy) if dy is not None else 0,
+                           at(dh), _ld(dh) if dh is not None else 0,
+                           at(grads.x), cols, at(grads.residual), cols, at(grads.gate), cols,
+                           at(grads.post_weight), at(grads.pre_weight))
+        st = _L().tg_norm_residual_backward(ctypes.byref(n), ctypes.byref(g), s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_norm_residual_backward")
+        return grads
+
+    return _on_stream(device, stream, (dy, dh, x, residual, post_weight, gate, pre_weight), body)
 
 
 def gemm_host(a, b, relu: bool = False, stream=None, device=None):

@@ -1,4 +1,4 @@
-"""Build libtgemm.so in-tree with nvcc for sm_103a (no CMake, one translation unit)."""
+"""Build libtgemm.so in-tree with nvcc for sm_103a (no CMake, a few translation units at once)."""
 
 from __future__ import annotations
 
@@ -37,8 +37,8 @@ def nvcc_command(out: str = LIB, extra: list[str] | None = None) -> list[str]:
     return [
         _nvcc(), "-gencode", ARCH, "-O3", "-std=c++17", "-lineinfo",
         "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
-        "-I", INCLUDE, "-I", CSRC,
-        os.path.join(CSRC, "tgemm.cu"), "-o", out,
+        "-t", "0", "-I", INCLUDE, "-I", CSRC,
+        *(os.path.join(CSRC, f) for f in ("tgemm.cu", "w4.cu", "norm.cu")), "-o", out,
     ] + (extra or [])
 
 
