@@ -1,6 +1,8 @@
 // tg_norm_residual and tg_norm_residual_backward (include/tgemm.h): argument
 // checks, workspace and launches.  The kernels and the formulas: norm.cuh.
 #include <cstring>
+#include <set>
+#include <type_traits>
 
 #include "norm.cuh"
 #include "op_host.h"
@@ -9,6 +11,9 @@ namespace {
 
 using tg::NormGradParams;
 using tg::NormParams;
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 constexpr int64_t kMaxCols = 32768;  // a row's fp32 values have to fit in shared memory
 
@@ -71,19 +76,82 @@ tg_status_t with_types(const tg_norm_t& a, F f) {
     return wide ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-tg_status_t launched() {
-    if (cudaGetLastError() != cudaSuccess) return TG_ERR_LAUNCH;
+// The row kernels count strides in 32 bits.
+bool narrow(int64_t a, int64_t b, int64_t c, int64_t d, int64_t e) {
+    return (a | b | c | d | e) < (int64_t{1} << 32);
+}
+
+// Whether every row of a matrix (or of none) lies on 8 elements: 16 or 32 bytes.
+bool wide(const void* p, int64_t ld, int bytes) {
+    return p == nullptr || (!misaligned(p, 8 * bytes) && ld % 8 == 0);
+}
+
+// One launch with dependent launch allowed.
+template <typename... Args, typename... Given>
+tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   Given... given) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
     return TG_OK;
 }
 
-template <typename Kernel>
-bool allow_smem(Kernel k, size_t bytes) {
-    if (bytes <= 48 * 1024) return true;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(bytes)) == cudaSuccess)
-        return true;
-    cudaGetLastError();
+// Of an SM's 228 KB of shared memory, for rings (a block has 5 KB and a reserved one besides).
+constexpr int kRingBytes = 214 * 1024;
+
+// How a kernel takes rows through rings.
+struct RowPlan {
+    int threads;  // of a group
+    int groups;   // of a block
+    int stages, stage_bytes;
+    int per_sm;   // blocks
+    size_t smem;
+};
+
+// `stage`: bytes of a group's stage; `more`: of a group besides its ring; `per_sm`: the blocks that registers allow on an SM.  False if no ring fits.
+bool plan_rows(int64_t rows, int threads, int stage, int more, int per_sm, int num_sms, RowPlan* r) {
+    if (rows > tg::kOpMaxDim - 65536) return false;  // they count rows ahead in 31 bits
+    r->threads = threads;
+    r->groups = tg::kNormThreads / threads;
+    // few rows: blocks on every SM before groups in a block
+    const int64_t each = (rows + num_sms - 1) / num_sms;
+    if (r->groups > each) r->groups = static_cast<int>(each);
+    r->stage_bytes = stage;
+    for (r->per_sm = per_sm; r->per_sm >= 1; --r->per_sm)
+        for (r->stages = 4; r->stages >= (r->per_sm > 1 ? 3 : 2); --r->stages) {
+            r->smem = static_cast<size_t>(r->groups) * (r->stages * stage + more);
+            if (r->per_sm * (r->smem + 6 * 1024) <= kRingBytes + 6 * 1024) return true;
+        }
     return false;
+}
+
+// Lets a kernel use the shared memory that a block may have, once per device.
+template <typename Kernel>
+bool allow_smem(Kernel k, int dev) {
+    static std::mutex m;
+    static std::set<std::pair<const void*, int>> done;
+    const auto key = std::make_pair(reinterpret_cast<const void*>(k), dev);
+    std::lock_guard<std::mutex> lk(m);
+    if (done.count(key) != 0) return true;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.insert(key);
+    return true;
 }
 
 }  // namespace
@@ -108,12 +176,47 @@ tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, 
     if ((st = tg::op_device(&dev)) != TG_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return with_types(*a, [&](auto tx, auto tr) {
-        auto kernel = tg::tg_norm_residual_simple<decltype(tx), decltype(tr)>;
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        // whether a thread may read and write 8 neighbouring columns at a time
+        const bool vec = p.cols % 8 == 0 && wide(p.x, p.ldx, sizeof(TX)) &&
+                         wide(p.r, p.ldr, sizeof(TR)) && wide(p.gate, p.ldg, sizeof(TX)) &&
+                         wide(p.wpost, 0, 4) && wide(p.wpre, 0, 4) &&
+                         wide(p.y, p.ldy, sizeof(TR)) && wide(p.h, p.ldh, sizeof(TX));
+        RowPlan r;
+        auto plan = [&](auto ch, auto v) {
+            constexpr int CH = decltype(ch)::value;
+            constexpr bool VEC = decltype(v)::value;
+            const int threads = static_cast<int>((p.cols + 256 * CH - 1) / (256 * CH)) * 32;
+            const int bx = tg::norm_stage_bytes<TX, CH, VEC>(threads, p.cols);
+            const int stage = bx + tg::norm_stage_bytes<TR, CH, VEC>(threads, p.cols);
+            const bool one_gate = p.rows_per_gate == p.rows;
+            const int gate = p.gate != nullptr ? bx : 0;
+            return threads <= tg::kNormThreads && narrow(p.ldx, p.ldr, p.ldg, p.ldy, p.ldh) &&
+                   plan_rows(p.rows, threads, stage + (one_gate ? 0 : gate), one_gate ? gate : 0,
+                             CH == 1 && VEC ? 2 : 1, dev.num_sms, &r);
+        };
+        auto run = [&](auto kernel) {
+            if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+            const int64_t most = int64_t{r.per_sm} * dev.num_sms;
+            const int64_t blocks = (p.rows + r.groups - 1) / r.groups;
+            return launch(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                          r.threads * r.groups, r.smem, s, p, r.threads, r.stages, r.stage_bytes);
+        };
+        if (vec) {
+            if (plan(Int<1>{}, std::true_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 1, true>);
+            if (plan(Int<2>{}, std::true_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 2, true>);
+            if (plan(Int<4>{}, std::true_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 4, true>);
+        } else {
+            if (plan(Int<1>{}, std::false_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 1, false>);
+            if (plan(Int<2>{}, std::false_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 2, false>);
+            if (plan(Int<4>{}, std::false_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 4, false>);
+        }
+        auto kernel = tg::tg_norm_residual_simple<TX, TR>;
         const size_t smem = static_cast<size_t>(p.cols) * 4;
-        if (!allow_smem(kernel, smem)) return TG_ERR_LAUNCH;
+        if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
         const int64_t grid = p.rows < 8 * dev.num_sms ? p.rows : 8 * dev.num_sms;
-        kernel<<<static_cast<unsigned>(grid), 256, smem, s>>>(p);
-        return launched();
+        return launch(kernel, dim3(static_cast<unsigned>(grid)), 256, smem, s, p);
     });
 }
 
@@ -172,36 +275,84 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
         q.dwpre = nullptr;
         if (st != TG_OK) return st;
     }
-    const int64_t most = 2 * dev.num_sms;
-    int64_t blocks = a->rows < most ? a->rows : most;
-    // Many gates: a block takes whole gates.  Few: it takes rows, and the
-    // blocks' shares of a gate are summed afterwards.
-    const bool gate_sums = q.dgate != nullptr && q.n.rows_per_gate > 1;
-    if (gate_sums && q.gates >= 2 * blocks) q.whole_gates = 1;
-    const int64_t gate_slots = !gate_sums ? 0 : q.whole_gates ? blocks : blocks + q.gates;
-    const int64_t slots = (q.dwpost != nullptr ? blocks : 0) + (q.dwpre != nullptr ? blocks : 0) +
-                          gate_slots;
-    if (slots > 0) {
-        void* ws = nullptr;
-        if ((st = g_workspace.get(dev.dev, s, static_cast<size_t>(slots * cols) * 4, &ws)) != TG_OK)
-            return st;
-        float* next = static_cast<float*>(ws);
-        if (q.dwpost != nullptr) q.ws_post = next, next += blocks * cols;
-        if (q.dwpre != nullptr) q.ws_pre = next, next += blocks * cols;
-        if (gate_slots > 0) q.ws_gate = next;
-    }
     return with_types(*a, [&](auto tx, auto tr) {
-        auto kernel = tg::tg_norm_grad_simple<decltype(tx), decltype(tr)>;
-        const size_t smem = static_cast<size_t>(cols) * 4;
-        if (!allow_smem(kernel, smem)) return TG_ERR_LAUNCH;
-        kernel<<<static_cast<unsigned>(blocks), 256, smem, s>>>(q);
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        const void* in[4] = {q.n.x, q.n.r, q.dy, q.dh};
+        const int64_t ld[4] = {q.n.ldx, q.n.ldr, q.lddy, q.lddh};
+        const int elem[4] = {sizeof(TX), sizeof(TR), sizeof(TR), sizeof(TX)};
+        bool vec = cols % 8 == 0 && wide(q.n.wpost, 0, 4) && wide(q.n.wpre, 0, 4) &&
+                   wide(q.n.gate, q.n.ldg, sizeof(TX)) && wide(q.dx, q.lddx, sizeof(TX)) &&
+                   wide(q.dr, q.lddr, sizeof(TR)) && wide(q.dgate, q.lddg, sizeof(TX)) &&
+                   wide(q.dwpost, 0, 4) && wide(q.dwpre, 0, 4);
+        for (int k = 0; k < 4; ++k) vec = vec && wide(in[k], ld[k], elem[k]);
+        RowPlan r;
+        auto plan = [&](auto ch, auto v) {
+            constexpr int CH = decltype(ch)::value;
+            constexpr bool VEC = decltype(v)::value;
+            const int threads = static_cast<int>((cols + 256 * CH - 1) / (256 * CH)) * 32;
+            const int bx = tg::norm_stage_bytes<TX, CH, VEC>(threads, cols);
+            const int stage = 2 * (bx + tg::norm_stage_bytes<TR, CH, VEC>(threads, cols));
+            const bool one_gate = q.n.rows_per_gate == a->rows;
+            const int gate = q.n.gate != nullptr ? bx : 0;
+            const int join = threads * CH * 32;  // a group's column sums
+            return threads <= tg::kNormThreads &&
+                   narrow(q.n.ldx, q.n.ldr, q.n.ldg, q.lddx, q.lddr) &&
+                   narrow(q.lddy, q.lddh, 0, 0, 0) &&
+                   plan_rows(a->rows, threads, stage + (one_gate ? 0 : gate),
+                             bx + (tg::kNormThreads / threads > 1 ? join : 0), 1, dev.num_sms, &r);
+        };
+        int ch = 0;  // columns of a thread / 8; 0: no ring fits
+        if (vec)
+            ch = plan(Int<1>{}, std::true_type{}) ? 1 : plan(Int<2>{}, std::true_type{}) ? 2 : 0;
+        else
+            ch = plan(Int<1>{}, std::false_type{}) ? 1 : plan(Int<2>{}, std::false_type{}) ? 2 : 0;
+        const int64_t most = ch != 0 ? dev.num_sms : 2 * dev.num_sms;
+        const int64_t wanted = ch != 0 ? (a->rows + r.groups - 1) / r.groups : a->rows;
+        const int64_t blocks = wanted < most ? wanted : most;
+        // Many gates: a block takes whole gates.  Few: it takes rows, and the
+        // blocks' shares of a gate are summed afterwards.
+        const bool gate_sums = q.dgate != nullptr && q.n.rows_per_gate > 1;
+        if (gate_sums && q.gates >= 2 * blocks) q.whole_gates = 1;
+        // (a thread of the row kernels sums its whole gates in registers)
+        const int64_t gate_slots = !gate_sums                ? 0
+                                   : !q.whole_gates ? blocks + q.gates
+                                   : ch != 0        ? 0
+                                                    : blocks;
+        const int64_t slots = (q.dwpost != nullptr ? blocks : 0) +
+                              (q.dwpre != nullptr ? blocks : 0) + gate_slots;
         if (slots > 0) {
-            const int64_t jobs = 2 + (q.whole_gates ? 0 : q.gates);
-            const dim3 grid(static_cast<unsigned>((cols + 31) / 32),
-                            static_cast<unsigned>(jobs < 1024 ? jobs : 1024));
-            tg::tg_norm_grad_sum<decltype(tx)><<<grid, 256, 0, s>>>(q, blocks);
+            void* ws = nullptr;
+            st = g_workspace.get(dev.dev, s, static_cast<size_t>(slots * cols) * 4, &ws);
+            if (st != TG_OK) return st;
+            float* next = static_cast<float*>(ws);
+            if (q.dwpost != nullptr) q.ws_post = next, next += blocks * cols;
+            if (q.dwpre != nullptr) q.ws_pre = next, next += blocks * cols;
+            if (gate_slots > 0) q.ws_gate = next;
         }
-        return launched();
+        const dim3 grid(static_cast<unsigned>(blocks));
+        if (ch != 0) {
+            auto run = [&](auto kernel) {
+                if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+                return launch(kernel, grid, r.threads * r.groups, r.smem, s, q, r.threads, r.stages,
+                              r.stage_bytes);
+            };
+            st = vec ? (ch == 1 ? run(tg::tg_norm_grad_rows<TX, TR, 1, true>)
+                                : run(tg::tg_norm_grad_rows<TX, TR, 2, true>))
+                     : (ch == 1 ? run(tg::tg_norm_grad_rows<TX, TR, 1, false>)
+                                : run(tg::tg_norm_grad_rows<TX, TR, 2, false>));
+        } else {
+            auto kernel = tg::tg_norm_grad_simple<TX, TR>;
+            const size_t smem = static_cast<size_t>(cols) * 4;
+            if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+            st = launch(kernel, grid, 256, smem, s, q);
+        }
+        if (st != TG_OK || slots == 0) return st;
+        const int64_t jobs = 2 + (q.whole_gates ? 0 : q.gates);
+        return launch(tg::tg_norm_grad_sum<TX>,
+                      dim3(static_cast<unsigned>((cols + 31) / 32),
+                           static_cast<unsigned>(jobs < 1024 ? jobs : 1024)),
+                      512, 0, s, q, blocks);
     });
 }
 
