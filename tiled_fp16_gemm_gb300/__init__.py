@@ -100,6 +100,7 @@ class tg_norm_grad_t(ctypes.Structure):
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _lib = None
+_DTYPES: dict = {}
 
 
 def _L():
@@ -519,17 +520,66 @@ def gemm_sp24(ac, e, b, relu: bool = False, out=None, stream=None, *, bias=None,
     return out
 
 
-def _on_stream(device, stream, used, body):
-    """``body(raw stream)`` with ``device`` current, its allocations made on the
-    stream that it launches on.  ``used``: the caller's tensors, kept from reuse
-    until that stream is done with them where it is not the current one."""
-    import torch
-    if stream is None:
-        if device.index == torch.cuda.current_device():
-            return body(torch.cuda.current_stream().cuda_stream)
-        with torch.cuda.device(device):
-            return body(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
+# The operators below are also called for single tokens, where this binding's own
+# time counts: each tensor is looked at once, with few attribute reads.
+
+_torch = None
+
+
+def _bind():
+    """torch, and what of it the operators call for every launch."""
+    global _torch, _DTYPES, _get_device, _raw_stream
+    if _torch is None:
+        import torch
+        _DTYPES = {torch.float16: TG_DTYPE_F16, torch.bfloat16: TG_DTYPE_BF16,
+                   torch.float32: TG_DTYPE_F32}
+        _get_device = torch.cuda.current_device
+        # the stream's handle without a Stream object around it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch = torch
+        _L()
+    return _torch
+
+
+def _matrix(t, name: str, dtype, rows: int, cols: int, index: int):
+    """(address, row stride) of a rows × cols tensor of ``dtype`` on device ``index``."""
+    try:
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.get_device() != index:
+            raise ValueError(f"{name} must be {rows}×{cols} on cuda:{index}")
+        stride = t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if stride[1] != 1 and cols > 1:
+        raise ValueError(f"{name} must be row-major (unit column stride)")
+    # a single row's stride is never used
+    return t.data_ptr(), stride[0] if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _vector(t, name: str, size: int, index: int) -> int:
+    """Address of a contiguous float32 vector of ``size`` elements."""
+    try:
+        shape = t.shape
+        if t.dtype is _torch.float32 and len(shape) == 1 and shape[0] == size \
+                and t.get_device() == index and (size < 2 or t.stride()[0] == 1):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {size} elements")
+
+
+def _on_stream(index: int, stream, used, body):
+    """``body(raw stream)`` where it is not just the current stream of the current
+    device: with device ``index`` current, and its allocations made on the stream
+    that it launches on.  ``used``: the caller's tensors, kept from reuse until that
+    stream is done with them where it is not the current one."""
+    torch = _torch
+    with torch.cuda.device(index):
+        if stream is None:
+            return body(_raw_stream(index))
         here = torch.cuda.current_stream()
         with torch.cuda.stream(stream):
             made = body(stream.cuda_stream)
@@ -541,24 +591,6 @@ def _on_stream(device, stream, used, body):
                 if t is not None:
                     t.record_stream(here)
     return made
-
-
-def _check_rows(t, name: str, rows: int, cols: int, dtype, device):
-    """A rows × cols tensor of ``dtype`` with unit column stride, on ``device``."""
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.device != device:
-        raise ValueError(f"{name} must be {rows}×{cols} on {device}")
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be row-major (unit column stride)")
-
-
-def _check_vector(t, name: str, size: int, device):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 1 \
-            or t.shape[0] != size or t.device != device or (size > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {size} elements")
 
 
 def gemm_w4(a, bq, bscale, N: int, group: int, relu: bool = False, out=None, stream=None, *,
@@ -574,106 +606,115 @@ def gemm_w4(a, bq, bscale, N: int, group: int, relu: bool = False, out=None, str
     (row stride a multiple of 16); without it every zero point is 8.  bias,
     residual, out_dtype, out and stream as for ``gemm``.
     """
-    import torch
-    _check_operand(a, "a")
-    M, K = a.shape
-    dtype, device = a.dtype, a.device
-    if not a.is_cuda:
+    torch = _torch or _bind()
+    try:
+        dtype = a.dtype
+        M, K = a.shape
+        index = a.get_device()
+    except (AttributeError, ValueError):
+        _check_operand(a, "a")
+        raise
+    if dtype is not torch.float16 and dtype is not torch.bfloat16 or index < 0:
+        _check_operand(a, "a")
         raise ValueError("a must be a CUDA tensor")
+    pa, lda = _matrix(a, "a", dtype, M, K, index)
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
     groups = (K + group - 1) // group
-    for t, name, kind, rows, width in ((bq, "bq", torch.uint8, N, (K + 1) // 2),
-                                       (bscale, "bscale", dtype, groups, N),
-                                       (bzero, "bzero", torch.uint8, groups, N)):
-        if t is None and name == "bzero":
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != kind or t.dim() != 2:
-            raise TypeError(f"{name} must be a 2-D {kind} tensor")
-        if t.shape[0] != rows or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+
+    def rows_of(t, name, kind, rows, width):  # rows of at least `width`
+        try:
+            if t.dtype is not kind:
+                raise TypeError(f"{name} must be a 2-D {kind} tensor, got {t.dtype}")
+            have = t.shape[-1]
+        except (AttributeError, IndexError):
+            raise TypeError(f"{name} must be a 2-D {kind} tensor") from None
+        if have < width:
             raise ValueError(f"{name} must be {rows} rows of at least {width}, row-major")
-        if t.device != device:
-            raise ValueError(f"{name} must be on a's device")
+        return _matrix(t, name, kind, rows, have, index)
+
+    pq, ldq = rows_of(bq, "bq", torch.uint8, N, (K + 1) // 2)
+    ps, lds = rows_of(bscale, "bscale", dtype, groups, N)
+    pz, ldz = rows_of(bzero, "bzero", torch.uint8, groups, N) if bzero is not None else (None, 0)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else dtype
-    if out_dtype not in (dtype, torch.float32):
+    if out_dtype is not dtype and out_dtype is not torch.float32:
         raise TypeError(f"out_dtype must be {dtype} or torch.float32, got {out_dtype}")
     if out is not None:
-        _check_rows(out, "out", M, N, out_dtype, device)
-    if bias is not None:
-        _check_vector(bias, "bias", N, device)
-    if residual is not None:
-        _check_rows(residual, "residual", M, N, dtype, device)
-    code = TG_DTYPE_BF16 if dtype == torch.bfloat16 else TG_DTYPE_F16
-
-    def up16(t):  # the row stride; a single row's is never used
-        return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
-
-    def body(s):
-        c = torch.empty((M, N), dtype=out_dtype, device=device) if out is None else out
-        epi = tg_epilogue_ex_t(
-            TG_EPI_RELU if relu else TG_EPI_NONE,
-            TG_DTYPE_F32 if out_dtype == torch.float32 else code,
-            bias.data_ptr() if bias is not None else None,
-            residual.data_ptr() if residual is not None else None,
-            _ld(residual) if residual is not None else 0)
-        st = _L().tg_gemm_w4(
-            code, a.data_ptr(), bq.data_ptr(), bscale.data_ptr(),
-            bzero.data_ptr() if bzero is not None else None, c.data_ptr(), M, N, K, group,
-            _ld(a), up16(bq), up16(bscale), up16(bzero) if bzero is not None else 0, _ld(c),
-            ctypes.byref(epi), s)
+        pc, ldc = _matrix(out, "out", out_dtype, M, N, index)
+    pb = _vector(bias, "bias", N, index) if bias is not None else None
+    pr, ldr = _matrix(residual, "residual", dtype, M, N, index) if residual is not None else (None, 0)
+    code = _DTYPES[dtype]
+    epi = tg_epilogue_ex_t(1 if relu else 0, _DTYPES[out_dtype], pb, pr, ldr)
+    if out is None and stream is None and index == _get_device():
+        c = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        st = _lib.tg_gemm_w4(code, pa, pq, ps, pz, c.data_ptr(), M, N, K, group, lda, ldq, lds, ldz,
+                             N, ctypes.byref(epi), _raw_stream(index))
         if st != TG_OK:
             raise TgemmError(st, "tg_gemm_w4")
         return c
 
-    return _on_stream(device, stream, (a, bq, bscale, bzero, bias, residual, out), body)
+    def body(s):
+        c = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
+        st = _lib.tg_gemm_w4(code, pa, pq, ps, pz, c.data_ptr(), M, N, K, group, lda, ldq, lds, ldz,
+                             N if out is None else ldc, ctypes.byref(epi), s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_gemm_w4")
+        return c
+
+    return _on_stream(index, stream, (a, bq, bscale, bzero, bias, residual, out), body)
 
 
 def _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps):
     """Checks and packs what the norms and their gradient share."""
-    import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    codes = {torch.float16: TG_DTYPE_F16, torch.bfloat16: TG_DTYPE_BF16,
-             torch.float32: TG_DTYPE_F32}
-    if x.dtype not in codes:
-        raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
-    if x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x must be a 2-D row-major CUDA tensor (unit column stride)")
-    rows, cols = x.shape
-    device = x.device
+    torch = _torch or _bind()
+    try:
+        dtype = x.dtype
+        rows, cols = x.shape
+        index = x.get_device()
+    except AttributeError:
+        raise TypeError("x must be a torch.Tensor") from None
+    except ValueError:
+        raise ValueError("x must be 2-D") from None
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
+    if index < 0:
+        raise ValueError("x must be a CUDA tensor")
     if cols > 32768:
         raise ValueError(f"x must have at most 32768 columns, got {cols}")
-    kind = x.dtype
+    px, ldx = _matrix(x, "x", dtype, rows, cols, index)
+    kind, kind_code, pr, ldr = dtype, code, None, 0
     if residual is not None:
-        kind = residual.dtype if isinstance(residual, torch.Tensor) else None
-        if kind not in (x.dtype, torch.float32):
-            raise TypeError(f"residual must be a {x.dtype} or float32 tensor")
-        _check_rows(residual, "residual", rows, cols, kind, device)
-    if post_weight is not None:
-        _check_vector(post_weight, "post_weight", cols, device)
-    if pre_weight is not None:
-        _check_vector(pre_weight, "pre_weight", cols, device)
-    gate_rows, ldg = 0, 0
+        kind = getattr(residual, "dtype", None)
+        if kind is not dtype:
+            if kind is not torch.float32:
+                raise TypeError(f"residual must be a {dtype} or float32 tensor")
+            kind_code = TG_DTYPE_F32
+        pr, ldr = _matrix(residual, "residual", kind, rows, cols, index)
+    pg, ldg, gate_rows = None, 0, 0
     if gate is not None:
-        if not isinstance(gate, torch.Tensor) or gate.dtype != x.dtype:
-            raise TypeError(f"gate must be a {x.dtype} tensor")
-        gate_rows = gate.shape[0] if gate.dim() == 2 else 1
-        if gate.dim() not in (1, 2) or gate.shape[-1] != cols or gate.device != device \
-                or (cols > 1 and gate.stride(-1) != 1):
-            raise ValueError(f"gate must be {cols} values, or rows of {cols}, on x's device")
+        try:
+            shape = gate.shape
+        except AttributeError:
+            raise TypeError(f"gate must be a {dtype} tensor") from None
+        if len(shape) == 1:
+            gate_rows = 1
+            pg, ldg = _matrix(gate.unsqueeze(0), "gate", dtype, 1, cols, index)
+        else:
+            gate_rows = shape[0]
+            pg, ldg = _matrix(gate, "gate", dtype, gate_rows, cols, index)
         if gate_rows < 1 or (rows > 0 and (gate_rows > rows or rows % gate_rows)):
             raise ValueError(f"the gate's {gate_rows} rows must divide x's {rows}")
-        ldg = _ld(gate) if gate.dim() == 2 else cols
     if not eps >= 0:
         raise ValueError(f"eps must not be negative, got {eps}")
-    n = tg_norm_t(codes[x.dtype], codes[kind], rows, cols, x.data_ptr(), _ld(x),
-                  residual.data_ptr() if residual is not None else None,
-                  _ld(residual) if residual is not None else 0,
-                  post_weight.data_ptr() if post_weight is not None else None,
-                  gate.data_ptr() if gate is not None else None, ldg, gate_rows,
-                  pre_weight.data_ptr() if pre_weight is not None else None, scale, eps)
-    return n, rows, cols, kind
+    n = tg_norm_t(
+        code, kind_code, rows, cols, px, ldx, pr, ldr,
+        _vector(post_weight, "post_weight", cols, index) if post_weight is not None else None,
+        pg, ldg, gate_rows,
+        _vector(pre_weight, "pre_weight", cols, index) if pre_weight is not None else None,
+        scale, eps)
+    return n, rows, cols, dtype, kind, index
 
 
 def norm_residual(x, residual=None, *, post_weight=None, gate=None, scale: float = 1.0,
@@ -693,30 +734,39 @@ def norm_residual(x, residual=None, *, post_weight=None, gate=None, scale: float
     be ``residual`` itself) and h to ``normed`` where given.  Runs on ``stream``
     (default: torch's current stream of x's device).
     """
-    import torch
-    n, rows, cols, kind = _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps)
-    device = x.device
+    n, rows, cols, dtype, kind, index = _norm_args(x, residual, post_weight, gate, scale,
+                                                   pre_weight, eps)
+    torch = _torch
+    py = ph = None
     if out is not None:
-        _check_rows(out, "out", rows, cols, kind, device)
+        py, ldy = _matrix(out, "out", kind, rows, cols, index)
     if normed is not None:
         if pre_weight is None:
             raise ValueError("normed needs pre_weight")
-        _check_rows(normed, "normed", rows, cols, x.dtype, device)
+        ph, ldh = _matrix(normed, "normed", dtype, rows, cols, index)
 
     def body(s):
-        y = torch.empty((rows, cols), dtype=kind, device=device) if out is None else out
-        h = normed
-        if h is None and pre_weight is not None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=device)
-        st = _L().tg_norm_residual(
-            ctypes.byref(n), y.data_ptr(), _ld(y), h.data_ptr() if h is not None else None,
-            _ld(h) if h is not None else 0, s)
+        shape, device = (rows, cols), x.device
+        y, h = out, normed
+        y_at, y_ld, h_at, h_ld = py, cols, ph, cols
+        if y is None:
+            y = torch.empty(shape, dtype=kind, device=device)
+            y_at = y.data_ptr()
+        else:
+            y_ld = ldy
+        if h is not None:
+            h_ld = ldh
+        elif pre_weight is not None:
+            h = torch.empty(shape, dtype=dtype, device=device)
+            h_at = h.data_ptr()
+        st = _lib.tg_norm_residual(ctypes.byref(n), y_at, y_ld, h_at, h_ld, s)
         if st != TG_OK:
             raise TgemmError(st, "tg_norm_residual")
         return y, h
 
-    return _on_stream(device, stream, (x, residual, post_weight, gate, pre_weight, out, normed),
-                      body)
+    if stream is None and index == _get_device():
+        return body(_raw_stream(index))
+    return _on_stream(index, stream, (x, residual, post_weight, gate, pre_weight, out, normed), body)
 
 
 class NormGrads(NamedTuple):
@@ -737,35 +787,42 @@ def norm_residual_backward(dy, dh, x, residual=None, *, post_weight=None, gate=N
     input's dtype and shape.  x and residual are those of the forward call: no
     ``out`` may have been written over them.
     """
-    import torch
-    n, rows, cols, kind = _norm_args(x, residual, post_weight, gate, scale, pre_weight, eps)
-    device = x.device
-    if dy is not None:
-        _check_rows(dy, "dy", rows, cols, kind, device)
+    n, rows, cols, dtype, kind, index = _norm_args(x, residual, post_weight, gate, scale,
+                                                   pre_weight, eps)
+    torch = _torch
+    pdy, lddy = _matrix(dy, "dy", kind, rows, cols, index) if dy is not None else (None, 0)
+    pdh, lddh = None, 0
     if dh is not None:
         if pre_weight is None:
             raise ValueError("dh needs pre_weight")
-        _check_rows(dh, "dh", rows, cols, x.dtype, device)
+        pdh, lddh = _matrix(dh, "dh", dtype, rows, cols, index)
 
     def body(s):
-        def like(t):
-            return torch.empty(t.shape, dtype=t.dtype, device=device) if t is not None else None
-
-        def at(t):
-            return t.data_ptr() if t is not None else None
-
-        grads = NormGrads(like(x), like(residual), like(gate), like(post_weight),
-                          like(pre_weight))
-        g = tg_norm_grad_t(at(dy), _ld(dy) if dy is not None else 0,
-                           at(dh), _ld(dh) if dh is not None else 0,
-                           at(grads.x), cols, at(grads.residual), cols, at(grads.gate), cols,
-                           at(grads.post_weight), at(grads.pre_weight))
-        st = _L().tg_norm_residual_backward(ctypes.byref(n), ctypes.byref(g), s)
+        empty, shape, device = torch.empty, (rows, cols), x.device
+        dx = empty(shape, dtype=dtype, device=device)
+        dr = dg = dpost = dpre = at_r = at_g = at_post = at_pre = None
+        if residual is not None:
+            dr = empty(shape, dtype=kind, device=device)
+            at_r = dr.data_ptr()
+        if gate is not None:
+            dg = empty(gate.shape, dtype=dtype, device=device)
+            at_g = dg.data_ptr()
+        if post_weight is not None:
+            dpost = empty(cols, dtype=torch.float32, device=device)
+            at_post = dpost.data_ptr()
+        if pre_weight is not None:
+            dpre = empty(cols, dtype=torch.float32, device=device)
+            at_pre = dpre.data_ptr()
+        g = tg_norm_grad_t(pdy, lddy, pdh, lddh, dx.data_ptr(), cols, at_r, cols, at_g, cols,
+                           at_post, at_pre)
+        st = _lib.tg_norm_residual_backward(ctypes.byref(n), ctypes.byref(g), s)
         if st != TG_OK:
             raise TgemmError(st, "tg_norm_residual_backward")
-        return grads
+        return NormGrads(dx, dr, dg, dpost, dpre)
 
-    return _on_stream(device, stream, (dy, dh, x, residual, post_weight, gate, pre_weight), body)
+    if stream is None and index == _get_device():
+        return body(_raw_stream(index))
+    return _on_stream(index, stream, (dy, dh, x, residual, post_weight, gate, pre_weight), body)
 
 
 def gemm_host(a, b, relu: bool = False, stream=None, device=None):

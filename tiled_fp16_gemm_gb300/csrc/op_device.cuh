@@ -1,6 +1,7 @@
 // Device helpers of the operators beside the GEMM (gemm_w4.cuh, norm.cuh).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,6 +37,57 @@ __device__ __forceinline__ void op_wait_previous() {
 }
 __device__ __forceinline__ void op_release_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ mbarriers and TMA
+
+__device__ __forceinline__ uint32_t op_smem(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void op_bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void op_bar_init_done() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void op_bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t op_bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok;
+}
+// Until the phase of `bar` with this parity is over, or `limit_ns` have passed: false.
+static __device__ __noinline__ bool op_bar_wait_slow(uint32_t bar, uint32_t parity,
+                                                     uint64_t limit_ns) {
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (op_bar_try(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 <= limit_ns);
+    return false;
+}
+__device__ __forceinline__ bool op_bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return op_bar_try(bar, parity) || op_bar_wait_slow(bar, parity, limit_ns);
+}
+
+// A box of a 2-D tensor map to shared memory; x is the contiguous coordinate.
+__device__ __forceinline__ void op_tma_2d(uint32_t dst, const void* map, uint32_t bar, uint32_t x,
+                                          uint32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
 }  // namespace tg

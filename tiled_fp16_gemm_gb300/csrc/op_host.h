@@ -2,6 +2,8 @@
 // they run on, and workspaces that belong to a stream.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -47,6 +49,37 @@ inline tg_status_t op_device(OpDevice* out) {
     out->dev = d;
     out->num_sms = sms[d];
     return TG_OK;
+}
+
+// Limit of every wait in a kernel (tg_debug_set_wait_timeout_ns), in tgemm.cu.
+uint64_t op_wait_limit_ns();
+
+// Whether a kernel of w4.cu gave up on a wait since the last call, on the current
+// device, which has to be idle.
+bool w4_take_timeout();
+
+// The 2-D tensor map of rows of `inner` elements, `row_bytes` apart, read in boxes of
+// box_inner × box_outer; zero outside.
+inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType type, uint64_t inner,
+                      uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                      CUtensorMapSwizzle swizzle) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }();
+    if (encode == nullptr) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_inner, box_outer};
+    cuuint32_t steps[2] = {1, 1};
+    return encode(map, type, 2, const_cast<void*>(ptr), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Device memory per (device, stream), grown on demand.  A buffer that became

@@ -20,6 +20,7 @@
 #include "gemm_sparse_pair.cuh"
 #include "gemm_skinny.cuh"
 #include "gemm_sparse.cuh"
+#include "op_host.h"
 #include "sparse_plan.h"
 #include "tile_schedule.h"
 
@@ -997,6 +998,8 @@ tg_status_t plan_limited(int64_t M, int64_t N, int64_t K, const PlanLimits& lim,
 
 }  // namespace
 
+uint64_t tg::op_wait_limit_ns() { return g_timeout_ns.load(); }
+
 // ====================================================================== C ABI
 
 extern "C" {
@@ -1292,9 +1295,10 @@ tg_status_t tg_sync_status(void* stream) {
         tg::splitk_reset_counters(dev);
         noalloc_reset_counters(dev);
         cudaGetLastError();
+        tg::w4_take_timeout();
         return TG_ERR_TIMEOUT;
     }
-    return TG_OK;
+    return tg::w4_take_timeout() ? TG_ERR_TIMEOUT : TG_OK;
 }
 
 }  // extern "C"

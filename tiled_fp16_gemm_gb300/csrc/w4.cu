@@ -33,16 +33,194 @@ tg_status_t launch_dense(int32_t in_dtype, const W4Params& p, const tg_epilogue_
     return tg_gemm_ex(in_dtype, p.A, ws, p.C, p.M, p.N, p.K, p.lda, ldo, p.ldc, &x, s);
 }
 
+// One launch with dependent launch allowed, in clusters of `cluster` blocks.
+template <typename... Args, typename... Given>
+tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
+                   cudaStream_t s, Given... given) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    return TG_OK;
+}
+
+constexpr int kSmem = 226 * 1024;
+
+// Shared memory of a block, or more than there is.
+template <int G, int NT>
+int64_t w4_smem_bytes(tg::W4Launch* q) {
+    using Step = tg::W4Step<G>;
+    const int64_t slice = (q->steps + q->cluster - 1) / q->cluster + 1;  // k steps of a block
+    const int64_t x = (slice * tg::kW4K * q->tokens * 2 + 511) / 512 * 512;
+    const int64_t join = q->wk > 1 ? int64_t{q->wn} * (q->wk - 1) * 1024 * NT : 0;
+    const int64_t res = q->cluster > 1 ? int64_t{q->rounds} * q->wn * q->tokens * tg::kW4Rows * 4 : 0;
+    for (q->stages = 4; q->stages >= 2; --q->stages) {
+        const int64_t all = tg::kW4Warps * 32 + x + tg::kW4Warps * q->stages * int64_t{Step::kBytes} + join + res;
+        if (all <= kSmem) {
+            q->x_bytes = static_cast<int32_t>(x);
+            q->join_bytes = static_cast<int32_t>(join);
+            return all;
+        }
+    }
+    return kSmem + 1;
+}
+
+// Clusters of `size` blocks that the device holds at once.
+template <typename Kernel>
+int max_clusters(Kernel kernel, int size, const tg::OpDevice& dev) {
+    if (size == 1) return dev.num_sms;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(size);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
+    cfg.blockDim = dim3(tg::kW4Threads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+// NT: tokens / 8.
+template <typename T, int G, int NT, bool ZERO>
+tg_status_t launch_tiles(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    auto kernel = tg::tg_gemm_w4<T, G, NT, ZERO>;
+    struct Limits {
+        std::once_flag once;
+        bool ok = false;
+        int clusters[4] = {};  // of 1, 2, 4, 8 blocks
+    };
+    static Limits limits[tg::kOpMaxDevices];
+    Limits& lim = limits[dev.dev];
+    std::call_once(lim.once, [&] {
+        lim.ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
+                 cudaSuccess;
+        for (int i = 0; i < 4; ++i) lim.clusters[i] = max_clusters(kernel, 1 << i, dev);
+        cudaGetLastError();
+    });
+    if (!lim.ok) return TG_ERR_LAUNCH;
+
+    tg::W4Launch q, best;
+    std::memset(&q, 0, sizeof(q));
+    q.p = p;
+    q.tokens = static_cast<int32_t>(p.M < 8 * NT ? p.M : 8 * NT);
+    int64_t by_m = (p.M + q.tokens - 1) / q.tokens;
+    q.steps = static_cast<int32_t>((p.K + tg::kW4K - 1) / tg::kW4K);
+    q.tiles = static_cast<int32_t>((p.N + tg::kW4Rows - 1) / tg::kW4Rows);
+    // The shape with the least time, in steps of a warp: a block takes rounds of
+    // tiles; a round costs its steps and a join, a block the fetch of A and, with a
+    // cluster, the last join.
+    double least = 1e300;
+    int64_t smem = 0;
+    for (; q.tokens >= 1 && least > 1e299; q.tokens /= 2) {  // k too long for so many tokens: fewer
+        by_m = (p.M + q.tokens - 1) / q.tokens;
+        for (int i = 0; i < 4; ++i) {
+            q.cluster = 1 << i;
+            if (q.cluster > q.steps) break;
+            if (lim.clusters[i] < 1) continue;
+            for (q.wk = 1; q.wk <= 16; q.wk *= 2) {
+                q.wn = tg::kW4Warps / q.wk;
+                const int64_t jobs = (q.tiles + q.wn - 1) / q.wn;
+                int64_t clusters = lim.clusters[i];
+                if (clusters > jobs) clusters = jobs;
+                q.rounds = static_cast<int32_t>((jobs + clusters - 1) / clusters);
+                q.clusters = static_cast<int32_t>((jobs + q.rounds - 1) / q.rounds);
+                const int64_t bytes = w4_smem_bytes<G, NT>(&q);
+                if (bytes > kSmem) continue;
+                const int64_t slice = (q.steps + q.cluster - 1) / q.cluster;
+                const int64_t each = (slice + q.wk - 1) / q.wk;
+                const double waves = static_cast<double>(
+                    (q.clusters * by_m + lim.clusters[i] - 1) / lim.clusters[i]);
+                const double time =
+                    waves * (q.rounds * (each + (q.wk > 1 ? 0.5 + 0.1 * q.wk * NT : 0.3)) +
+                             0.01 * slice * q.tokens + (q.cluster > 1 ? 3.0 : 0.0) +
+                             (q.stages < 4 ? 2.0 * (4 - q.stages) : 0.0));
+                if (time < least) least = time, best = q, smem = bytes;
+            }
+        }
+    }
+    if (least > 1e299) {
+        const int64_t blocks = ((p.M + 7) / 8 * p.N + 7) / 8;
+        const int64_t most = 8 * dev.num_sms;
+        return launch(tg::tg_gemm_w4_simple<T>,
+                      dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, 1, s, p);
+    }
+    by_m = (p.M + best.tokens - 1) / best.tokens;
+    best.limit_ns = tg::op_wait_limit_ns();
+    using Step = tg::W4Step<G>;
+    constexpr CUtensorMapDataType type =
+        std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t groups = (p.K + G - 1) / G;
+    CUtensorMap codes, scales, zeros;
+    if (!tg::op_map_2d(&codes, p.Bq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (p.K + 1) / 2, p.N, p.ldbq,
+                       tg::kW4K / 2, tg::kW4Rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !tg::op_map_2d(&scales, p.scale, type, p.N, groups, p.lds * 2, tg::kW4Rows, Step::kGroups,
+                       CU_TENSOR_MAP_SWIZZLE_NONE))
+        return TG_ERR_LAUNCH;
+    zeros = scales;
+    if (ZERO && !tg::op_map_2d(&zeros, p.zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.N, groups, p.ldz,
+                               tg::kW4Rows, Step::kGroups, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return TG_ERR_LAUNCH;
+    return launch(kernel,
+                  dim3(static_cast<unsigned>(best.clusters * best.cluster), static_cast<unsigned>(by_m)),
+                  tg::kW4Threads, static_cast<size_t>(smem), best.cluster, s, best, codes, scales, zeros);
+}
+
+template <typename T, int G, bool ZERO>
+tg_status_t launch_group(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    if (p.M <= 8) return launch_tiles<T, G, 1, ZERO>(p, dev, s);
+    return launch_tiles<T, G, 2, ZERO>(p, dev, s);
+}
+
+template <typename T, int G>
+tg_status_t launch_zero(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    return p.zero != nullptr ? launch_group<T, G, true>(p, dev, s)
+                             : launch_group<T, G, false>(p, dev, s);
+}
+
 template <typename T>
 tg_status_t launch_rows(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
-    const int64_t jobs = (p.M + 7) / 8 * p.N;
-    const int64_t blocks = (jobs + 7) / 8;
-    const int64_t grid = blocks < 8 * dev.num_sms ? blocks : 8 * dev.num_sms;
-    tg::tg_gemm_w4_simple<T><<<static_cast<unsigned>(grid), 256, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? TG_OK : TG_ERR_LAUNCH;
+    if (p.group == 32) return launch_zero<T, 32>(p, dev, s);
+    if (p.group == 64) return launch_zero<T, 64>(p, dev, s);
+    return launch_zero<T, 128>(p, dev, s);
 }
 
 }  // namespace
+
+bool tg::w4_take_timeout() {
+    unsigned int n = 0;
+    if (cudaMemcpyFromSymbol(&n, tg::g_w4_timeouts, sizeof(n)) != cudaSuccess || n == 0) {
+        cudaGetLastError();
+        return false;
+    }
+    n = 0;
+    cudaMemcpyToSymbol(tg::g_w4_timeouts, &n, sizeof(n));
+    cudaGetLastError();
+    return true;
+}
 
 extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* Bq,
                                   const void* Bscale, const void* Bzero, void* C, int64_t M,
