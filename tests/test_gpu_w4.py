@@ -96,6 +96,46 @@ def test_layer_sizes(tg, M, N, K):
     check(tg, M, N, K, BF16, 128, True)
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 2311, 2305), (33, 5003, 3001), (17, 3001, 4099), (48, 129, 60000),
+                                   (9, 9001, 4111), (16, 20000, 2048), (64, 40000, 136), (40, 4096, 1280)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_batches_of_odd_sizes(tg, M, N, K, group):
+    """Row blocks shared by several blocks, ends inside units, groups and bytes."""
+    check(tg, M, N, K, HALF, group, True, bias=True, pad=1)
+    check(tg, M, N, K, BF16, group, False, residual=True, out_dtype=torch.float32, seed=1)
+
+
+def test_batches_of_changing_shapes(tg):
+    """One stream's workspace serves every shape: what one call leaves there does not
+    show in the next."""
+    for M, N, K in ((64, 2304, 2304), (64, 16384, 1024), (9, 8192, 8192), (64, 2304, 2304),
+                    (33, 128, 50000), (64, 16384, 1024)):
+        check(tg, M, N, K, HALF, 64, True)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (8, 1000, 4096), (40, 4096, 4096)])
+def test_a_wait_that_runs_out_is_reported_once(tg, M, N, K):
+    """A fetch that is left out: the kernel gives up within its limit and returns, the
+    status says so once, and the next call is right."""
+    a, bq, bscale, bzero = make(M, N, K, HALF, 64, True)
+    want = tg.gemm_w4(a, bq, bscale, N, 64, bzero=bzero)
+    tg.sync_status()
+    try:
+        tg.tg_debug_set_wait_timeout_ns(20_000_000)
+        tg.tg_debug_inject(1)
+        tg.gemm_w4(a, bq, bscale, N, 64, bzero=bzero)
+        with pytest.raises(tg.TgemmError) as e:
+            tg.sync_status()
+        assert e.value.status == tg.TG_ERR_TIMEOUT
+        tg.sync_status()
+    finally:
+        tg.tg_debug_inject(0)
+        tg.tg_debug_set_wait_timeout_ns(0)
+    for _ in range(2):
+        assert torch.equal(tg.gemm_w4(a, bq, bscale, N, 64, bzero=bzero), want)
+    tg.sync_status()
+
+
 def test_exact_on_small_integers(tg):
     """Scales of 1 and small integers: every sum is an integer below 2^24, exact in
     fp32 in any order, so the result is exact."""

@@ -89,9 +89,13 @@ struct W4Step {
 // Warps that gave up on a wait.
 static __device__ unsigned int g_w4_timeouts;
 
+// What copies under way get to land before a block that gave up on them ends.
+constexpr uint64_t kW4LandNs = 1000000000ull;
+
 struct W4Launch {
     W4Params p;
     uint64_t limit_ns;
+    int32_t inject;    // 1: block 0's first fetch is left out (for tests of the limit)
     int32_t wn, wk;    // tiles of a block at a time, k-pieces
     int32_t tokens;    // rows of A per block
     int32_t steps;     // k steps in all
@@ -237,12 +241,12 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
         if (lane == 0) {
             const uint32_t step = s0 + wk + f_step * q.wk;
             const uint32_t to = ring + f_slot * Step::kBytes, bar = bars + 8 * f_slot;
-            op_bar_expect(bar, kW4StepCodes + Step::kScaleBytes + (ZERO ? Step::kZeroBytes : 0));
-            op_tma_2d(to, &codes, bar, step * (kW4K / 2), f_n);
-            op_tma_2d(to + kW4StepCodes, &scales, bar, f_n, step * Step::kGroups);
-            if (ZERO)
-                op_tma_2d(to + Step::kZeroAt, &zeros, bar, f_n,
-                          step * Step::kGroups);
+            if (!(q.inject == 1 && blockIdx.x == 0 && f_round == 0 && f_step == 0)) {
+                op_bar_expect(bar, kW4StepCodes + Step::kScaleBytes + (ZERO ? Step::kZeroBytes : 0));
+                op_tma_2d(to, &codes, bar, step * (kW4K / 2), f_n);
+                op_tma_2d(to + kW4StepCodes, &scales, bar, f_n, step * Step::kGroups);
+                if (ZERO) op_tma_2d(to + Step::kZeroAt, &zeros, bar, f_n, step * Step::kGroups);
+            }
         }
         f_slot = f_slot + 1 == q.stages ? 0 : f_slot + 1;
         if (++f_step == mine) {
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
     float* results = pieces + q.join_bytes / 4;
     int slot = 0;
     uint32_t parity = 0;
-    bool given_up = false;
+    bool given_up = false, lost = false;
     for (int round = 0; round < q.rounds; ++round) {
         const int64_t n0 = ((int64_t{round} * q.clusters + cluster_no) * q.wn + wn) * kW4Rows;
         float sum[2][NT][4];
@@ -313,9 +317,13 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
         uint32_t x_at = wk * 4 * x_pitch;
         if (n0 < p.N) {
             for (int i = 0; i < mine; ++i) {
-                if (!given_up) given_up = !op_bar_wait(bars + 8 * slot, parity, q.limit_ns);
-                __syncwarp();  // all lanes have read the slot before
-                fetch();
+                if (!lost && !op_bar_wait(bars + 8 * slot, parity, q.limit_ns)) {
+                    // reported; nothing more is fetched once copies do not come at all
+                    given_up = true;
+                    lost = !op_bar_wait(bars + 8 * slot, parity, kW4LandNs);
+                }
+                lost = __any_sync(0xffffffffu, lost);  // (and all lanes have read the slot before)
+                if (!lost) fetch();
                 const uint32_t at = ring + slot * Step::kBytes;
                 const uint32_t wl = at + w_lane;
                 const unsigned char* tail = w4_shared + (at - op_smem(w4_shared)) + kW4StepCodes;

@@ -66,13 +66,17 @@ __device__ __forceinline__ uint32_t op_bar_try(uint32_t bar, uint32_t parity) {
     return ok;
 }
 // Until the phase of `bar` with this parity is over, or `limit_ns` have passed: false.
+// The clock is read only now and then, and no sleep time is asked for: a sleeping warp
+// woke up late, and the roles of a block wait for one another all the time.
 static __device__ __noinline__ bool op_bar_wait_slow(uint32_t bar, uint32_t parity,
                                                      uint64_t limit_ns) {
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    uint64_t t0 = 0, t = 0;
     do {
-        if (op_bar_try(bar, parity)) return true;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (op_bar_try(bar, parity)) return true;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (t0 == 0) t0 = t;
     } while (t - t0 <= limit_ns);
     return false;
 }

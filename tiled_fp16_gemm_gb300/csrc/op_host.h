@@ -54,6 +54,9 @@ inline tg_status_t op_device(OpDevice* out) {
 // Limit of every wait in a kernel (tg_debug_set_wait_timeout_ns), in tgemm.cu.
 uint64_t op_wait_limit_ns();
 
+// The mode that tg_debug_inject set for the next launch, which is then 0 again.
+int32_t op_take_inject();
+
 // Whether a kernel of w4.cu gave up on a wait since the last call, on the current
 // device, which has to be idle.
 bool w4_take_timeout();
@@ -90,7 +93,9 @@ inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType typ
 // anything is enqueued, and the capture stays valid.
 class OpWorkspace {
   public:
-    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out) {
+    // `fresh` (if given): whether this is the buffer's first use since `epoch` changed.
+    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, bool* fresh = nullptr,
+                    uint64_t epoch = 0) {
         // the per-thread default stream is one handle for a stream per thread
         const size_t thread =
             s == cudaStreamPerThread ? std::hash<std::thread::id>{}(std::this_thread::get_id()) : 0;
@@ -115,7 +120,11 @@ class OpWorkspace {
             }
             b.p = p;
             b.bytes = want;
+            b.used = false;
         }
+        if (fresh != nullptr) *fresh = !b.used || b.epoch != epoch;
+        b.used = true;
+        b.epoch = epoch;
         *out = b.p;
         return TG_OK;
     }
@@ -124,6 +133,8 @@ class OpWorkspace {
     struct Buffer {
         void* p = nullptr;
         size_t bytes = 0;
+        bool used = false;
+        uint64_t epoch = 0;
     };
     std::mutex m_;
     std::map<std::tuple<int, cudaStream_t, size_t>, Buffer> of_;

@@ -999,6 +999,7 @@ tg_status_t plan_limited(int64_t M, int64_t N, int64_t K, const PlanLimits& lim,
 }  // namespace
 
 uint64_t tg::op_wait_limit_ns() { return g_timeout_ns.load(); }
+int32_t tg::op_take_inject() { return g_inject.exchange(0); }
 
 // ====================================================================== C ABI
 

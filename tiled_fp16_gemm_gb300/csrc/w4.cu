@@ -1,8 +1,12 @@
 // tg_gemm_w4 (include/tgemm.h): argument checks and launches.  The kernels
 // and the formulas: gemm_w4.cuh.
 #include <cstring>
+#include <set>
+
+#include <atomic>
 
 #include "gemm_w4.cuh"
+#include "gemm_w4_tc.cuh"
 #include "op_host.h"
 
 namespace {
@@ -10,6 +14,8 @@ namespace {
 using tg::W4Params;
 
 tg::OpWorkspace g_workspace;  // 16-bit weights of the dense path
+tg::OpWorkspace g_tc;         // of tg_gemm_w4_tc: counters, sums of shares, A in order
+std::atomic<uint64_t> g_timeouts{0};  // how often a wait ran out: counters are then cleared
 
 bool misaligned(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
@@ -170,6 +176,7 @@ tg_status_t launch_tiles(const W4Params& p, const tg::OpDevice& dev, cudaStream_
     }
     by_m = (p.M + best.tokens - 1) / best.tokens;
     best.limit_ns = tg::op_wait_limit_ns();
+    best.inject = tg::op_take_inject();
     using Step = tg::W4Step<G>;
     constexpr CUtensorMapDataType type =
         std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -189,8 +196,92 @@ tg_status_t launch_tiles(const W4Params& p, const tg::OpDevice& dev, cudaStream_
                   tg::kW4Threads, static_cast<size_t>(smem), best.cluster, s, best, codes, scales, zeros);
 }
 
+// Opts a kernel into its shared memory, once per device.
+template <typename Kernel>
+bool allow_smem(Kernel kernel, int bytes, int dev) {
+    static std::mutex m;
+    static std::set<std::pair<const void*, int>> done;
+    const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
+    std::lock_guard<std::mutex> lk(m);
+    if (done.count(key) != 0) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    done.insert(key);
+    return true;
+}
+
+// Up to 64 rows of A, on tcgen05.
+template <typename T, int G, int NP, bool ZERO>
+tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    using S = tg::TcShape<G, NP>;
+    auto kernel = tg::tg_gemm_w4_tc<T, G, NP, ZERO>;
+    if (!allow_smem(kernel, S::kSmem, dev.dev)) return TG_ERR_LAUNCH;
+    tg::TcLaunch q;
+    q.p = p;
+    q.limit_ns = tg::op_wait_limit_ns();
+    q.inject = 0;
+    q.k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
+    q.units = (p.N + tg::kTcRows - 1) / tg::kTcRows * q.k_units;
+    const int64_t blocks = q.units < dev.num_sms ? q.units : dev.num_sms;
+    // the counters' place is the same for every shape: each launch leaves them at zero
+    // for the stream's next one
+    constexpr int64_t counter_bytes = 64 * 1024;
+    if (blocks * 32 > counter_bytes) return TG_ERR_UNSUPPORTED_DEVICE;
+    const int64_t slot_bytes = 2 * blocks * NP * tg::kTcRows * 4;
+    const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
+    void* ws = nullptr;
+    bool fresh = false;
+    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
+                              &ws, &fresh, g_timeouts.load());
+    if (st != TG_OK) return st;
+    if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    q.counters = static_cast<uint32_t*>(ws);
+    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + counter_bytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + counter_bytes + slot_bytes);
+    constexpr CUtensorMapDataType type =
+        std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t groups = (p.K + G - 1) / G;
+    CUtensorMap codes, scales, zeros, ordered;
+    if (!tg::op_map_2d(&codes, p.Bq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (p.K + 1) / 2, p.N, p.ldbq,
+                       tg::kTcK / 2, tg::kTcRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !tg::op_map_2d(&scales, p.scale, type, p.N, groups, p.lds * 2, tg::kTcRows, S::kGroups,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !tg::op_map_2d(&ordered, order, type, ldo, p.M, ldo * 2, 64, NP, CU_TENSOR_MAP_SWIZZLE_128B))
+        return TG_ERR_LAUNCH;
+    zeros = scales;
+    if (ZERO && !tg::op_map_2d(&zeros, p.zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.N, groups, p.ldz,
+                               tg::kTcRows, S::kGroups, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return TG_ERR_LAUNCH;
+    q.inject = tg::op_take_inject();
+    st = launch(tg::tg_w4_order,
+                dim3(static_cast<unsigned>((ldo / 8 + 255) / 256), static_cast<unsigned>(p.M)), 256, 0, 1, s,
+                static_cast<const uint16_t*>(p.A), p.lda, p.K, order, ldo);
+    if (st != TG_OK) return st;
+    return launch(kernel, dim3(static_cast<unsigned>(blocks)), S::kThreads, S::kSmem, 1, s, q, codes,
+                  scales, zeros, ordered);
+}
+
+// Whether the tcgen05 kernel is the faster one.  With B MB of codes it took about 7 us +
+// 0.3·B (up to 32 rows; 0.5·B up to 64), the other 3 us + 0.53·B for every 16 rows
+// (16384×8192, B = 67, 16 / 32 / 64 rows: 31 / 36 / 44 us against 35 / 67 / 123).
+bool prefer_tc(const W4Params& p) {
+    if (p.M <= 8) return false;
+    const double mb = static_cast<double>(p.N) * static_cast<double>(p.K) / 2e6;
+    return 7.0 + (p.M <= 32 ? 0.3 : 0.5) * mb < 3.0 + 0.53 * static_cast<double>((p.M + 15) / 16) * mb;
+}
+
 template <typename T, int G, bool ZERO>
 tg_status_t launch_group(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    if (prefer_tc(p)) {
+        if (p.M <= 16) return launch_tc<T, G, 16, ZERO>(p, dev, s);
+        if (p.M <= 32) return launch_tc<T, G, 32, ZERO>(p, dev, s);
+        return launch_tc<T, G, 64, ZERO>(p, dev, s);
+    }
     if (p.M <= 8) return launch_tiles<T, G, 1, ZERO>(p, dev, s);
     return launch_tiles<T, G, 2, ZERO>(p, dev, s);
 }
@@ -217,6 +308,7 @@ bool tg::w4_take_timeout() {
         return false;
     }
     n = 0;
+    ++g_timeouts;
     cudaMemcpyToSymbol(tg::g_w4_timeouts, &n, sizeof(n));
     cudaGetLastError();
     return true;
