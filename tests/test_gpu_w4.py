@@ -105,6 +105,21 @@ def test_batches_of_odd_sizes(tg, M, N, K, group):
     check(tg, M, N, K, BF16, group, False, residual=True, out_dtype=torch.float32, seed=1)
 
 
+@pytest.mark.parametrize("M", [65, 127, 129, 200, 400])
+@pytest.mark.parametrize("dtype,group,zeros", [(HALF, 128, True), (BF16, 32, False), (BF16, 64, True)])
+def test_fp32_results_round_no_weight(tg, M, dtype, group, zeros):
+    """However many rows: an fp32 result has fp32 sums' error and no more."""
+    N, K = 1100, 2311
+    a, bq, bscale, bzero = make(M, N, K, dtype, group, zeros, 3, 1)
+    r = torch.randn(M, N, device="cuda").to(dtype)
+    b = torch.randn(N, device="cuda")
+    c = tg.gemm_w4(a, bq, bscale, N, group, True, bzero=bzero, bias=b, residual=r,
+                   out_dtype=torch.float32)
+    W = ops64.w4_weight(bq, bscale, bzero, N, K, group)
+    want, bound = ops64.w4(a, W, bias=b, relu=True, residual=r)
+    ops64.assert_close(c, want, bound, f"{M} {dtype} {group}")
+
+
 def test_batches_of_changing_shapes(tg):
     """One stream's workspace serves every shape: what one call leaves there does not
     show in the next."""

@@ -488,6 +488,16 @@ __global__ void __launch_bounds__(256) tg_gemm_w4_simple(const W4Params p) {
     }
 }
 
+// Both halves times s, each rounded once.
+__device__ __forceinline__ uint32_t w4_scale(uint32_t v, __half s) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&v), __half2half2(s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t w4_scale(uint32_t v, __nv_bfloat16 s) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), __bfloat162bfloat162(s));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // W as a K×N matrix of T (row stride ldo, a multiple of 8), for the dense GEMM
 // on many rows of A.  Here (code - zero)·scale is rounded to T, as the tensor
 // cores read 16-bit operands: at most half an ulp of each weight, an error of
@@ -505,17 +515,16 @@ __global__ void __launch_bounds__(256)
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t n0 = t % tiles_n * 64, k0 = t / tiles_n * 128;
         const int64_t kb = k0 + 16 * kq;
-        float v[2][16];
+        uint32_t v[2][2][4];  // of two rows and two words: pairs (w_i, w_i+4)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int64_t n = n0 + 2 * pair + i;
-            float s = 0.0f;
-            int z = 8;
-            uint32_t w[2] = {0, 0};
+            T s = op_round<T>(0.0f);
+            uint32_t z = 8, w[2] = {0, 0};
             if (n < p.N && kb < p.K) {
                 const int64_t g = kb / p.group;
-                s = op_to_float(static_cast<const T*>(p.scale)[g * p.lds + n]);
-                if (p.zero != nullptr) z = p.zero[g * p.ldz + n] & 15;
+                s = static_cast<const T*>(p.scale)[g * p.lds + n];
+                if (p.zero != nullptr) z = p.zero[g * p.ldz + n] & 15u;
                 const uint8_t* src = p.Bq + n * p.ldbq + kb / 2;
                 if (kb + 16 <= p.K) {
                     const uint2 u = *reinterpret_cast<const uint2*>(src);
@@ -526,15 +535,21 @@ __global__ void __launch_bounds__(256)
                         w[j >> 2] |= static_cast<uint32_t>(src[j]) << (8 * (j & 3));
                 }
             }
+            const W4Decode<T> decode(z);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v[i][j] = s * static_cast<float>(static_cast<int>(w[j >> 3] >> (4 * (j & 7)) & 15u) - z);
+            for (int j = 0; j < 2; ++j) {
+                decode(w[j], v[i][j]);  // code - zero point, exactly
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][j][e] = w4_scale(v[i][j][e], s);
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            alignas(4) const T two[2] = {op_round<T>(v[0][j]), op_round<T>(v[1][j])};
-            tile[16 * kq + j][pair] = *reinterpret_cast<const uint32_t*>(two);
-        }
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                tile[16 * kq + 8 * j + e][pair] = __byte_perm(v[0][j][e], v[1][j][e], 0x5410);
+                tile[16 * kq + 8 * j + 4 + e][pair] = __byte_perm(v[0][j][e], v[1][j][e], 0x7632);
+            }
         __syncthreads();
         for (int c = threadIdx.x; c < 128 * 8; c += 256) {
             const int64_t k = k0 + (c >> 3), n = n0 + 8 * (c & 7);

@@ -21,10 +21,6 @@ bool misaligned(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 
-// Above this many rows of A the weights are decoded to 16 bits once and the
-// dense GEMM runs on them.
-constexpr int64_t kDenseRows = 64;
-
 template <typename T>
 tg_status_t launch_dense(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
                          const tg::OpDevice& dev, cudaStream_t s) {
@@ -293,10 +289,38 @@ tg_status_t launch_zero(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
 }
 
 template <typename T>
-tg_status_t launch_rows(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+tg_status_t launch_few(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
     if (p.group == 32) return launch_zero<T, 32>(p, dev, s);
     if (p.group == 64) return launch_zero<T, 64>(p, dev, s);
     return launch_zero<T, 128>(p, dev, s);
+}
+
+// Whether the weights are decoded to T once, each rounded, and the dense GEMM runs on
+// them, instead of passes of 64 rows through the kernels above.  Never for an fp32 result,
+// which the rounding of the weights would spoil.  With B MB of codes a pass takes about
+// 19 us + 0.34·B, the dense way 8 us + 2.27·B up to 256 rows (16384×8192, B = 67, 128 /
+// 192 / 256 rows: 83 / 126 / 169 us against 160 / 160 / 159; 4096×4096, 128 rows: 43
+// against 26).
+bool prefer_dense(const W4Params& p) {
+    if (p.M <= 64 || p.out_f32) return false;
+    const double mb = static_cast<double>(p.N) * static_cast<double>(p.K) / 2e6;
+    return 8.0 + 2.27 * mb < static_cast<double>((p.M + 63) / 64) * (19.0 + 0.34 * mb);
+}
+
+template <typename T>
+tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
+                        const tg::OpDevice& dev, cudaStream_t s) {
+    if (prefer_dense(p)) return launch_dense<T>(in_dtype, p, x, dev, s);
+    for (int64_t m = 0; m < p.M; m += 64) {
+        W4Params q = p;
+        q.M = p.M - m < 64 ? p.M - m : 64;
+        q.A = static_cast<const T*>(p.A) + m * p.lda;
+        q.C = static_cast<char*>(p.C) + m * p.ldc * (p.out_f32 ? 4 : 2);
+        if (p.resid != nullptr) q.resid = static_cast<const T*>(p.resid) + m * p.ldr;
+        const tg_status_t st = launch_few<T>(q, dev, s);
+        if (st != TG_OK) return st;
+    }
+    return TG_OK;
 }
 
 }  // namespace
@@ -375,9 +399,6 @@ extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* B
     p.relu = x.activation == TG_EPI_RELU ? 1 : 0;
     p.out_f32 = x.out_dtype == TG_DTYPE_F32 ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (M > kDenseRows)
-        return in_dtype == TG_DTYPE_BF16 ? launch_dense<__nv_bfloat16>(in_dtype, p, x, dev, s)
-                                         : launch_dense<__half>(in_dtype, p, x, dev, s);
-    return in_dtype == TG_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(p, dev, s)
-                                     : launch_rows<__half>(p, dev, s);
+    return in_dtype == TG_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(in_dtype, p, x, dev, s)
+                                     : launch_rows<__half>(in_dtype, p, x, dev, s);
 }
