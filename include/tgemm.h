@@ -292,16 +292,15 @@ tg_status_t tg_gemm_sp24(int32_t in_dtype, const void* Ac, const void* E, const 
  * Bzero     device, ceil(K/group) rows of N bytes, row stride ldbz ≥ N, 16-byte
  *           aligned, ldbz a multiple of 16 (else TG_ERR_MISALIGNED); or NULL.
  * C, ldc, epi, stream  as tg_gemm_ex.
- * Rounding  Few rows, and any number of rows with an fp32 result: no weight is
- *           rounded, the group sums of A·(code - z) are scaled in fp32; the codes
- *           are read once for every 64 rows.  Many rows with a 16-bit result: W is
- *           decoded once to in_dtype, each weight rounded, and the dense GEMM runs
- *           on it.  Which of the two is the faster one decides between them.
- * Memory    The decoded W (K × roundup(N, 8) elements), or for 9 to 64 rows A in
- *           the kernel's order and the blocks' shares of sums, in buffers that
- *           belong to the (device, stream), are grown on demand and kept until
- *           process exit.  The first call of a size on a stream has to come before
- *           any capture (else TG_ERR_NO_MEMORY).
+ * Rounding  Up to 64 rows, and any number of rows with an fp32 result: no weight
+ *           is rounded, the group sums of A·(code - z) are scaled in fp32; the
+ *           codes are read once for every 64 rows.  More rows with a 16-bit result:
+ *           each W[n][k] is rounded to in_dtype, as a dense weight would be.
+ * Memory    A in the kernels' order and the blocks' shares of sums (9 rows and
+ *           more), or W decoded (K × roundup(N, 8) elements, where the dense GEMM
+ *           is the faster way), in buffers that belong to the (device, stream), are
+ *           grown on demand and kept until process exit.  The first call of a size
+ *           on a stream has to come before any capture (else TG_ERR_NO_MEMORY).
  * K == 0:   C = out(act(bias) + R); A, Bq, Bscale and Bzero may be NULL.
  * Errors:   TG_ERR_INVALID_VALUE for an unknown type, activation or group, a
  *           size out of range, a stride below its row, a NULL pointer where one

@@ -105,6 +105,38 @@ def test_batches_of_odd_sizes(tg, M, N, K, group):
     check(tg, M, N, K, BF16, group, False, residual=True, out_dtype=torch.float32, seed=1)
 
 
+@pytest.mark.parametrize("M,N,K", [(65, 1, 1), (66, 5, 300), (100, 129, 127), (257, 600, 4099), (512, 4096, 2304),
+                                   (300, 5003, 3001), (1000, 1031, 515), (70, 20000, 2048), (512, 16384, 8192),
+                                   (129, 256, 60000), (3000, 2048, 1040), (70000, 64, 136)])
+@pytest.mark.parametrize("dtype,group,zeros", [(HALF, 128, False), (BF16, 32, True), (HALF, 64, True)])
+def test_many_rows(tg, M, N, K, dtype, group, zeros):
+    """Tiles of several widths, whole and shared, with ends inside units, groups and bytes."""
+    check(tg, M, N, K, dtype, group, zeros, bias=True, relu=True, residual=True, pad=1)
+
+
+@pytest.mark.parametrize("M", [16, 64, 512])
+@pytest.mark.parametrize("dtype,group", [(HALF, 128), (BF16, 32), (HALF, 64)])
+def test_units_of_k_stay_apart(tg, M, dtype, group):
+    """Row m of A picks 128 columns of W, again and again: a stage of codes, scales or zero
+    points that is refilled too early, or read too late, shows in one column of results."""
+    N, K = 8192, 8192
+    _, bq, bscale, bzero = make(1, N, K, dtype, group, True)
+    a = torch.zeros(M, K, device="cuda", dtype=dtype)
+    for m in range(M):
+        a[m, m % 64 * 128:m % 64 * 128 + 128] = 1
+    W = ops64.w4_weight(bq, bscale, bzero, N, K, group).reshape(N, 64, 128)
+    want = W.sum(2).T.repeat(-(-M // 64), 1)[:M]
+    size = W.abs().sum(2).T.repeat(-(-M // 64), 1)[:M]
+    bound = (K + 4) * 2.0 ** -23 * size + (ops64.U[dtype] if M > DENSE_ROWS else 0.0) * size
+    for _ in range(20):
+        ops64.assert_close(tg.gemm_w4(a, bq, bscale, N, group, bzero=bzero), want, bound, f"{M}")
+
+
+@pytest.mark.parametrize("M", [100, 512])
+def test_a_wait_that_runs_out_with_many_rows(tg, M):
+    test_a_wait_that_runs_out_is_reported_once(tg, M, 4096, 4096)
+
+
 @pytest.mark.parametrize("M", [65, 127, 129, 200, 400])
 @pytest.mark.parametrize("dtype,group,zeros", [(HALF, 128, True), (BF16, 32, False), (BF16, 64, True)])
 def test_fp32_results_round_no_weight(tg, M, dtype, group, zeros):

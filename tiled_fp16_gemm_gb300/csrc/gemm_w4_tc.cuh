@@ -81,18 +81,28 @@ __device__ __forceinline__ int64_t tc_block_of(int64_t units, int64_t blocks, in
 // A in the order of the decoded pairs, in rows of `ldo` (a multiple of 128), zero past
 // column K: out[8q + (0 4 1 5 2 6 3 7)] <- a[8q + (0 .. 7)] read by place: 0 4 1 5 2 6 3 7.
 __global__ void __launch_bounds__(256)
-    tg_w4_order(const uint16_t* __restrict__ A, int64_t lda, int64_t K, uint16_t* __restrict__ out,
-                int64_t ldo) {
+    tg_w4_order(const uint16_t* __restrict__ A, int64_t lda, int64_t M, int64_t K,
+                uint16_t* __restrict__ out, int64_t ldo) {
     op_wait_previous();
     op_release_next();
     const int64_t c = int64_t{blockIdx.x} * 256 + threadIdx.x;
     if (8 * c >= ldo) return;
-    const uint16_t* a = A + blockIdx.y * lda;
-    uint32_t h[8];
+    const bool wide = (reinterpret_cast<uintptr_t>(A) & 15) == 0 && lda % 8 == 0 && 8 * c + 8 <= K;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        const uint16_t* a = A + m * lda;
+        uint4 x;
+        if (wide) {
+            x = *reinterpret_cast<const uint4*>(a + 8 * c);
+        } else {
+            uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 8 * c + i < K ? a[8 * c + i] : 0;
-    *reinterpret_cast<uint4*>(out + blockIdx.y * ldo + 8 * c) =
-        make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
+            for (int i = 0; i < 8; ++i) h[i] = 8 * c + i < K ? a[8 * c + i] : 0;
+            x = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+        *reinterpret_cast<uint4*>(out + m * ldo + 8 * c) =
+            make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+    }
 }
 
 // 16 columns of this warp's lanes from registers.
@@ -342,8 +352,6 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
 #pragma unroll
             for (int c = 0; c < S::kGroups; ++c)
                 z[c] = ZERO ? tc_shared[at - base + kTcZeroAt + c * kTcRows + row] & 15u : 8u;
-            __syncwarp();
-            if (lane == 0) tc_arrive(c_empty + 8 * s);
             const int old = i - kTcABufs;
             if (old >= 0 && !wait(done + 8 * (old % kTcDone), old / kTcDone & 1)) break;
             tc_after_sync();
@@ -364,7 +372,12 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) tc_arrive(a_full + 8 * a);
+            if (lane == 0) {
+                tc_arrive(a_full + 8 * a);
+                // not before the codes have been used: with the arrival right behind the
+                // loads a stage was refilled before the last of them had come back
+                tc_arrive(c_empty + 8 * s);
+            }
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ sums and C
@@ -387,8 +400,6 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             for (int c = 0; c < S::kGroups; ++c)
                 scale[c] = op_to_float(*reinterpret_cast<const T*>(
                     tc_shared + (ss - base) + s * kTcScaleBytes + (c * kTcRows + row) * 2));
-            __syncwarp();
-            if (lane == 0) tc_arrive(s_empty + 8 * s);
             if (!wait(done + 8 * (i % kTcDone), i / kTcDone & 1)) break;
             tc_after_sync();
             const uint32_t at = d_cols + lanes + d * S::kDCols;
@@ -414,7 +425,10 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             }
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) tc_arrive(d_empty + 8 * d);
+            if (lane == 0) {
+                tc_arrive(d_empty + 8 * d);
+                tc_arrive(s_empty + 8 * s);  // the scales have been used, as the codes above
+            }
             if (kb + 1 == q.k_units || i + 1 == n_units) {
                 const int64_t n = row_block * kTcRows + row;
                 bool last = true;

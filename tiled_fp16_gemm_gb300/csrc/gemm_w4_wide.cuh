@@ -1,0 +1,403 @@
+// Products of many rows of A with 4-bit weights and a 16-bit result, on tcgen05: W·Aᵀ
+// with W decoded into tensor memory, each weight rounded to T.
+//
+// As in gemm_w4_tc.cuh the weights are the MMA's A operand (units of 128 rows of W by
+// 128 k), decoded by threads that own a row.  Here (code - z) · s is rounded to T before
+// it is stored, as a dense 16-bit weight would be: an error of at most half an ulp of
+// each weight, below that of a 16-bit result's rounding for all but cancelling sums.  So
+// one accumulator of up to 256 tokens runs over the whole of k, and the MMAs (1024 cycles
+// a unit at 256 tokens) hide the decoding (some 270 instructions of each scheduler).
+//
+// What bounds it after that is the way of A to the SMs: a unit's tokens are 64 KB, which
+// every block would fetch for itself.  The blocks of a cluster take row blocks side by
+// side at the same k: each fetches its part of the tokens and multicasts it to all.
+//
+// Roles of a block's 24 warps (all meet on mbarriers):
+//   0             fetches codes, scales and zero points by TMA
+//   1             issues the MMAs of a unit, and its commits
+//   2             fetches its part of A by TMA, for every block of the cluster
+//   4-7, 20-23    read the accumulator back and write C, 16 tokens at a time in turn
+//   8-19          decode, in three groups of four warps that take units in turn
+// The clusters have whole tiles, or share all units (tile by tile, k inside) evenly: then
+// each block leaves its sums of a shared tile in the workspace, and the last one to come
+// adds all of them, in the order of k: the same bits every time.
+#pragma once
+
+#include "gemm_w4_tc.cuh"
+
+namespace tg {
+
+constexpr int kWideCluster = 2;
+constexpr int kWideThreads = 768;
+constexpr int kWideStages = 3;           // of codes, and of A
+constexpr int kWideTokens = 256;         // of a tile at most
+constexpr int kWideCodeBytes = 10240;    // codes 8192, scales ≤ 1024, zero points ≤ 512
+constexpr int kWideScaleAt = 8192;
+constexpr int kWideZeroAt = 9216;
+constexpr int kWideXBytes = kWideTokens * 256;
+constexpr int kWideSmem = 1024 + kWideStages * (kWideXBytes + kWideCodeBytes) + 256;
+
+struct WideLaunch {
+    W4Params p;
+    uint64_t limit_ns;
+    int32_t inject;      // 1: block 0's first codes are left out (for tests of the limit)
+    int32_t tokens;      // of a tile: a multiple of 32
+    int32_t m_tiles;
+    int32_t k_units;
+    int64_t units;       // in all: (row blocks / cluster) · m_tiles · k_units
+    int32_t grain;       // units that stay together: k_units (whole tiles) or 1
+    int32_t clusters;
+    float* slots;        // two per block: the sums of its first and last tile
+    uint32_t* counters;  // eight per block
+};
+
+// A box to the same place in every block of the cluster, and its bytes to their barriers.
+__device__ __forceinline__ void wide_tma_all(uint32_t dst, const void* map, uint32_t bar, uint32_t x,
+                                             uint32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar),
+        "h"(static_cast<uint16_t>((1 << kWideCluster) - 1))
+        : "memory");
+}
+
+// The MMAs of a unit, then the commits: to `done` here, to `free` in every block.  As
+// tc_unit, with one accumulator; `box`: the second 64 k of b, in 16 bytes.
+__device__ __forceinline__ void wide_unit(uint32_t d, uint32_t a, uint64_t b, uint32_t box, uint32_t idesc,
+                                          uint32_t add, uint32_t done, uint32_t free) {
+    asm volatile(
+        "{\n\t.reg .pred e, first, one;\n\t.reg .b32 ak;\n\t.reg .b64 bk, bx;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 one, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, first;\n\t"
+        "add.u32 ak, %1, 8;\n\tadd.u64 bk, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "add.u32 ak, %1, 16;\n\tadd.u64 bk, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "add.u32 ak, %1, 24;\n\tadd.u64 bk, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "cvt.u64.u32 bx, %3;\n\tadd.u64 bk, %2, bx;\n\tadd.u32 ak, %1, 32;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 40;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 48;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 56;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%7], %8;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(box), "r"(idesc), "r"(add), "r"(done), "r"(free),
+        "h"(static_cast<uint16_t>((1 << kWideCluster) - 1))
+        : "memory");
+}
+
+// 16 sums of a share, which lie [token / 4][row][token % 4].
+__device__ __forceinline__ void wide_load(const float* from, float (&v)[16]) {
+#pragma unroll
+    for (int m = 0; m < 16; m += 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(from + m * kTcRows));
+        v[m] = f.x, v[m + 1] = f.y, v[m + 2] = f.z, v[m + 3] = f.w;
+    }
+}
+// Reports all MMAs so far to a barrier here.
+__device__ __forceinline__ void wide_commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+template <typename T, int G, bool ZERO>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    tg_gemm_w4_wide(const __grid_constant__ WideLaunch q, const __grid_constant__ CUtensorMap codes,
+                    const __grid_constant__ CUtensorMap scales, const __grid_constant__ CUtensorMap zeros,
+                    const __grid_constant__ CUtensorMap order) {
+    constexpr int kGroups = kTcK / G;
+    extern __shared__ __align__(1024) unsigned char wide_dynamic[];
+    const W4Params& p = q.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = blockIdx.x % kWideCluster, cluster_no = blockIdx.x / kWideCluster;
+    const uint32_t base = (op_smem(wide_dynamic) + 1023) & ~1023u;
+    unsigned char* const shared = wide_dynamic + (base - op_smem(wide_dynamic));
+    const uint32_t xs = base, cs = xs + kWideStages * kWideXBytes;
+    const uint32_t bars = cs + kWideStages * kWideCodeBytes;
+    const uint32_t c_full = bars, c_empty = c_full + 8 * kWideStages;
+    const uint32_t x_full = c_empty + 8 * kWideStages, x_empty = x_full + 8 * kWideStages;
+    const uint32_t a_full = x_empty + 8 * kWideStages, done = a_full + 8 * kTcABufs;
+    const uint32_t d_full = done + 8 * kTcDone, d_empty = d_full + 8;
+    unsigned char* after = shared + (d_empty + 8 - base);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
+    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out
+
+    op_release_next();
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < kWideStages; ++i) {
+            op_bar_init(c_full + 8 * i, 1);
+            op_bar_init(c_empty + 8 * i, 4);
+            op_bar_init(x_full + 8 * i, 1);
+            op_bar_init(x_empty + 8 * i, kWideCluster);
+        }
+        for (int i = 0; i < kTcABufs; ++i) op_bar_init(a_full + 8 * i, 4);
+        for (int i = 0; i < kTcDone; ++i) op_bar_init(done + 8 * i, 1);
+        op_bar_init(d_full, 1);
+        op_bar_init(d_empty, 8);
+        op_bar_init_done();
+        *dead = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         op_smem(tmem_at))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before_sync();
+    __syncthreads();
+    w4_cluster_sync();  // no copy or commit reaches a block before its barriers are there
+    tc_after_sync();
+    // all columns are this block's, so they begin at 0
+    constexpr uint32_t tmem = 0;
+    constexpr uint32_t d_cols = tmem + 64 * kTcABufs;
+
+    const int64_t grains = q.units / q.grain;
+    const int64_t u0 = tc_first(grains, q.clusters, cluster_no) * q.grain;
+    const int n_units =
+        static_cast<int>(tc_first(grains, q.clusters, cluster_no + 1) * q.grain - u0);
+    int64_t tile = u0 / q.k_units;
+    int kb = static_cast<int>(u0 - tile * q.k_units);
+    // A warp waits; false once a wait has run out, here or in another warp.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, op_bar_try(bar, parity))) return true;
+        const bool ok = *dead == 0 && op_bar_wait_slow(bar, parity, q.limit_ns);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (lane == 0) {
+            *dead = 1;
+            atomicOr(&g_w4_timeouts, 1u);
+        }
+        __syncwarp();
+        return false;
+    };
+    auto next_unit = [&] {
+        if (++kb == q.k_units) kb = 0, ++tile;
+    };
+    auto first_row = [&] { return (tile / q.m_tiles * kWideCluster + rank) * kTcRows; };
+    auto first_token = [&] { return tile % q.m_tiles * q.tokens; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ codes
+        // No wait for the ordering kernel: see gemm_w4_tc.cuh.
+        int issued = 0;
+        for (int i = 0; i < n_units; ++i, next_unit()) {
+            const int s = i % kWideStages;
+            if (i >= kWideStages && !wait(c_empty + 8 * s, (i / kWideStages - 1) & 1)) break;
+            if (lane == 0 && !(q.inject == 1 && blockIdx.x == 0 && i == 0)) {
+                const uint32_t to = cs + s * kWideCodeBytes, bar = c_full + 8 * s;
+                const uint32_t n = static_cast<uint32_t>(first_row());
+                op_bar_expect(bar, 8192 + (ZERO ? 384 : 256) * kGroups);
+                op_tma_2d(to, &codes, bar, kb * 64, n);
+                op_tma_2d(to + kWideScaleAt, &scales, bar, n, kb * kGroups);
+                if (ZERO) op_tma_2d(to + kWideZeroAt, &zeros, bar, n, kb * kGroups);
+            }
+            issued = i + 1;
+        }
+        // copies under way have to land before the block ends
+        bool ok = true;
+        for (int i = issued > kWideStages ? issued - kWideStages : 0; ok && i < issued; ++i)
+            if (lane == 0) ok = op_bar_wait(c_full + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ A
+        op_wait_previous();
+        const uint32_t part = q.tokens / kWideCluster;
+        int issued = 0;
+        for (int i = 0; i < n_units; ++i, next_unit()) {
+            const int s = i % kWideStages;
+            if (i >= kWideStages && !wait(x_empty + 8 * s, (i / kWideStages - 1) & 1)) break;
+            if (lane == 0) {
+                const uint32_t to = xs + s * kWideXBytes + rank * part * 128, bar = x_full + 8 * s;
+                const uint32_t m = static_cast<uint32_t>(first_token()) + rank * part;
+                op_bar_expect(bar, q.tokens * 256);
+                wide_tma_all(to, &order, bar, kb * kTcK, m);
+                wide_tma_all(to + q.tokens * 128, &order, bar, kb * kTcK + 64, m);
+            }
+            issued = i + 1;
+        }
+        // the copies have to land, and the other blocks' commits to arrive, before this
+        // block ends
+        bool ok = true;
+        for (int i = issued > kWideStages ? issued - kWideStages : 0; ok && i < issued; ++i)
+            if (lane == 0)
+                ok = op_bar_wait(x_full + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs) &&
+                     op_bar_wait(x_empty + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
+        const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) |
+                               (static_cast<uint32_t>(q.tokens >> 3) << 17) | (8u << 24);
+        int issued = 0, tiles = 0;
+        for (int i = 0; i < n_units; ++i) {
+            const int s = i % kWideStages, a = i % kTcABufs;
+            const bool first = i == 0 || kb == 0;
+            if (!wait(x_full + 8 * s, i / kWideStages & 1)) break;
+            if (first && tiles++ > 0 && !wait(d_empty, tiles & 1)) break;
+            if (!wait(a_full + 8 * a, i / kTcABufs & 1)) break;
+            tc_after_sync();
+            wide_unit(d_cols, tmem + 64 * a, tc_desc(xs + s * kWideXBytes), q.tokens * 128 / 16, idesc,
+                      first ? 0 : 1, done + 8 * (i % kTcDone), x_empty + 8 * s);
+            if (kb + 1 == q.k_units || i + 1 == n_units) wide_commit(d_full);
+            issued = i + 1;
+            next_unit();
+        }
+        // the MMAs have to be over before the tensor memory is given back
+        if (issued > 0 && lane == 0)
+            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kW4LandNs);
+        __syncwarp();
+    } else if (warp >= 8 && warp < 20) {
+        // ------------------------------------------------------------ decoding
+        const int group = (warp - 8) >> 2;
+        const uint32_t row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        for (int i = group; i < n_units; i += kTcGroups) {
+            const int s = i % kWideStages, a = i % kTcABufs;
+            if (!wait(c_full + 8 * s, i / kWideStages & 1)) break;
+            const uint32_t at = cs + s * kWideCodeBytes;
+            uint4 w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] = w4_lds128(at + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+            uint32_t z[kGroups];
+            T scale[kGroups];
+#pragma unroll
+            for (int c = 0; c < kGroups; ++c) {
+                scale[c] = *reinterpret_cast<const T*>(shared + (at - base) + kWideScaleAt +
+                                                       (c * kTcRows + row) * 2);
+                z[c] = ZERO ? shared[at - base + kWideZeroAt + c * kTcRows + row] & 15u : 8u;
+            }
+            const int old = i - kTcABufs;
+            if (old >= 0 && !wait(done + 8 * (old % kTcDone), old / kTcDone & 1)) break;
+            tc_after_sync();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const W4Decode<T> decode(z[c * 32 / G]);
+                const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                uint32_t r[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t v[4];
+                    decode(words[j], v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[4 * j + e] = w4_scale(v[e], scale[c * 32 / G]);
+                }
+                tc_store16(tmem + lanes + 64 * a + 16 * c, r);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                tc_arrive(a_full + 8 * a);
+                // not before the codes have been used: with the arrival right behind the
+                // loads a stage was refilled before the last of them had come back
+                tc_arrive(c_empty + 8 * s);
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ C
+        op_wait_previous();
+        const int quarter = warp & 3, set = warp < 8 ? 0 : 1;
+        const uint32_t row = 32 * quarter + lane;
+        const uint32_t at = d_cols + (static_cast<uint32_t>(32 * quarter) << 16);
+        const int64_t slot = int64_t{q.tokens} * kTcRows;
+        int i = 0;
+        uint32_t tiles = 0;
+        while (i < n_units) {
+            const int kb0 = kb;
+            const int len = q.k_units - kb < n_units - i ? q.k_units - kb : n_units - i;
+            // (a barrier of its own: a parity says nothing of a phase further off than one)
+            if (!wait(d_full, tiles++ & 1)) break;
+            tc_after_sync();
+            const int64_t n = first_row() + row, m0 = first_token();
+            const int tokens = static_cast<int>(p.M - m0 < q.tokens ? p.M - m0 : q.tokens);
+            const bool whole = len == q.k_units;
+            float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
+            for (int c = 16 * set; c < tokens; c += 32) {
+                uint32_t r[16];
+                tc_load(at + c, r);
+                if (whole) {
+                    if (n < p.N) {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m)
+                            if (c + m < tokens) w4_store<T>(p, m0 + c + m, n, __uint_as_float(r[m]));
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 16; m += 4)
+                        __stcg(reinterpret_cast<float4*>(mine + (c + m) * kTcRows),
+                               make_float4(__uint_as_float(r[m]), __uint_as_float(r[m + 1]),
+                                           __uint_as_float(r[m + 2]), __uint_as_float(r[m + 3])));
+                }
+            }
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) tc_arrive(d_empty);
+            if (!whole) {  // a share of a tile
+                __threadfence();
+                __syncwarp();
+                const int head = static_cast<int>(tc_block_of(q.units, q.clusters, tile * q.k_units));
+                const int tail = static_cast<int>(tc_block_of(q.units, q.clusters, (tile + 1) * q.k_units - 1));
+                uint32_t before = 0;
+                if (lane == 0) {
+                    uint32_t* count = q.counters + 8 * (head * kWideCluster + rank) + 4 * set + quarter;
+                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                                 : "=r"(before)
+                                 : "l"(count)
+                                 : "memory");
+                    if (before == static_cast<uint32_t>(tail - head)) *count = 0;  // for the next launch
+                }
+                before = __shfl_sync(0xffffffffu, before, 0);
+                __threadfence();
+                if (before == static_cast<uint32_t>(tail - head)) {
+                    // the head's share is in its second slot, the others' in their first
+                    for (int c = 16 * set; c < tokens; c += 32) {
+                        float sum[16];
+                        const float* from = q.slots + (2 * (int64_t{head} * kWideCluster + rank) + 1) * slot +
+                                            c * kTcRows + row * 4;
+                        wide_load(from, sum);
+                        // two at a time under way
+                        from = q.slots + 2 * (int64_t{head + 1} * kWideCluster + rank) * slot + c * kTcRows +
+                               row * 4;
+                        const int64_t step = 2 * kWideCluster * slot;
+                        for (int b = head + 1; b <= tail; b += 2, from += 2 * step) {
+                            float v[16], w[16];
+                            wide_load(from, v);
+                            if (b < tail) wide_load(from + step, w);
+#pragma unroll
+                            for (int m = 0; m < 16; ++m) sum[m] += v[m];
+                            if (b < tail) {
+#pragma unroll
+                                for (int m = 0; m < 16; ++m) sum[m] += w[m];
+                            }
+                        }
+                        if (n < p.N) {
+#pragma unroll
+                            for (int m = 0; m < 16; ++m)
+                                if (c + m < tokens) w4_store<T>(p, m0 + c + m, n, sum[m]);
+                        }
+                    }
+                }
+            }
+            i += len;
+            kb = 0;
+            ++tile;
+        }
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_at)
+                     : "memory");
+    }
+    w4_cluster_sync();  // no block leaves while another's copies or commits may come
+}
+
+}  // namespace tg

@@ -7,6 +7,7 @@
 
 #include "gemm_w4.cuh"
 #include "gemm_w4_tc.cuh"
+#include "gemm_w4_wide.cuh"
 #include "op_host.h"
 
 namespace {
@@ -84,7 +85,7 @@ int64_t w4_smem_bytes(tg::W4Launch* q) {
 
 // Clusters of `size` blocks that the device holds at once.
 template <typename Kernel>
-int max_clusters(Kernel kernel, int size, const tg::OpDevice& dev) {
+int max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
     if (size == 1) return dev.num_sms;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -94,8 +95,8 @@ int max_clusters(Kernel kernel, int size, const tg::OpDevice& dev) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
-    cfg.blockDim = dim3(tg::kW4Threads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
@@ -120,7 +121,7 @@ tg_status_t launch_tiles(const W4Params& p, const tg::OpDevice& dev, cudaStream_
     std::call_once(lim.once, [&] {
         lim.ok = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) ==
                  cudaSuccess;
-        for (int i = 0; i < 4; ++i) lim.clusters[i] = max_clusters(kernel, 1 << i, dev);
+        for (int i = 0; i < 4; ++i) lim.clusters[i] = max_clusters(kernel, 1 << i, tg::kW4Threads, kSmem, dev);
         cudaGetLastError();
     });
     if (!lim.ok) return TG_ERR_LAUNCH;
@@ -256,10 +257,109 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
     q.inject = tg::op_take_inject();
     st = launch(tg::tg_w4_order,
                 dim3(static_cast<unsigned>((ldo / 8 + 255) / 256), static_cast<unsigned>(p.M)), 256, 0, 1, s,
-                static_cast<const uint16_t*>(p.A), p.lda, p.K, order, ldo);
+                static_cast<const uint16_t*>(p.A), p.lda, p.M, p.K, order, ldo);
     if (st != TG_OK) return st;
     return launch(kernel, dim3(static_cast<unsigned>(blocks)), S::kThreads, S::kSmem, 1, s, q, codes,
                   scales, zeros, ordered);
+}
+
+// Fills in the tile's width and the division of the work with the least time, and returns
+// that time in us.  Measured: a unit
+// takes 0.37 us + 1.4 ns per token (0.46 / 0.55 / 0.73 us at 64 / 128 / 256 tokens); a
+// tile that is shared 4 us + 18 ns per token and share more.  (256 rows of 16384×8192:
+// whole tiles on 64 of 76 clusters 50 us, all shared evenly 58; 2048 rows of 16384×4096:
+// 221 and 194.)
+double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
+    q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
+    constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
+    const int64_t row_tiles = (p.N + rows - 1) / rows;
+    double least = 1e300;
+    for (int32_t tokens = 32; tokens <= tg::kWideTokens; tokens += 32) {
+        const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
+        const double unit = 0.37 + 0.0014 * tokens;
+        for (const int32_t grain : {q->k_units, 1}) {
+            const int64_t grains = tiles * q->k_units / grain;
+            const int64_t clusters = grains < limit ? grains : limit;
+            const int64_t most = (grains + clusters - 1) / clusters * grain;
+            double time = unit * static_cast<double>(most);
+            if (grain != q->k_units && (most % q->k_units != 0 || grains % clusters != 0))
+                time += 4.0 + 0.018 * tokens * (2.0 + static_cast<double>(q->k_units) / static_cast<double>(most));
+            if (time < least) {
+                least = time;
+                q->tokens = tokens;
+                q->m_tiles = static_cast<int32_t>(m_tiles);
+                q->grain = grain;
+                q->clusters = static_cast<int32_t>(clusters);
+                q->units = tiles * q->k_units;
+            }
+        }
+    }
+    return 5.5 + least;
+}
+
+// Many rows of A with a 16-bit result, on tcgen05.
+template <typename T, int G, bool ZERO>
+tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    auto kernel = tg::tg_gemm_w4_wide<T, G, ZERO>;
+    struct Limits {
+        std::once_flag once;
+        int clusters = 0;
+    };
+    static Limits limits[tg::kOpMaxDevices];
+    Limits& lim = limits[dev.dev];
+    std::call_once(lim.once, [&] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tg::kWideSmem) ==
+            cudaSuccess)
+            lim.clusters = max_clusters(kernel, tg::kWideCluster, tg::kWideThreads, tg::kWideSmem, dev);
+        cudaGetLastError();
+    });
+    if (lim.clusters < 1) return TG_ERR_LAUNCH;
+    tg::WideLaunch q;
+    std::memset(&q, 0, sizeof(q));
+    q.p = p;
+    q.limit_ns = tg::op_wait_limit_ns();
+    plan_wide(p, lim.clusters, &q);
+    const int64_t blocks = int64_t{q.clusters} * tg::kWideCluster;
+    constexpr int64_t counter_bytes = 64 * 1024;  // as in launch_tc
+    if (blocks * 32 > counter_bytes) return TG_ERR_UNSUPPORTED_DEVICE;
+    const int64_t slot_bytes = 2 * blocks * q.tokens * tg::kTcRows * 4;
+    const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
+    void* ws = nullptr;
+    bool fresh = false;
+    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
+                              &ws, &fresh, g_timeouts.load());
+    if (st != TG_OK) return st;
+    if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    q.counters = static_cast<uint32_t*>(ws);
+    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + counter_bytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + counter_bytes + slot_bytes);
+    constexpr CUtensorMapDataType type =
+        std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t groups = (p.K + G - 1) / G;
+    constexpr uint32_t unit_groups = tg::kTcK / G;
+    CUtensorMap codes, scales, zeros, ordered;
+    if (!tg::op_map_2d(&codes, p.Bq, CU_TENSOR_MAP_DATA_TYPE_UINT8, (p.K + 1) / 2, p.N, p.ldbq,
+                       tg::kTcK / 2, tg::kTcRows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !tg::op_map_2d(&scales, p.scale, type, p.N, groups, p.lds * 2, tg::kTcRows, unit_groups,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !tg::op_map_2d(&ordered, order, type, ldo, p.M, ldo * 2, 64,
+                       static_cast<uint32_t>(q.tokens / tg::kWideCluster), CU_TENSOR_MAP_SWIZZLE_128B))
+        return TG_ERR_LAUNCH;
+    zeros = scales;
+    if (ZERO && !tg::op_map_2d(&zeros, p.zero, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.N, groups, p.ldz,
+                               tg::kTcRows, unit_groups, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return TG_ERR_LAUNCH;
+    q.inject = tg::op_take_inject();
+    st = launch(tg::tg_w4_order,
+                dim3(static_cast<unsigned>((ldo / 8 + 255) / 256),
+                     static_cast<unsigned>(p.M < 32768 ? p.M : 32768)),
+                256, 0, 1, s, static_cast<const uint16_t*>(p.A), p.lda, p.M, p.K, order, ldo);
+    if (st != TG_OK) return st;
+    return launch(kernel, dim3(static_cast<unsigned>(blocks)), tg::kWideThreads, tg::kWideSmem,
+                  tg::kWideCluster, s, q, codes, scales, zeros, ordered);
 }
 
 // Whether the tcgen05 kernel is the faster one.  With B MB of codes it took about 7 us +
@@ -273,6 +373,7 @@ bool prefer_tc(const W4Params& p) {
 
 template <typename T, int G, bool ZERO>
 tg_status_t launch_group(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
+    if (p.M > 64) return launch_wide<T, G, ZERO>(p, dev, s);
     if (prefer_tc(p)) {
         if (p.M <= 16) return launch_tc<T, G, 16, ZERO>(p, dev, s);
         if (p.M <= 32) return launch_tc<T, G, 32, ZERO>(p, dev, s);
@@ -295,22 +396,23 @@ tg_status_t launch_few(const W4Params& p, const tg::OpDevice& dev, cudaStream_t 
     return launch_zero<T, 128>(p, dev, s);
 }
 
-// Whether the weights are decoded to T once, each rounded, and the dense GEMM runs on
-// them, instead of passes of 64 rows through the kernels above.  Never for an fp32 result,
-// which the rounding of the weights would spoil.  With B MB of codes a pass takes about
-// 19 us + 0.34·B, the dense way 8 us + 2.27·B up to 256 rows (16384×8192, B = 67, 128 /
-// 192 / 256 rows: 83 / 126 / 169 us against 160 / 160 / 159; 4096×4096, 128 rows: 43
-// against 26).
-bool prefer_dense(const W4Params& p) {
-    if (p.M <= 64 || p.out_f32) return false;
-    const double mb = static_cast<double>(p.N) * static_cast<double>(p.K) / 2e6;
-    return 8.0 + 2.27 * mb < static_cast<double>((p.M + 63) / 64) * (19.0 + 0.34 * mb);
+// Many rows, a 16-bit result: whether the weights are decoded to T in memory and the dense
+// GEMM runs on them.  With B MB of codes that takes about 8 us + 1.5·B and the GEMM at
+// 1750 TFLOP/s (4096 rows of 4096×4096: 90 us, of 1024×1024: 13).
+bool prefer_dense(const W4Params& p, const tg::OpDevice& dev) {
+    tg::WideLaunch q;
+    const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
+    return 8.0 + 1.5 * nk / 2e6 + 2.0 * nk * static_cast<double>(p.M) / 1750e6 <
+           plan_wide(p, dev.num_sms / tg::kWideCluster, &q);
 }
 
+// Up to 64 rows of A, and any number with an fp32 result, which the rounding of the weights
+// would spoil, go through the exact kernels, 64 rows at a time.
 template <typename T>
 tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
                         const tg::OpDevice& dev, cudaStream_t s) {
-    if (prefer_dense(p)) return launch_dense<T>(in_dtype, p, x, dev, s);
+    if (p.M > 64 && !p.out_f32)
+        return prefer_dense(p, dev) ? launch_dense<T>(in_dtype, p, x, dev, s) : launch_few<T>(p, dev, s);
     for (int64_t m = 0; m < p.M; m += 64) {
         W4Params q = p;
         q.M = p.M - m < 64 ? p.M - m : 64;
