@@ -13,7 +13,7 @@
 // added, times the row's scale, to the sums that a thread keeps in registers.
 //
 // Roles of a block's 20 warps, or 24 for 64 columns (all meet on mbarriers):
-//   0      fetches codes, scales and zero points by TMA, kCodeStages units ahead
+//   0      fetches codes, scales and zero points by TMA, kTcCodeStages units ahead
 //   1      issues the MMAs of a unit, and one commit
 //   2      fetches A by TMA
 //   4-7    read the accumulators back (a quarter of the rows each), scale and sum,
@@ -22,6 +22,13 @@
 // The blocks share all units (row block by row block, k inside) evenly.  Where a row
 // block is shared, each block leaves its sums in the workspace, and the last one to
 // come adds all of them, in the order of k: the same bits every time.
+//
+// What bounds it: the turn of a unit through its accumulator (issue, MMAs, wake-up, read
+// back, release), about 0.4 us with 16 columns, where an SM could get the unit's codes in
+// 0.19.  A wait costs 80 to 110 cycles even when there is nothing to wait for, so the MMA
+// warp has one barrier for all that a unit needs.  Measured: 16384×8192, G = 128, 16 / 32 /
+// 64 rows 28.6 / 32.9 / 41.8 us (2.5 / 2.1 / 1.7 TB/s; with three barriers per unit 31.0 /
+// 34.3 / 45.4), G = 32 with 64 rows 53 us (one accumulator only).
 #pragma once
 
 #include "gemm_w4.cuh"
@@ -31,14 +38,13 @@ namespace tg {
 constexpr int kTcRows = 128;
 constexpr int kTcK = 128;
 constexpr int kTcGroups = 3;       // of decoding warps
-// Depths of the rings, all divisors of kTcTurn: a role's loop is unrolled that far, and
-// its addresses and most parities are constants.
+// Depths of the rings, all divisors of kTcTurn: the MMA warp's loop is unrolled that far,
+// and its addresses and parities are constants.
 constexpr int kTcTurn = 8;
 constexpr int kTcCodeStages = 8;
-constexpr int kTcCodeBytes = 9216;    // codes 8192, zero points ≤ 512
-constexpr int kTcZeroAt = 8192;
-constexpr int kTcScaleStages = 8;     // apart: read later than the codes
-constexpr int kTcScaleBytes = 1024;
+constexpr int kTcCodeBytes = 10240;   // codes 8192, scales ≤ 1024, zero points ≤ 512
+constexpr int kTcScaleAt = 8192;
+constexpr int kTcZeroAt = 9216;
 constexpr int kTcXStages = 4;
 constexpr int kTcABufs = 4;
 constexpr int kTcDone = 8;            // barriers of finished units
@@ -48,14 +54,13 @@ struct TcShape {
     static constexpr int kGroups = kTcK / G;     // of k in a unit
     static constexpr int kDCols = NP * kGroups;  // accumulator columns of a unit
     static constexpr int kDBufs = 2 * kDCols <= 256 ? 2 : 1;
-    static_assert(kTcCodeStages == kTcScaleStages, "fetched together");
+    static_assert(kTcXStages == kTcABufs, "one barrier for both");
     static_assert(64 * kTcABufs + kDBufs * kDCols <= 512, "tensor memory");
     static constexpr int kXBytes = NP * 256;     // two boxes of 64 k
     static constexpr int kCols = NP < 32 ? NP : 32;  // of a thread's sums
     static constexpr int kSets = NP / kCols;         // of summing warps
     static constexpr int kThreads = 32 * (16 + 4 * kSets);
-    static constexpr int kSmem = 1024 + kTcXStages * kXBytes + kTcCodeStages * kTcCodeBytes +
-                                 kTcScaleStages * kTcScaleBytes + 512;
+    static constexpr int kSmem = 1024 + kTcXStages * kXBytes + kTcCodeStages * kTcCodeBytes + 512;
 };
 
 struct TcLaunch {
@@ -204,12 +209,9 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
     const uint32_t base = (op_smem(tc_dynamic) + 1023) & ~1023u;
     unsigned char* const tc_shared = tc_dynamic + (base - op_smem(tc_dynamic));
     const uint32_t xs = base, cs = xs + kTcXStages * S::kXBytes;
-    const uint32_t ss = cs + kTcCodeStages * kTcCodeBytes;
-    const uint32_t bars = ss + kTcScaleStages * kTcScaleBytes;
+    const uint32_t bars = cs + kTcCodeStages * kTcCodeBytes;
     const uint32_t c_full = bars, c_empty = c_full + 8 * kTcCodeStages;
-    const uint32_t s_full = c_empty + 8 * kTcCodeStages, s_empty = s_full + 8 * kTcScaleStages;
-    const uint32_t x_full = s_empty + 8 * kTcScaleStages, a_full = x_full + 8 * kTcXStages;
-    const uint32_t d_empty = a_full + 8 * kTcABufs, done = d_empty + 8 * 2;
+    const uint32_t ready = c_empty + 8 * kTcCodeStages, done = ready + 8 * kTcABufs;
     unsigned char* after = tc_shared + (done + 8 * kTcDone - base);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
     volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out
@@ -218,15 +220,10 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
     if (warp == 0 && lane == 0) {
         for (int i = 0; i < kTcCodeStages; ++i) {
             op_bar_init(c_full + 8 * i, 1);
-            op_bar_init(c_empty + 8 * i, 4);
+            op_bar_init(c_empty + 8 * i, 4 + 4 * S::kSets);  // decoded, and summed up
         }
-        for (int i = 0; i < kTcScaleStages; ++i) {
-            op_bar_init(s_full + 8 * i, 1);
-            op_bar_init(s_empty + 8 * i, 4 * S::kSets);
-        }
-        for (int i = 0; i < kTcXStages; ++i) op_bar_init(x_full + 8 * i, 1);
-        for (int i = 0; i < kTcABufs; ++i) op_bar_init(a_full + 8 * i, 4);
-        for (int i = 0; i < S::kDBufs; ++i) op_bar_init(d_empty + 8 * i, 4 * S::kSets);
+        // all that a unit's MMAs wait for: W decoded, A's copies, the accumulator read
+        for (int i = 0; i < kTcABufs; ++i) op_bar_init(ready + 8 * i, 4 + 1 + 4 * S::kSets);
         for (int i = 0; i < kTcDone; ++i) op_bar_init(done + 8 * i, 1);
         op_bar_init_done();
         *dead = 0;
@@ -273,26 +270,22 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
         for (int i = 0; i < n_units; ++i, next_unit()) {
             const int s = i % kTcCodeStages;
             const uint32_t old = (i / kTcCodeStages - 1) & 1;
-            if (i >= kTcCodeStages && !(wait(c_empty + 8 * s, old) && wait(s_empty + 8 * s, old))) break;
+            if (i >= kTcCodeStages && !wait(c_empty + 8 * s, old)) break;
             if (lane == 0) {
                 const uint32_t to = cs + s * kTcCodeBytes, bar = c_full + 8 * s;
                 const uint32_t n = static_cast<uint32_t>(row_block) * kTcRows;
                 if (!(q.inject == 1 && blockIdx.x == 0 && i == 0)) {
-                    op_bar_expect(bar, 8192 + (ZERO ? 128 * S::kGroups : 0));
+                    op_bar_expect(bar, 8192 + (ZERO ? 384 : 256) * S::kGroups);
                     op_tma_2d(to, &codes, bar, kb * 64, n);
+                    op_tma_2d(to + kTcScaleAt, &scales, bar, n, kb * S::kGroups);
                     if (ZERO) op_tma_2d(to + kTcZeroAt, &zeros, bar, n, kb * S::kGroups);
                 }
-                op_bar_expect(s_full + 8 * s, 256 * S::kGroups);
-                op_tma_2d(ss + s * kTcScaleBytes, &scales, s_full + 8 * s, n, kb * S::kGroups);
             }
             issued = i + 1;
         }
         // copies under way have to land before the block ends
         for (int i = issued > kTcCodeStages ? issued - kTcCodeStages : 0; i < issued; ++i)
-            if (lane == 0) {
-                op_bar_wait(c_full + 8 * (i % kTcCodeStages), i / kTcCodeStages & 1, kW4LandNs);
-                op_bar_wait(s_full + 8 * (i % kTcCodeStages), i / kTcCodeStages & 1, kW4LandNs);
-            }
+            if (lane == 0) op_bar_wait(c_full + 8 * (i % kTcCodeStages), i / kTcCodeStages & 1, kW4LandNs);
     } else if (warp == 2) {
         // ------------------------------------------------------------ A
         op_wait_previous();
@@ -302,15 +295,17 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             const int old = i - kTcXStages;
             if (old >= 0 && !wait(done + 8 * (old % kTcDone), old / kTcDone & 1)) break;
             if (lane == 0) {
-                const uint32_t to = xs + s * S::kXBytes, bar = x_full + 8 * s;
+                const uint32_t to = xs + s * S::kXBytes, bar = ready + 8 * s;
                 op_bar_expect(bar, S::kXBytes);
                 op_tma_2d(to, &order, bar, kb * kTcK, 0);
                 op_tma_2d(to + S::kXBytes / 2, &order, bar, kb * kTcK + 64, 0);
             }
             issued = i + 1;
         }
-        for (int i = issued > kTcXStages ? issued - kTcXStages : 0; i < issued; ++i)
-            if (lane == 0) op_bar_wait(x_full + 8 * (i % kTcXStages), i / kTcXStages & 1, kW4LandNs);
+        // copies under way have to land before the block ends: with their units' MMAs
+        bool ok = true;
+        for (int i = issued > kTcXStages ? issued - kTcXStages : 0; ok && i < issued; ++i)
+            if (lane == 0) ok = op_bar_wait(done + 8 * (i % kTcDone), i / kTcDone & 1, kW4LandNs);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
@@ -321,13 +316,11 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
 #pragma unroll
             for (int j = 0; j < kTcTurn; ++j) {
                 if (i0 + j >= n_units) break;
-                const int a = j % kTcABufs, d = j % S::kDBufs, s = j % kTcXStages;
-                ok = wait(x_full + 8 * s, j / kTcXStages & 1) &&
-                     (i0 + j < S::kDBufs || wait(d_empty + 8 * d, (j / S::kDBufs - 1) & 1)) &&
-                     wait(a_full + 8 * a, j / kTcABufs & 1);
+                const int a = j % kTcABufs, d = j % S::kDBufs;
+                ok = wait(ready + 8 * a, j / kTcABufs & 1);
                 if (!ok) break;
                 tc_after_sync();
-                tc_unit<G, NP>(d_cols + d * S::kDCols, tmem + 64 * a, tc_desc(xs + s * S::kXBytes), idesc,
+                tc_unit<G, NP>(d_cols + d * S::kDCols, tmem + 64 * a, tc_desc(xs + a * S::kXBytes), idesc,
                                done + 8 * j);
                 issued = i0 + j + 1;
             }
@@ -373,7 +366,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             tc_before_sync();
             __syncwarp();
             if (lane == 0) {
-                tc_arrive(a_full + 8 * a);
+                tc_arrive(ready + 8 * a);
                 // not before the codes have been used: with the arrival right behind the
                 // loads a stage was refilled before the last of them had come back
                 tc_arrive(c_empty + 8 * s);
@@ -392,16 +385,18 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
 #pragma unroll
         for (int m = 0; m < NC; ++m) sum[m] = 0.0f;
         int kb0 = kb;  // first unit of the row block here
+        if (lane == 0)  // the accumulators are empty at first
+            for (int i = 0; i < S::kDBufs; ++i) tc_arrive(ready + 8 * i);
         for (int i = 0; i < n_units; ++i) {
-            const int s = i % kTcScaleStages, d = i % S::kDBufs;
-            if (!wait(s_full + 8 * s, i / kTcScaleStages & 1)) break;
+            const int s = i % kTcCodeStages, d = i % S::kDBufs;
+            // (the scales came with the codes, and those were decoded)
+            if (!wait(done + 8 * (i % kTcDone), i / kTcDone & 1)) break;
+            tc_after_sync();
             float scale[S::kGroups];
 #pragma unroll
             for (int c = 0; c < S::kGroups; ++c)
                 scale[c] = op_to_float(*reinterpret_cast<const T*>(
-                    tc_shared + (ss - base) + s * kTcScaleBytes + (c * kTcRows + row) * 2));
-            if (!wait(done + 8 * (i % kTcDone), i / kTcDone & 1)) break;
-            tc_after_sync();
+                    tc_shared + (cs - base) + s * kTcCodeBytes + kTcScaleAt + (c * kTcRows + row) * 2));
             const uint32_t at = d_cols + lanes + d * S::kDCols;
             if constexpr (NP == 16 && S::kGroups > 1) {  // two groups at a time
 #pragma unroll
@@ -426,8 +421,8 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             tc_before_sync();
             __syncwarp();
             if (lane == 0) {
-                tc_arrive(d_empty + 8 * d);
-                tc_arrive(s_empty + 8 * s);  // the scales have been used, as the codes above
+                tc_arrive(ready + 8 * ((i + S::kDBufs) % kTcABufs));
+                tc_arrive(c_empty + 8 * s);  // the scales have been used, as the codes above
             }
             if (kb + 1 == q.k_units || i + 1 == n_units) {
                 const int64_t n = row_block * kTcRows + row;

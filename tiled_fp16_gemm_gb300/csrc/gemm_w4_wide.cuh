@@ -8,14 +8,21 @@
 // one accumulator of up to 256 tokens runs over the whole of k, and the MMAs (1024 cycles
 // a unit at 256 tokens) hide the decoding (some 270 instructions of each scheduler).
 //
-// What bounds it after that is the way of A to the SMs: a unit's tokens are 64 KB, which
-// every block would fetch for itself.  The blocks of a cluster take row blocks side by
-// side at the same k: each fetches its part of the tokens and multicasts it to all.
+// The blocks work in pairs (cta_group::2): the MMA takes 256 rows of W, 128 in each block's
+// tensor memory, and half of the tokens from each block's shared memory.  With blocks of
+// their own, the tokens multicast to both, a unit took 1370 cycles; the MMAs' reads and the
+// copies' writes then ask for all of the shared memory's 128 bytes a cycle.  Now it takes
+// 1070 with 256 tokens (the MMAs bound it) and 780 with 128 (the codes' arrival does).  An
+// arrival at the even block with release.cluster cost 1900 cycles; the plain form does not.
+//
+// Measured, 16384×8192, fp16, G = 128: 65 / 128 / 256 / 512 / 2048 rows 34 / 35 / 45 / 85 /
+// 329 us; the last two are 1600 and 1670 TFLOP/s.  (Decoding to memory, then the dense GEMM:
+// 160 us for 256 rows, 193 for 512.)  At 512 rows 64 of the 76 pairs work, on whole tiles.
 //
 // Roles of a block's 24 warps (all meet on mbarriers):
 //   0             fetches codes, scales and zero points by TMA
-//   1             issues the MMAs of a unit, and its commits
-//   2             fetches its part of A by TMA, for every block of the cluster
+//   1             of the even block: issues the pair's MMAs, and the commits to both
+//   2             fetches this block's half of the tokens by TMA
 //   4-7, 20-23    read the accumulator back and write C, 16 tokens at a time in turn
 //   8-19          decode, in three groups of four warps that take units in turn
 // The clusters have whole tiles, or share all units (tile by tile, k inside) evenly: then
@@ -29,13 +36,15 @@ namespace tg {
 
 constexpr int kWideCluster = 2;
 constexpr int kWideThreads = 768;
-constexpr int kWideStages = 3;           // of codes, and of A
+constexpr int kWideStages = 6;           // of codes
+constexpr int kWideXStages = 4;
 constexpr int kWideTokens = 256;         // of a tile at most
 constexpr int kWideCodeBytes = 10240;    // codes 8192, scales ≤ 1024, zero points ≤ 512
 constexpr int kWideScaleAt = 8192;
 constexpr int kWideZeroAt = 9216;
-constexpr int kWideXBytes = kWideTokens * 256;
-constexpr int kWideSmem = 1024 + kWideStages * (kWideXBytes + kWideCodeBytes) + 256;
+constexpr int kWideXBytes = kWideTokens / 2 * 256;
+constexpr int kWideSmem =
+    1024 + kWideXStages * kWideXBytes + kWideStages * kWideCodeBytes + 512;
 
 struct WideLaunch {
     W4Params p;
@@ -51,45 +60,53 @@ struct WideLaunch {
     uint32_t* counters;  // eight per block
 };
 
-// A box to the same place in every block of the cluster, and its bytes to their barriers.
-__device__ __forceinline__ void wide_tma_all(uint32_t dst, const void* map, uint32_t bar, uint32_t x,
-                                             uint32_t y) {
+// Address of this block's `addr` in block `rank` of the pair.
+__device__ __forceinline__ uint32_t wide_at(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void wide_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A box to this block, its bytes to a barrier of either block.
+__device__ __forceinline__ void wide_tma(uint32_t dst, const void* map, uint32_t bar, uint32_t x, uint32_t y) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar),
-        "h"(static_cast<uint16_t>((1 << kWideCluster) - 1))
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
-// The MMAs of a unit, then the commits: to `done` here, to `free` in every block.  As
-// tc_unit, with one accumulator; `box`: the second 64 k of b, in 16 bytes.
+// The MMAs of a unit, then the commits, to `done` and `free` of both blocks.  As tc_unit,
+// with one accumulator; `box`: the second 64 k of b, in 16 bytes.
 __device__ __forceinline__ void wide_unit(uint32_t d, uint32_t a, uint64_t b, uint32_t box, uint32_t idesc,
                                           uint32_t add, uint32_t done, uint32_t free) {
     asm volatile(
         "{\n\t.reg .pred e, first, one;\n\t.reg .b32 ak;\n\t.reg .b64 bk, bx;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "setp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 one, 0, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, first;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %4, first;\n\t"
         "add.u32 ak, %1, 8;\n\tadd.u64 bk, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u32 ak, %1, 16;\n\tadd.u64 bk, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u32 ak, %1, 24;\n\tadd.u64 bk, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "cvt.u64.u32 bx, %3;\n\tadd.u64 bk, %2, bx;\n\tadd.u32 ak, %1, 32;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 40;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 48;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 56;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%6], %8;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%7], %8;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(box), "r"(idesc), "r"(add), "r"(done), "r"(free),
-        "h"(static_cast<uint16_t>((1 << kWideCluster) - 1))
+        "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 
@@ -101,12 +118,45 @@ __device__ __forceinline__ void wide_load(const float* from, float (&v)[16]) {
         v[m] = f.x, v[m + 1] = f.y, v[m + 2] = f.z, v[m + 3] = f.w;
     }
 }
-// Reports all MMAs so far to a barrier here.
+// Reports all MMAs so far to a barrier of both blocks.
 __device__ __forceinline__ void wide_commit(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;\n\t}" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
         : "memory");
+}
+// p + n, not before it is needed: sixteen addresses at once do not fit the registers.
+template <typename P>
+__device__ __forceinline__ P* wide_step(P* p, int64_t n) {
+    P* r;
+    asm volatile("add.s64 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(n));
+    return r;
+}
+// Epilogue and store of 16 tokens of row n, `most` of them.
+template <typename T>
+__device__ __forceinline__ void wide_store(const W4Params& p, int64_t m, int64_t n, int most, float bias,
+                                           float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] += bias;
+        if (p.relu) v[i] = v[i] > 0.0f ? v[i] : 0.0f;
+    }
+    if (p.resid != nullptr) {
+        const char* r = static_cast<const char*>(p.resid) + 2 * (m * p.ldr + n);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < most) v[i] += op_to_float(*reinterpret_cast<const T*>(r));
+            r = wide_step(r, 2 * p.ldr);
+        }
+    }
+    char* c = static_cast<char*>(p.C) + 2 * (m * p.ldc + n);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i < most) *reinterpret_cast<T*>(c) = op_round<T>(v[i]);
+        c = wide_step(c, 2 * p.ldc);
+    }
 }
 
 template <typename T, int G, bool ZERO>
@@ -121,11 +171,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int rank = blockIdx.x % kWideCluster, cluster_no = blockIdx.x / kWideCluster;
     const uint32_t base = (op_smem(wide_dynamic) + 1023) & ~1023u;
     unsigned char* const shared = wide_dynamic + (base - op_smem(wide_dynamic));
-    const uint32_t xs = base, cs = xs + kWideStages * kWideXBytes;
+    const uint32_t xs = base, cs = xs + kWideXStages * kWideXBytes;
     const uint32_t bars = cs + kWideStages * kWideCodeBytes;
     const uint32_t c_full = bars, c_empty = c_full + 8 * kWideStages;
-    const uint32_t x_full = c_empty + 8 * kWideStages, x_empty = x_full + 8 * kWideStages;
-    const uint32_t a_full = x_empty + 8 * kWideStages, done = a_full + 8 * kTcABufs;
+    const uint32_t x_full = c_empty + 8 * kWideStages, x_empty = x_full + 8 * kWideXStages;
+    const uint32_t a_full = x_empty + 8 * kWideXStages, done = a_full + 8 * kTcABufs;
     const uint32_t d_full = done + 8 * kTcDone, d_empty = d_full + 8;
     unsigned char* after = shared + (d_empty + 8 - base);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
@@ -136,21 +186,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int i = 0; i < kWideStages; ++i) {
             op_bar_init(c_full + 8 * i, 1);
             op_bar_init(c_empty + 8 * i, 4);
-            op_bar_init(x_full + 8 * i, 1);
-            op_bar_init(x_empty + 8 * i, kWideCluster);
         }
-        for (int i = 0; i < kTcABufs; ++i) op_bar_init(a_full + 8 * i, 4);
+        for (int i = 0; i < kWideXStages; ++i) {
+            op_bar_init(x_full + 8 * i, 1);  // of the even block: both blocks' copies
+            op_bar_init(x_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kTcABufs; ++i) op_bar_init(a_full + 8 * i, 8);  // of the even block
         for (int i = 0; i < kTcDone; ++i) op_bar_init(done + 8 * i, 1);
         op_bar_init(d_full, 1);
-        op_bar_init(d_empty, 8);
+        op_bar_init(d_empty, 16);  // of the even block
         op_bar_init_done();
         *dead = 0;
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          op_smem(tmem_at))
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_before_sync();
     __syncthreads();
@@ -208,42 +260,39 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------ A
         op_wait_previous();
-        const uint32_t part = q.tokens / kWideCluster;
+        const uint32_t part = q.tokens / 2;
         int issued = 0;
         for (int i = 0; i < n_units; ++i, next_unit()) {
-            const int s = i % kWideStages;
-            if (i >= kWideStages && !wait(x_empty + 8 * s, (i / kWideStages - 1) & 1)) break;
+            const int s = i % kWideXStages;
+            if (i >= kWideXStages && !wait(x_empty + 8 * s, (i / kWideXStages - 1) & 1)) break;
             if (lane == 0) {
-                const uint32_t to = xs + s * kWideXBytes + rank * part * 128, bar = x_full + 8 * s;
+                const uint32_t to = xs + s * kWideXBytes, bar = wide_at(x_full + 8 * s, 0);
                 const uint32_t m = static_cast<uint32_t>(first_token()) + rank * part;
-                op_bar_expect(bar, q.tokens * 256);
-                wide_tma_all(to, &order, bar, kb * kTcK, m);
-                wide_tma_all(to + q.tokens * 128, &order, bar, kb * kTcK + 64, m);
+                if (rank == 0) op_bar_expect(x_full + 8 * s, q.tokens * 256);
+                wide_tma(to, &order, bar, kb * kTcK, m);
+                wide_tma(to + part * 128, &order, bar, kb * kTcK + 64, m);
             }
             issued = i + 1;
         }
-        // the copies have to land, and the other blocks' commits to arrive, before this
-        // block ends
+        // the copies have to land, and the commits to arrive, before this block ends
         bool ok = true;
-        for (int i = issued > kWideStages ? issued - kWideStages : 0; ok && i < issued; ++i)
-            if (lane == 0)
-                ok = op_bar_wait(x_full + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs) &&
-                     op_bar_wait(x_empty + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs);
+        for (int i = issued > kWideXStages ? issued - kWideXStages : 0; ok && i < issued; ++i)
+            if (lane == 0) ok = op_bar_wait(x_empty + 8 * (i % kWideXStages), i / kWideXStages & 1, kW4LandNs);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
         const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) |
-                               (static_cast<uint32_t>(q.tokens >> 3) << 17) | (8u << 24);
+                               (static_cast<uint32_t>(q.tokens >> 3) << 17) | (16u << 24);
         int issued = 0, tiles = 0;
-        for (int i = 0; i < n_units; ++i) {
-            const int s = i % kWideStages, a = i % kTcABufs;
+        for (int i = 0; rank == 0 && i < n_units; ++i) {
+            const int s = i % kWideXStages, a = i % kTcABufs;
             const bool first = i == 0 || kb == 0;
-            if (!wait(x_full + 8 * s, i / kWideStages & 1)) break;
+            if (!wait(x_full + 8 * s, i / kWideXStages & 1)) break;
             if (first && tiles++ > 0 && !wait(d_empty, tiles & 1)) break;
             if (!wait(a_full + 8 * a, i / kTcABufs & 1)) break;
             tc_after_sync();
-            wide_unit(d_cols, tmem + 64 * a, tc_desc(xs + s * kWideXBytes), q.tokens * 128 / 16, idesc,
+            wide_unit(d_cols, tmem + 64 * a, tc_desc(xs + s * kWideXBytes), q.tokens / 2 * 128 / 16, idesc,
                       first ? 0 : 1, done + 8 * (i % kTcDone), x_empty + 8 * s);
             if (kb + 1 == q.k_units || i + 1 == n_units) wide_commit(d_full);
             issued = i + 1;
@@ -294,7 +343,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             tc_before_sync();
             __syncwarp();
             if (lane == 0) {
-                tc_arrive(a_full + 8 * a);
+                wide_arrive(wide_at(a_full + 8 * a, 0));
                 // not before the codes have been used: with the arrival right behind the
                 // loads a stage was refilled before the last of them had come back
                 tc_arrive(c_empty + 8 * s);
@@ -318,16 +367,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int64_t n = first_row() + row, m0 = first_token();
             const int tokens = static_cast<int>(p.M - m0 < q.tokens ? p.M - m0 : q.tokens);
             const bool whole = len == q.k_units;
+            const float bias = p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
             float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
             for (int c = 16 * set; c < tokens; c += 32) {
                 uint32_t r[16];
                 tc_load(at + c, r);
                 if (whole) {
-                    if (n < p.N) {
+                    float v[16];
 #pragma unroll
-                        for (int m = 0; m < 16; ++m)
-                            if (c + m < tokens) w4_store<T>(p, m0 + c + m, n, __uint_as_float(r[m]));
-                    }
+                    for (int m = 0; m < 16; ++m) v[m] = __uint_as_float(r[m]);
+                    if (n < p.N) wide_store<T>(p, m0 + c, n, tokens - c, bias, v);
                 } else {
 #pragma unroll
                     for (int m = 0; m < 16; m += 4)
@@ -338,7 +387,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) tc_arrive(d_empty);
+            if (lane == 0) wide_arrive(wide_at(d_empty, 0));
             if (!whole) {  // a share of a tile
                 __threadfence();
                 __syncwarp();
@@ -377,11 +426,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 for (int m = 0; m < 16; ++m) sum[m] += w[m];
                             }
                         }
-                        if (n < p.N) {
-#pragma unroll
-                            for (int m = 0; m < 16; ++m)
-                                if (c + m < tokens) w4_store<T>(p, m0 + c + m, n, sum[m]);
-                        }
+                        if (n < p.N) wide_store<T>(p, m0 + c, n, tokens - c, bias, sum);
                     }
                 }
             }
@@ -392,12 +437,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     tc_before_sync();
     __syncthreads();
+    w4_cluster_sync();  // neither block's memory or barriers are used by the other any more
     if (warp == 1) {
+        __syncwarp();
         tc_after_sync();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_at)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(*tmem_at)
                      : "memory");
     }
-    w4_cluster_sync();  // no block leaves while another's copies or commits may come
 }
 
 }  // namespace tg

@@ -264,11 +264,10 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
 }
 
 // Fills in the tile's width and the division of the work with the least time, and returns
-// that time in us.  Measured: a unit
-// takes 0.37 us + 1.4 ns per token (0.46 / 0.55 / 0.73 us at 64 / 128 / 256 tokens); a
-// tile that is shared 4 us + 18 ns per token and share more.  (256 rows of 16384×8192:
-// whole tiles on 64 of 76 clusters 50 us, all shared evenly 58; 2048 rows of 16384×4096:
-// 221 and 194.)
+// that time in us.  Measured: a unit takes 2.4 ns per token, and 0.43 us at least (what the
+// codes take to come and be decoded); a tile that is shared 4 us + 18 ns per token and share
+// more; A in order 4 bytes an element at 4 TB/s.  16384×8192 with 65 / 128 / 192 / 256 / 512
+// rows: 34 / 36 / 38 / 46 / 86 us, on 64 of 76 pairs, with whole tiles.
 double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
     q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
@@ -276,7 +275,7 @@ double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
     double least = 1e300;
     for (int32_t tokens = 32; tokens <= tg::kWideTokens; tokens += 32) {
         const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
-        const double unit = 0.37 + 0.0014 * tokens;
+        const double unit = tokens < 180 ? 0.43 : 0.0024 * tokens;
         for (const int32_t grain : {q->k_units, 1}) {
             const int64_t grains = tiles * q->k_units / grain;
             const int64_t clusters = grains < limit ? grains : limit;
@@ -294,7 +293,7 @@ double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
             }
         }
     }
-    return 5.5 + least;
+    return 5.5 + least + 1e-6 * static_cast<double>(p.M) * static_cast<double>(p.K);
 }
 
 // Many rows of A with a 16-bit result, on tcgen05.
@@ -364,7 +363,7 @@ tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
 
 // Whether the tcgen05 kernel is the faster one.  With B MB of codes it took about 7 us +
 // 0.3·B (up to 32 rows; 0.5·B up to 64), the other 3 us + 0.53·B for every 16 rows
-// (16384×8192, B = 67, 16 / 32 / 64 rows: 31 / 36 / 44 us against 35 / 67 / 123).
+// (16384×8192, B = 67, 16 / 32 / 64 rows: 29 / 33 / 42 us against 35 / 67 / 123).
 bool prefer_tc(const W4Params& p) {
     if (p.M <= 8) return false;
     const double mb = static_cast<double>(p.N) * static_cast<double>(p.K) / 2e6;
@@ -397,13 +396,16 @@ tg_status_t launch_few(const W4Params& p, const tg::OpDevice& dev, cudaStream_t 
 }
 
 // Many rows, a 16-bit result: whether the weights are decoded to T in memory and the dense
-// GEMM runs on them.  With B MB of codes that takes about 8 us + 1.5·B and the GEMM at
-// 1750 TFLOP/s (4096 rows of 4096×4096: 90 us, of 1024×1024: 13).
+// GEMM runs on them.  With B MB of codes that takes about 10 us + 1.5·B and the GEMM at
+// 1800 TFLOP/s; tg_gemm_w4_wide, decoding every weight once for 256 rows, does not pass
+// 1600 in long runs (4096 rows of 1024×1024: 13 us against 17, of 16384×8192: 712 against
+// 700).
 bool prefer_dense(const W4Params& p, const tg::OpDevice& dev) {
     tg::WideLaunch q;
     const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
-    return 8.0 + 1.5 * nk / 2e6 + 2.0 * nk * static_cast<double>(p.M) / 1750e6 <
-           plan_wide(p, dev.num_sms / tg::kWideCluster, &q);
+    const double flops = 2.0 * nk * static_cast<double>(p.M);
+    const double wide = plan_wide(p, dev.num_sms / tg::kWideCluster, &q);
+    return 10.0 + 1.5 * nk / 2e6 + flops / 1800e6 < (wide > flops / 1600e6 ? wide : flops / 1600e6);
 }
 
 // Up to 64 rows of A, and any number with an fp32 result, which the rounding of the weights
