@@ -84,6 +84,14 @@ def test_gates(tg, rows, gates):
     check(tg, rows, 65, F32, F32, gates=gates, pad=3)
 
 
+@pytest.mark.parametrize("cols,pad", [(4097, 0), (4104, 8), (5121, 1), (9000, 0), (16392, 8), (30000, 3)])
+@pytest.mark.parametrize("rows,gates", [(1, 1), (40, 40), (300, 3), (300, 100), (700, 1), (400, 200)])
+def test_long_rows(tg, cols, pad, rows, gates):
+    """Rows that several blocks share, with gates of one, some and all rows."""
+    check(tg, rows, cols, torch.bfloat16, torch.float32, gates=gates, pad=pad)
+    check(tg, rows, cols, torch.float16, torch.float16, gates=gates, pad=pad, post=rows != 300)
+
+
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("gates", [0, 1])

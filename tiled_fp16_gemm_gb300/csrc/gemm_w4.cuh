@@ -503,8 +503,8 @@ __device__ __forceinline__ uint32_t w4_scale(uint32_t v, __nv_bfloat16 s) {
 // cores read 16-bit operands: at most half an ulp of each weight, an error of
 // the size that storing C in T has.  One 128 k × 64 n tile per block
 // iteration, turned round in shared memory; a thread decodes 16 k of two
-// neighbouring rows of W, so that it stores pairs of n.  256 threads.  Bound by its
-// stores: 16384×8192 takes about 100 us for 336 MB (3.3 TB/s).
+// neighbouring rows of W, so that it stores pairs of n.  256 threads.
+// 16384×8192 takes about 100 us for 336 MB (3.3 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256)
     tg_w4_dequant(const W4Params p, T* __restrict__ out, int64_t ldo) {

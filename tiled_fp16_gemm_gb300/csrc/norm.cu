@@ -86,21 +86,25 @@ bool wide(const void* p, int64_t ld, int bytes) {
     return p == nullptr || (!misaligned(p, 8 * bytes) && ld % 8 == 0);
 }
 
-// One launch with dependent launch allowed.
+// One launch with dependent launch allowed, in clusters of `cluster` blocks.
 template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                   Given... given) {
+tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
+                   cudaStream_t s, Given... given) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_LAUNCH;
@@ -154,6 +158,36 @@ bool allow_smem(Kernel k, int dev) {
     return true;
 }
 
+// Clusters of `size` blocks that the device holds at once (asked once for each shape).
+template <typename Kernel>
+int64_t max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
+    static std::mutex m;
+    static std::map<std::tuple<const void*, int, int, size_t, int>, int> known;
+    const auto key = std::make_tuple(reinterpret_cast<const void*>(kernel), size, threads, smem, dev.dev);
+    std::lock_guard<std::mutex> lk(m);
+    const auto it = known.find(key);
+    if (it != known.end()) return it->second;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(size);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[key] = n;
+    return n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -201,7 +235,7 @@ tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, 
             const int64_t most = int64_t{r.per_sm} * dev.num_sms;
             const int64_t blocks = (p.rows + r.groups - 1) / r.groups;
             return launch(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                          r.threads * r.groups, r.smem, s, p, r.threads, r.stages, r.stage_bytes);
+                          r.threads * r.groups, r.smem, 1, s, p, r.threads, r.stages, r.stage_bytes);
         };
         if (vec) {
             if (plan(Int<1>{}, std::true_type{})) return run(tg::tg_norm_residual_rows<TX, TR, 1, true>);
@@ -216,7 +250,7 @@ tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, 
         const size_t smem = static_cast<size_t>(p.cols) * 4;
         if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
         const int64_t grid = p.rows < 8 * dev.num_sms ? p.rows : 8 * dev.num_sms;
-        return launch(kernel, dim3(static_cast<unsigned>(grid)), 256, smem, s, p);
+        return launch(kernel, dim3(static_cast<unsigned>(grid)), 256, smem, 1, s, p);
     });
 }
 
@@ -287,28 +321,35 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
                    wide(q.dwpost, 0, 4) && wide(q.dwpre, 0, 4);
         for (int k = 0; k < 4; ++k) vec = vec && wide(in[k], ld[k], elem[k]);
         RowPlan r;
-        auto plan = [&](auto ch, auto v) {
-            constexpr int CH = decltype(ch)::value;
+        // 8 columns of a thread; longer rows on the blocks of a cluster
+        int split = 1;
+        while (split < tg::kNormSplit && cols > int64_t{split} * 8 * tg::kNormThreads) split *= 2;
+        const int part = split == 1 ? static_cast<int>(cols)
+                                    : static_cast<int>((cols + 8 * split - 1) / (8 * split)) * 8;
+        auto plan = [&](auto v) {
             constexpr bool VEC = decltype(v)::value;
-            const int threads = static_cast<int>((cols + 256 * CH - 1) / (256 * CH)) * 32;
-            const int bx = tg::norm_stage_bytes<TX, CH, VEC>(threads, cols);
-            const int stage = 2 * (bx + tg::norm_stage_bytes<TR, CH, VEC>(threads, cols));
+            const int threads = (part + 255) / 256 * 32;
+            const int bx = tg::norm_stage_bytes<TX, 1, VEC>(threads, part);
+            const int stage = 2 * (bx + tg::norm_stage_bytes<TR, 1, VEC>(threads, part));
             const bool one_gate = q.n.rows_per_gate == a->rows;
             const int gate = q.n.gate != nullptr ? bx : 0;
-            const int join = threads * CH * 32;  // a group's column sums
-            return threads <= tg::kNormThreads &&
-                   narrow(q.n.ldx, q.n.ldr, q.n.ldg, q.lddx, q.lddr) &&
-                   narrow(q.lddy, q.lddh, 0, 0, 0) &&
+            const int join = threads * 32;  // a group's column sums
+            // (the groups of a block would take rows in turn: one, where blocks share rows)
+            return narrow(q.n.ldx, q.n.ldr, q.n.ldg, q.lddx, q.lddr) &&
+                   narrow(q.lddy, q.lddh, 0, 0, 0) && (split == 1 || threads > tg::kNormThreads / 2) &&
                    plan_rows(a->rows, threads, stage + (one_gate ? 0 : gate),
                              bx + (tg::kNormThreads / threads > 1 ? join : 0), 1, dev.num_sms, &r);
         };
-        int ch = 0;  // columns of a thread / 8; 0: no ring fits
-        if (vec)
-            ch = plan(Int<1>{}, std::true_type{}) ? 1 : plan(Int<2>{}, std::true_type{}) ? 2 : 0;
-        else
-            ch = plan(Int<1>{}, std::false_type{}) ? 1 : plan(Int<2>{}, std::false_type{}) ? 2 : 0;
-        const int64_t most = ch != 0 ? dev.num_sms : 2 * dev.num_sms;
-        const int64_t wanted = ch != 0 ? (a->rows + r.groups - 1) / r.groups : a->rows;
+        const bool ring = vec ? plan(std::true_type{}) : plan(std::false_type{});
+        int64_t most = ring ? dev.num_sms : 2 * dev.num_sms;
+        if (ring && split > 1) {
+            const auto kernel = vec ? tg::tg_norm_grad_rows<TX, TR, true, true>
+                                    : tg::tg_norm_grad_rows<TX, TR, false, true>;
+            if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+            most = max_clusters(kernel, split, r.threads, r.smem, dev);
+            if (most < 1) return TG_ERR_LAUNCH;
+        }
+        const int64_t wanted = ring ? (a->rows + r.groups - 1) / r.groups : a->rows;
         const int64_t blocks = wanted < most ? wanted : most;
         // Many gates: a block takes whole gates.  Few: it takes rows, and the
         // blocks' shares of a gate are summed afterwards.
@@ -317,7 +358,7 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
         // (a thread of the row kernels sums its whole gates in registers)
         const int64_t gate_slots = !gate_sums                ? 0
                                    : !q.whole_gates ? blocks + q.gates
-                                   : ch != 0        ? 0
+                                   : ring           ? 0
                                                     : blocks;
         const int64_t slots = (q.dwpost != nullptr ? blocks : 0) +
                               (q.dwpre != nullptr ? blocks : 0) + gate_slots;
@@ -330,29 +371,31 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
             if (q.dwpre != nullptr) q.ws_pre = next, next += blocks * cols;
             if (gate_slots > 0) q.ws_gate = next;
         }
-        const dim3 grid(static_cast<unsigned>(blocks));
-        if (ch != 0) {
+        const dim3 grid(static_cast<unsigned>(ring ? blocks * split : blocks));
+        if (ring) {
             auto run = [&](auto kernel) {
                 if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
-                return launch(kernel, grid, r.threads * r.groups, r.smem, s, q, r.threads, r.stages,
-                              r.stage_bytes);
+                return launch(kernel, grid, r.threads * r.groups, r.smem, split, s, q, r.threads, r.stages,
+                              r.stage_bytes, split, part);
             };
-            st = vec ? (ch == 1 ? run(tg::tg_norm_grad_rows<TX, TR, 1, true>)
-                                : run(tg::tg_norm_grad_rows<TX, TR, 2, true>))
-                     : (ch == 1 ? run(tg::tg_norm_grad_rows<TX, TR, 1, false>)
-                                : run(tg::tg_norm_grad_rows<TX, TR, 2, false>));
+            if (split > 1)
+                st = vec ? run(tg::tg_norm_grad_rows<TX, TR, true, true>)
+                         : run(tg::tg_norm_grad_rows<TX, TR, false, true>);
+            else
+                st = vec ? run(tg::tg_norm_grad_rows<TX, TR, true, false>)
+                         : run(tg::tg_norm_grad_rows<TX, TR, false, false>);
         } else {
             auto kernel = tg::tg_norm_grad_simple<TX, TR>;
             const size_t smem = static_cast<size_t>(cols) * 4;
             if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
-            st = launch(kernel, grid, 256, smem, s, q);
+            st = launch(kernel, grid, 256, smem, 1, s, q);
         }
         if (st != TG_OK || slots == 0) return st;
-        const int64_t jobs = 2 + (q.whole_gates ? 0 : q.gates);
+        const int64_t jobs = 2 + (gate_sums && !q.whole_gates ? q.gates : 0);
         return launch(tg::tg_norm_grad_sum<TX>,
                       dim3(static_cast<unsigned>((cols + 31) / 32),
                            static_cast<unsigned>(jobs < 1024 ? jobs : 1024)),
-                      512, 0, s, q, blocks);
+                      512, 0, 1, s, q, blocks, jobs);
     });
 }
 

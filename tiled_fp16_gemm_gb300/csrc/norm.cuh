@@ -235,6 +235,7 @@ __device__ __forceinline__ void norm_commit() {
 }
 
 constexpr int kNormThreads = 512;  // of a block
+constexpr int kNormSplit = 8;      // blocks that share a row, at most
 
 // Until the oldest of the stages - 1 groups under way is there (2 to 4 stages).
 __device__ __forceinline__ void norm_wait(int stages) {
@@ -550,6 +551,56 @@ __global__ void __launch_bounds__(kNormThreads, CH == 1 && VEC ? 2 : 1)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+template <typename T>
+__device__ __forceinline__ const void* norm_at(const void* p, int col) {
+    return p != nullptr ? static_cast<const T*>(p) + col : nullptr;
+}
+
+// Sums of the blocks of a cluster, over distributed shared memory.  An exchange costs some
+// 0.85 us: the barrier's release waits for the stores of the row before.
+template <bool MULTI>
+struct NormPeers {
+    __device__ __forceinline__ NormPeers(int, int) {}
+    template <int N>
+    __device__ __forceinline__ void add(float (&)[N]) {}
+};
+template <>
+struct NormPeers<true> {
+    float* values;  // [2][block of the cluster][8]
+    int rank, count;
+    int turn = 0;  // one exchange's values are still read when the next one's are written
+
+    __device__ __forceinline__ NormPeers(int rank, int count) : rank(rank), count(count) {
+        __shared__ float room[2 * kNormSplit * 8];
+        values = room;
+        sync();  // the other blocks have begun
+    }
+    __device__ __forceinline__ static void sync() {
+        asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    }
+    // The blocks' v (the same in all threads of a block), in the order of the blocks.
+    template <int N>
+    __device__ __forceinline__ void add(float (&v)[N]) {
+        float* all = values + turn * kNormSplit * 8;
+        if (static_cast<int>(threadIdx.x) < count) {  // a thread for each block
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(to)
+                         : "r"(op_smem(all + rank * 8)), "r"(threadIdx.x));
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * k), "f"(v[k]) : "memory");
+        }
+        sync();
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = all[k];
+        for (int b = 1; b < count; ++b)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += all[b * 8 + k];
+        turn ^= 1;
+    }
+};
+
 // Gradient.  A thread keeps its columns' sums over its rows in registers; a block
 // joins its groups' sums in shared memory and writes one share.  Two reductions per
 // row: with t = o·g (so y = r + s·t) first Σ x² for rx, then
@@ -560,42 +611,58 @@ __global__ void __launch_bounds__(kNormThreads, CH == 1 && VEC ? 2 : 1)
 // whole_gates: a group takes all rows of its gates, and writes their gradients
 // itself.  Else the groups of a block take its rows in turn, and the block's share
 // of a gate's gradient is joined whenever a gate's rows end.
-template <typename TX, typename TR, int CH, bool VEC>
+//
+// MULTI: the `split` blocks of a cluster share their rows, `part` columns each (the last
+// one the rest), and add up their sums: for rows of more columns than a block's threads
+// have in registers (8 each; with 16 a thread's sums did not fit, and 2048 rows of 8192
+// columns took 107 us).
+template <typename TX, typename TR, bool VEC, bool MULTI>
 __global__ void __launch_bounds__(kNormThreads)
-    tg_norm_grad_rows(const NormGradParams q, int threads, int stages, int stage_bytes) {
+    tg_norm_grad_rows(const NormGradParams q, int threads, int stages, int stage_bytes, int split,
+                      int part) {
+    constexpr int CH = 1;
     extern __shared__ __align__(16) unsigned char norm_stage[];
     __shared__ __align__(16) float red[8 * 160];
     const NormParams& p = q.n;
     NormGroup g = norm_group(threads, red, 8 * 160);
-    const NormCols<CH, VEC> c{g.tid, g.threads, static_cast<int>(p.cols)};
+    const int rank = MULTI ? blockIdx.x % split : 0;
+    const int64_t block = MULTI ? blockIdx.x / split : blockIdx.x;
+    const int64_t blocks = MULTI ? gridDim.x / split : gridDim.x;
+    const int c0 = MULTI ? rank * part : 0;  // first column here
+    int cols = static_cast<int>(p.cols) - c0;
+    if (MULTI && cols > part) cols = part;
+    const NormCols<CH, VEC> c{g.tid, g.threads, cols};
+    NormPeers<MULTI> peers(rank, split);
+    const float* const wpost = p.wpost != nullptr ? p.wpost + c0 : nullptr;
+    const float* const wpre = p.wpre != nullptr ? p.wpre + c0 : nullptr;
     const float inv = 1.0f / static_cast<float>(p.cols);
     const int rows = static_cast<int>(p.rows), per = static_cast<int>(p.rows_per_gate);
     int row0, row1, stride = 1;
     if (q.whole_gates) {
-        const int64_t groups = int64_t{gridDim.x} * g.count;
-        const int64_t i = int64_t{blockIdx.x} * g.count + g.index;
+        const int64_t groups = blocks * g.count;
+        const int64_t i = block * g.count + g.index;
         row0 = static_cast<int>(norm_first_row(q.gates, groups, i)) * per;
         row1 = static_cast<int>(norm_first_row(q.gates, groups, i + 1)) * per;
     } else {
-        row0 = static_cast<int>(norm_first_row(rows, gridDim.x, blockIdx.x)) + g.index;
-        row1 = static_cast<int>(norm_first_row(rows, gridDim.x, blockIdx.x + 1));
+        row0 = static_cast<int>(norm_first_row(rows, blocks, block)) + g.index;
+        row1 = static_cast<int>(norm_first_row(rows, blocks, block + 1));
         stride = g.count;
     }
     unsigned char* mine = norm_stage + g.index * stages * stage_bytes;
     unsigned char* behind = norm_stage + g.count * stages * stage_bytes;  // the ring
-    const int bx = norm_stage_bytes<TX, CH, VEC>(threads, p.cols);
-    const int br = norm_stage_bytes<TR, CH, VEC>(threads, p.cols);
+    const int bx = norm_stage_bytes<TX, CH, VEC>(threads, MULTI ? part : p.cols);
+    const int br = norm_stage_bytes<TR, CH, VEC>(threads, MULTI ? part : p.cols);
     const bool one_gate = per == rows;
     NormInput<TX, CH, VEC> in_x, in_dh, in_g;
     NormInput<TR, CH, VEC> in_r, in_dy;
-    in_x.start(c, p.x, p.ldx, mine, stages, stage_bytes);
-    in_dh.start(c, q.dh, q.lddh, mine + bx, stages, stage_bytes);
-    in_r.start(c, p.r, p.ldr, mine + 2 * bx, stages, stage_bytes);
-    in_dy.start(c, q.dy, q.lddy, mine + 2 * bx + br, stages, stage_bytes);
+    in_x.start(c, norm_at<TX>(p.x, c0), p.ldx, mine, stages, stage_bytes);
+    in_dh.start(c, norm_at<TX>(q.dh, c0), q.lddh, mine + bx, stages, stage_bytes);
+    in_r.start(c, norm_at<TR>(p.r, c0), p.ldr, mine + 2 * bx, stages, stage_bytes);
+    in_dy.start(c, norm_at<TR>(q.dy, c0), q.lddy, mine + 2 * bx + br, stages, stage_bytes);
     if (one_gate)
-        in_g.start(c, p.gate, p.ldg, behind + g.index * bx, 1, 0);
+        in_g.start(c, norm_at<TX>(p.gate, c0), p.ldg, behind + g.index * bx, 1, 0);
     else
-        in_g.start(c, p.gate, p.ldg, mine + 2 * (bx + br), stages, stage_bytes);
+        in_g.start(c, norm_at<TX>(p.gate, c0), p.ldg, mine + 2 * (bx + br), stages, stage_bytes);
     int to_fetch = row0;
     auto fetch = [&](int slot) {
         if (to_fetch < row1) {
@@ -614,12 +681,9 @@ __global__ void __launch_bounds__(kNormThreads)
     if (one_gate) in_g.fetch(c, 0, 0);
     for (int s = 0; s < stages - 1; ++s) fetch(s);
 
-    constexpr bool kHold = CH == 1;  // weights and the row's values in registers
-    F2 held_post[4], held_pre[4];
-    if (kHold) {
-        norm_weight<CH, VEC>(p.wpost, c, 0, held_post);
-        norm_weight<CH, VEC>(p.wpre, c, 0, held_pre);
-    }
+    F2 wo[4], wp[4];
+    norm_weight<CH, VEC>(wpost, c, 0, wo);
+    norm_weight<CH, VEC>(wpre, c, 0, wp);
     F2 sum_post[CH][4], sum_pre[CH][4], sum_gate[CH][4];
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch)
@@ -684,23 +748,18 @@ __global__ void __launch_bounds__(kNormThreads)
                 for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) a = f2_fma(x[ch][i], x[ch][i], a);
-                rx = rsqrtf(g.sum(f2_sum(a)) * inv + p.eps);
+                float v[1] = {g.sum(f2_sum(a))};
+                peers.add(v);
+                rx = rsqrtf(v[0] * inv + p.eps);
             }
             const F2 rx2 = f2(rx, rx);
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch)  // m from here on
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[ch][i] = f2_mul(x[ch][i], rx2);
-            F2 y[4], dy[4], dh[4], gt[4], wo[4], wp[4];
-            // a chunk's inputs and weights, and y
+            F2 y[4], dy[4], dh[4], gt[4];
+            // a chunk's inputs, and y
             auto chunk = [&](int ch) {
-                if (kHold) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) wo[i] = held_post[i], wp[i] = held_pre[i];
-                } else {
-                    norm_weight<CH, VEC>(p.wpost, c, ch, wo);
-                    norm_weight<CH, VEC>(p.wpre, c, ch, wp);
-                }
                 in_g.get(c, gate_at, gate_row, ch, gt, 1.0f);
                 in_r.get(c, at, row, ch, y);
                 in_dy.get(c, at, row, ch, dy);
@@ -730,6 +789,7 @@ __global__ void __launch_bounds__(kNormThreads)
                 for (int k = 0; k < 5; ++k) s[k] = f2_sum(a[k]);
             }
             g.sum5(s);
+            peers.add(s);
             const float ry = in_dh.base != nullptr ? rsqrtf(s[0] * inv + p.eps) : 0.0f;
             const float cy = ry * ry * s[1] * inv;
             // -mean(dm·m) · rx: what dx gets of m
@@ -741,12 +801,11 @@ __global__ void __launch_bounds__(kNormThreads)
                 q.dgate != nullptr && q.ws_gate == nullptr &&
                 (row + stride >= row1 || norm_gate_row(row + stride, per) != gate_row);
             TX* out_x = static_cast<TX*>(q.dx) +
-                        static_cast<uint64_t>(row) * static_cast<uint32_t>(q.lddx);
+                        static_cast<uint64_t>(row) * static_cast<uint32_t>(q.lddx) + c0;
             TR* out_r = static_cast<TR*>(q.dr) +
-                        static_cast<uint64_t>(row) * static_cast<uint32_t>(q.lddr);
+                        static_cast<uint64_t>(row) * static_cast<uint32_t>(q.lddr) + c0;
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
-                if (!kHold) chunk(ch);
                 F2 dx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -763,7 +822,7 @@ __global__ void __launch_bounds__(kNormThreads)
                 if (own_gate) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dx[i] = f2_mul(sum_gate[ch][i], scale2);
-                    c.store(static_cast<TX*>(q.dgate) + gate_row * q.lddg, ch, dx);
+                    c.store(static_cast<TX*>(q.dgate) + gate_row * q.lddg + c0, ch, dx);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sum_gate[ch][i] = 0;
                 }
@@ -771,7 +830,7 @@ __global__ void __launch_bounds__(kNormThreads)
             slot = slot + 1 == stages ? 0 : slot + 1;
         }
         if (q.ws_gate != nullptr) {
-            join(sum_gate, q.ws_gate + (int64_t{blockIdx.x} + gate_no) * p.cols, p.scale);
+            join(sum_gate, q.ws_gate + (block + gate_no) * p.cols + c0, p.scale);
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
@@ -780,8 +839,8 @@ __global__ void __launch_bounds__(kNormThreads)
         first = end;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (q.ws_post != nullptr) join(sum_post, q.ws_post + blockIdx.x * p.cols, p.scale);
-    if (q.ws_pre != nullptr) join(sum_pre, q.ws_pre + blockIdx.x * p.cols, 1.0f);
+    if (q.ws_post != nullptr) join(sum_post, q.ws_post + block * p.cols + c0, p.scale);
+    if (q.ws_pre != nullptr) join(sum_pre, q.ws_pre + block * p.cols + c0, 1.0f);
 }
 
 // ------------------------------------------------------------------ any width
@@ -937,15 +996,15 @@ __device__ __forceinline__ int64_t norm_block_of(int64_t rows, int64_t blocks, i
 // warps with every 16th share each, 8 of them under way at a time.
 template <typename TX>
 __global__ void __launch_bounds__(512)
-    tg_norm_grad_sum(const NormGradParams q, int64_t blocks) {
+    tg_norm_grad_sum(const NormGradParams q, int64_t blocks, int64_t jobs) {
     __shared__ float part[16][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     op_release_next();
     op_wait_previous();
     const int64_t c = int64_t{blockIdx.x} * 32 + lane;
-    for (int64_t job = blockIdx.y; job < 2 + q.gates; job += gridDim.y) {
+    for (int64_t job = blockIdx.y; job < jobs; job += gridDim.y) {
         const float* src = job == 0 ? q.ws_post : job == 1 ? q.ws_pre : q.ws_gate;
-        if (src == nullptr || (job >= 2 && q.whole_gates)) continue;
+        if (src == nullptr) continue;
         int64_t lo = 0, hi = blocks;
         if (job >= 2) {  // gate i: slots block + i of the blocks that have its rows
             const int64_t i = job - 2, per = q.n.rows_per_gate;
