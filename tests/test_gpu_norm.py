@@ -92,6 +92,25 @@ def test_long_rows(tg, cols, pad, rows, gates):
     check(tg, rows, cols, torch.float16, torch.float16, gates=gates, pad=pad, post=rows != 300)
 
 
+@pytest.mark.parametrize("rows,gates", [(1, 1), (6, 0), (6, 3)])
+def test_plain_and_general_calls_agree(tg, rows, gates):
+    """A call whose results are given takes another way through the binding: the same bits."""
+    x, kept, dy, dh = make(rows, 520, torch.bfloat16, torch.float32, gates=gates)
+    y, h = tg.norm_residual(x, **kept)
+    other = tg.norm_residual(x, out=torch.empty_like(y), normed=torch.empty_like(h), **kept)
+    assert torch.equal(y, other[0]) and torch.equal(h, other[1])
+    grads = tg.norm_residual_backward(dy, dh, x, **kept)
+    assert isinstance(grads, tg.NormGrads)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for a, b in zip(grads, tg.norm_residual_backward(dy, dh, x, stream=stream, **kept)):
+        stream.synchronize()
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+    weight = torch.nn.Parameter(kept["pre_weight"])
+    again = tg.norm_residual(x, **dict(kept, pre_weight=weight))
+    assert torch.equal(again[1], h) and not again[1].requires_grad
+
+
 @pytest.mark.parametrize("residual", [True, False])
 @pytest.mark.parametrize("post", [True, False])
 @pytest.mark.parametrize("gates", [0, 1])

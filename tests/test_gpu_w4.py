@@ -152,6 +152,17 @@ def test_fp32_results_round_no_weight(tg, M, dtype, group, zeros):
     ops64.assert_close(c, want, bound, f"{M} {dtype} {group}")
 
 
+@pytest.mark.parametrize("out_dtype", [None, torch.float32])
+def test_plain_and_general_calls_agree(tg, out_dtype):
+    """A call whose result is given takes another way through the binding: the same bits."""
+    a, bq, bscale, bzero = make(3, 200, 300, HALF, 64, True)
+    b, r = torch.randn(200, device="cuda"), torch.randn(3, 200, device="cuda").half()
+    kw = dict(relu=True, bzero=bzero, bias=b, residual=r)
+    c = tg.gemm_w4(a, bq, bscale, 200, 64, out_dtype=out_dtype, **kw)
+    assert c.dtype is (out_dtype or HALF) and c.shape == (3, 200)
+    assert torch.equal(c, tg.gemm_w4(a, bq, bscale, 200, 64, out=torch.empty_like(c), **kw))
+
+
 def test_batches_of_changing_shapes(tg):
     """One stream's workspace serves every shape: what one call leaves there does not
     show in the next."""

@@ -521,16 +521,24 @@ def gemm_sp24(ac, e, b, relu: bool = False, out=None, stream=None, *, bias=None,
 
 
 # The operators below are also called for single tokens, where this binding's own
-# time counts: each tensor is looked at once, with few attribute reads.
+# time counts.  A plain call (current stream of the current device, results to be made)
+# is checked and made by csrc/calls.cpp; what that does not take comes here, where each
+# tensor is looked at once, with few attribute reads.
 
 _torch = None
+_plain = None
 
 
 def _bind():
     """torch, and what of it the operators call for every launch."""
-    global _torch, _DTYPES, _get_device, _raw_stream
+    global _torch, _DTYPES, _get_device, _raw_stream, _plain
     if _torch is None:
         import torch
+        lib = _L()
+        from . import _calls as calls  # built with libtgemm.so; no fallback if it is missing
+        calls.bind(*(ctypes.cast(f, _vp).value for f in
+                     (lib.tg_gemm_w4, lib.tg_norm_residual, lib.tg_norm_residual_backward)), NormGrads)
+        _plain = calls
         _DTYPES = {torch.float16: TG_DTYPE_F16, torch.bfloat16: TG_DTYPE_BF16,
                    torch.float32: TG_DTYPE_F32}
         _get_device = torch.cuda.current_device
@@ -538,8 +546,14 @@ def _bind():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch = torch
-        _L()
     return _torch
+
+
+def _made(result, name: str):
+    """What a native call made; a status it returned is raised."""
+    if type(result) is int:
+        raise TgemmError(result, name)
+    return result
 
 
 def _matrix(t, name: str, dtype, rows: int, cols: int, index: int):
@@ -607,6 +621,10 @@ def gemm_w4(a, bq, bscale, N: int, group: int, relu: bool = False, out=None, str
     residual, out_dtype, out and stream as for ``gemm``.
     """
     torch = _torch or _bind()
+    if out is None and stream is None:
+        made = _plain.gemm_w4(a, bq, bscale, N, group, relu, bzero, bias, residual, out_dtype)
+        if made is not None:
+            return _made(made, "tg_gemm_w4")
     try:
         dtype = a.dtype
         M, K = a.shape
@@ -646,13 +664,6 @@ def gemm_w4(a, bq, bscale, N: int, group: int, relu: bool = False, out=None, str
     pr, ldr = _matrix(residual, "residual", dtype, M, N, index) if residual is not None else (None, 0)
     code = _DTYPES[dtype]
     epi = tg_epilogue_ex_t(1 if relu else 0, _DTYPES[out_dtype], pb, pr, ldr)
-    if out is None and stream is None and index == _get_device():
-        c = torch.empty((M, N), dtype=out_dtype, device=a.device)
-        st = _lib.tg_gemm_w4(code, pa, pq, ps, pz, c.data_ptr(), M, N, K, group, lda, ldq, lds, ldz,
-                             N, ctypes.byref(epi), _raw_stream(index))
-        if st != TG_OK:
-            raise TgemmError(st, "tg_gemm_w4")
-        return c
 
     def body(s):
         c = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
@@ -734,6 +745,12 @@ def norm_residual(x, residual=None, *, post_weight=None, gate=None, scale: float
     be ``residual`` itself) and h to ``normed`` where given.  Runs on ``stream``
     (default: torch's current stream of x's device).
     """
+    if _torch is None:
+        _bind()
+    if out is None and normed is None and stream is None:
+        made = _plain.norm_residual(x, residual, post_weight, gate, scale, pre_weight, eps)
+        if made is not None:
+            return _made(made, "tg_norm_residual")
     n, rows, cols, dtype, kind, index = _norm_args(x, residual, post_weight, gate, scale,
                                                    pre_weight, eps)
     torch = _torch
@@ -787,6 +804,13 @@ def norm_residual_backward(dy, dh, x, residual=None, *, post_weight=None, gate=N
     input's dtype and shape.  x and residual are those of the forward call: no
     ``out`` may have been written over them.
     """
+    if _torch is None:
+        _bind()
+    if stream is None:
+        made = _plain.norm_residual_backward(dy, dh, x, residual, post_weight, gate, scale,
+                                             pre_weight, eps)
+        if made is not None:
+            return _made(made, "tg_norm_residual_backward")
     n, rows, cols, dtype, kind, index = _norm_args(x, residual, post_weight, gate, scale,
                                                    pre_weight, eps)
     torch = _torch
