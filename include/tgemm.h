@@ -499,7 +499,8 @@ void tg_debug_set_wait_timeout_ns(uint64_t ns);
 /* mode 1: the next persistent/skinny launch withholds its first
  * "accumulator ready" signal, so its epilogue waits out the timeout and the
  * kernel returns early with TG_ERR_TIMEOUT recorded.  (tg_gemm_w4's kernels
- * withhold their first fetch of codes instead.)  mode 0: off.  The
+ * withhold their first fetch of codes instead; tg_norm_residual_backward, where
+ * blocks share rows, one block's first sums.)  mode 0: off.  The
  * setting applies to exactly one launch. */
 void tg_debug_inject(int32_t mode);
 

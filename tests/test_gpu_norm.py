@@ -92,6 +92,28 @@ def test_long_rows(tg, cols, pad, rows, gates):
     check(tg, rows, cols, torch.float16, torch.float16, gates=gates, pad=pad, post=rows != 300)
 
 
+def test_a_wait_for_another_block_that_runs_out_is_reported_once(tg):
+    """Values that are not sent: the gradient's kernel gives up within its limit and
+    returns, the status says so once, and the next call is right."""
+    x, kept, dy, dh = make(3, 9000, torch.bfloat16, torch.bfloat16)
+    want = tg.norm_residual_backward(dy, dh, x, **kept)
+    tg.sync_status()
+    try:
+        tg.tg_debug_set_wait_timeout_ns(20_000_000)
+        tg.tg_debug_inject(1)
+        tg.norm_residual_backward(dy, dh, x, **kept)
+        with pytest.raises(tg.TgemmError) as e:
+            tg.sync_status()
+        assert e.value.status == tg.TG_ERR_TIMEOUT
+        tg.sync_status()
+    finally:
+        tg.tg_debug_inject(0)
+        tg.tg_debug_set_wait_timeout_ns(0)
+    for a, b in zip(tg.norm_residual_backward(dy, dh, x, **kept), want):
+        assert torch.equal(a, b)
+    tg.sync_status()
+
+
 @pytest.mark.parametrize("rows,gates", [(1, 1), (6, 0), (6, 3)])
 def test_plain_and_general_calls_agree(tg, rows, gates):
     """A call whose results are given takes another way through the binding: the same bits."""

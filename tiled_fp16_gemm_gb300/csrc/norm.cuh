@@ -240,6 +240,7 @@ __device__ __forceinline__ void norm_commit() {
 
 constexpr int kNormThreads = 512;  // of a block
 constexpr int kNormSplit = 8;      // blocks that share a row, at most
+__device__ unsigned int g_norm_timeouts;  // not 0: a wait for another block ran out
 
 // Until the oldest of the stages - 1 groups under way is there (2 to 4 stages).
 __device__ __forceinline__ void norm_wait(int stages) {
@@ -560,24 +561,40 @@ __device__ __forceinline__ const void* norm_at(const void* p, int col) {
     return p != nullptr ? static_cast<const T*>(p) + col : nullptr;
 }
 
-// Sums of the blocks of a cluster, over distributed shared memory.  An exchange costs some
-// 0.85 us: the barrier's release waits for the stores of the row before.
+// Sums of the blocks of a cluster, over distributed shared memory: each block's values go
+// to every block with their bytes counted on its mbarrier.  By the rows' times an exchange
+// takes some 0.65 us; with cluster barriers, whose release waits for the stores of the row
+// before, 0.85 (2048×8192 bf16 92 us against 104).
 template <bool MULTI>
 struct NormPeers {
-    __device__ __forceinline__ NormPeers(int, int) {}
+    __device__ __forceinline__ NormPeers(int, int, uint64_t, bool) {}
     template <int N>
     __device__ __forceinline__ void add(float (&)[N]) {}
+    __device__ __forceinline__ void end() {}
 };
 template <>
 struct NormPeers<true> {
     float* values;  // [2][block of the cluster][8]
+    uint32_t bars;  // [2]
     int rank, count;
-    int turn = 0;  // one exchange's values are still read when the next one's are written
+    uint64_t limit_ns;
+    bool silent;          // for tests of the limit: the first values are not sent
+    bool lost = false;    // a wait ran out: reported; nothing more is sent or waited for
+    int turn = 0;         // one exchange's values are still read when the next one's come
+    uint32_t parity = 0;  // of both barriers
 
-    __device__ __forceinline__ NormPeers(int rank, int count) : rank(rank), count(count) {
-        __shared__ float room[2 * kNormSplit * 8];
+    __device__ __forceinline__ NormPeers(int rank, int count, uint64_t limit_ns, bool silent)
+        : rank(rank), count(count), limit_ns(limit_ns), silent(silent) {
+        __shared__ __align__(16) float room[2 * kNormSplit * 8];
+        __shared__ __align__(8) unsigned long long two[2];
         values = room;
-        sync();  // the other blocks have begun
+        bars = op_smem(two);
+        if (threadIdx.x == 0) {
+            op_bar_init(bars, 1);
+            op_bar_init(bars + 8, 1);
+            op_bar_init_done();
+        }
+        sync();  // the other blocks' barriers are there
     }
     __device__ __forceinline__ static void sync() {
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -586,23 +603,36 @@ struct NormPeers<true> {
     template <int N>
     __device__ __forceinline__ void add(float (&v)[N]) {
         float* all = values + turn * kNormSplit * 8;
-        if (static_cast<int>(threadIdx.x) < count) {  // a thread for each block
-            uint32_t to;
+        const uint32_t bar = bars + 8 * turn;
+        if (threadIdx.x == 0 && !lost) op_bar_expect(bar, count * N * 4);
+        if (static_cast<int>(threadIdx.x) < count && !silent && !lost) {  // a thread for each block
+            uint32_t to, at;
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                          : "=r"(to)
                          : "r"(op_smem(all + rank * 8)), "r"(threadIdx.x));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(bar), "r"(threadIdx.x));
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * k), "f"(v[k]) : "memory");
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(to + 4 * k),
+                    "f"(v[k]), "r"(at)
+                    : "memory");
         }
-        sync();
+        silent = false;
+        if (!lost && !op_bar_wait(bar, parity, limit_ns)) {
+            lost = true;
+            atomicOr(&g_norm_timeouts, 1u);
+        }
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = all[k];
         for (int b = 1; b < count; ++b)
 #pragma unroll
             for (int k = 0; k < N; ++k) v[k] += all[b * 8 + k];
         turn ^= 1;
+        if (turn == 0) parity ^= 1;
     }
+    // No block leaves while another's values may be on their way to it.
+    __device__ __forceinline__ void end() { sync(); }
 };
 
 // Gradient.  A thread keeps its columns' sums over its rows in registers; a block
@@ -618,7 +648,8 @@ struct NormPeers<true> {
 //
 // Bound by issue and by the reductions' latency, one block of 512 threads on an SM: its
 // registers hold the sums.  8192×4096 bf16 112 us (3.6 TB/s), fp32 stream 131 us (4.6);
-// 1021×5119 fp16, unaligned, a gate per row, 73 us; 2048×16000 bf16 217 us.
+// 1021×5119 fp16, unaligned, a gate per row, 62 us; 2048×8192 and 2048×16000 bf16 92 and
+// 194 us.
 //
 // MULTI: the `split` blocks of a cluster share their rows, `part` columns each (the last
 // one the rest), and add up their sums: for rows of more columns than a block's threads
@@ -627,7 +658,7 @@ struct NormPeers<true> {
 template <typename TX, typename TR, bool VEC, bool MULTI>
 __global__ void __launch_bounds__(kNormThreads)
     tg_norm_grad_rows(const NormGradParams q, int threads, int stages, int stage_bytes, int split,
-                      int part) {
+                      int part, uint64_t limit_ns, int inject) {
     constexpr int CH = 1;
     extern __shared__ __align__(16) unsigned char norm_stage[];
     __shared__ __align__(16) float red[8 * 160];
@@ -640,7 +671,7 @@ __global__ void __launch_bounds__(kNormThreads)
     int cols = static_cast<int>(p.cols) - c0;
     if (MULTI && cols > part) cols = part;
     const NormCols<CH, VEC> c{g.tid, g.threads, cols};
-    NormPeers<MULTI> peers(rank, split);
+    NormPeers<MULTI> peers(rank, split, limit_ns, inject == 1 && blockIdx.x == 1);
     const float* const wpost = p.wpost != nullptr ? p.wpost + c0 : nullptr;
     const float* const wpre = p.wpre != nullptr ? p.wpre + c0 : nullptr;
     const float inv = 1.0f / static_cast<float>(p.cols);
@@ -849,13 +880,14 @@ __global__ void __launch_bounds__(kNormThreads)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (q.ws_post != nullptr) join(sum_post, q.ws_post + block * p.cols + c0, p.scale);
     if (q.ws_pre != nullptr) join(sum_pre, q.ws_pre + block * p.cols + c0, 1.0f);
+    peers.end();
 }
 
 // ------------------------------------------------------------------ any width
 //
 // What the rings do not hold: a forward row of more than 16384 columns, or of fp32 values
 // that do not fit twice; strides of 2^32 elements; 2^31 rows.  Values are read again for
-// each pass, from L2 (2048×16000 bf16, gradient: 1.8 ms, 217 us by the rings).
+// each pass, from L2 (2048×16000 bf16, gradient: 1.8 ms, 194 us by the rings).
 
 // Row by row, the unrounded y of the row in shared memory.
 template <typename TX, typename TR>

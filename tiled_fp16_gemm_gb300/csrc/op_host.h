@@ -57,9 +57,10 @@ uint64_t op_wait_limit_ns();
 // The mode that tg_debug_inject set for the next launch, which is then 0 again.
 int32_t op_take_inject();
 
-// Whether a kernel of w4.cu gave up on a wait since the last call, on the current
-// device, which has to be idle.
+// Whether a kernel of w4.cu or norm.cu gave up on a wait since the last call, on the
+// current device, which has to be idle.
 bool w4_take_timeout();
+bool norm_take_timeout();
 
 // The 2-D tensor map of rows of `inner` elements, `row_bytes` apart, read in boxes of
 // box_inner × box_outer; zero outside.

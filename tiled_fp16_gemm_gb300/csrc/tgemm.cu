@@ -1297,9 +1297,11 @@ tg_status_t tg_sync_status(void* stream) {
         noalloc_reset_counters(dev);
         cudaGetLastError();
         tg::w4_take_timeout();
+        tg::norm_take_timeout();
         return TG_ERR_TIMEOUT;
     }
-    return tg::w4_take_timeout() ? TG_ERR_TIMEOUT : TG_OK;
+    const bool w4 = tg::w4_take_timeout(), norm = tg::norm_take_timeout();
+    return w4 || norm ? TG_ERR_TIMEOUT : TG_OK;
 }
 
 }  // extern "C"
