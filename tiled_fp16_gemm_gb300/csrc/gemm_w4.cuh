@@ -502,6 +502,18 @@ __device__ __forceinline__ uint32_t w4_scale(uint32_t v, __nv_bfloat16 s) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// What the rounding to `high` = v·s left, exactly.
+__device__ __forceinline__ uint32_t w4_scale_rest(uint32_t v, __half s, uint32_t high) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), __half2half2(s),
+                              __hneg2(*reinterpret_cast<const __half2*>(&high)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t w4_scale_rest(uint32_t v, __nv_bfloat16 s, uint32_t high) {
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v), __bfloat162bfloat162(s),
+                                     __hneg2(*reinterpret_cast<const __nv_bfloat162*>(&high)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // W as a K×N matrix of T (row stride ldo, a multiple of 8), for the dense GEMM
 // on very many rows of A.  Here (code - zero)·scale is rounded to T, as the tensor
 // cores read 16-bit operands: at most half an ulp of each weight, an error of

@@ -1,5 +1,5 @@
-// Products of many rows of A with 4-bit weights and a 16-bit result, on tcgen05: W·Aᵀ
-// with W decoded into tensor memory, each weight rounded to T.
+// Products of many rows of A with 4-bit weights, on tcgen05: W·Aᵀ with W decoded into
+// tensor memory, for a 16-bit result each weight rounded to T.
 //
 // As in gemm_w4_tc.cuh the weights are the MMA's A operand (units of 128 rows of W by
 // 128 k), decoded by threads that own a row.  Here (code - z) · s is rounded to T before
@@ -7,6 +7,11 @@
 // each weight, below that of a 16-bit result's rounding for all but cancelling sums.  So
 // one accumulator of up to 256 tokens runs over the whole of k, and the MMAs (1024 cycles
 // a unit at 256 tokens) hide the decoding (some 270 instructions of each scheduler).
+//
+// EXACT, for an fp32 result: the rounding's error, (code - z) · s minus the rounded value,
+// is a T too (the product has 15 bits at most, its last place that of s or above), and one
+// fused multiplication and addition gives it.  It is the operand of a second set of MMAs on
+// the same tokens, so no weight is rounded; units take two places in tensor memory.
 //
 // The blocks work in pairs (cta_group::2): the MMA takes 256 rows of W, 128 in each block's
 // tensor memory, and half of the tokens from each block's shared memory.  With blocks of
@@ -18,6 +23,8 @@
 // Measured, 16384×8192, fp16, G = 128: 65 / 128 / 256 / 512 / 2048 rows 34 / 35 / 45 / 85 /
 // 329 us; the last two are 1600 and 1670 TFLOP/s.  (Decoding to memory, then the dense GEMM:
 // 160 us for 256 rows, 193 for 512.)  At 512 rows 64 of the 76 pairs work, on whole tiles.
+// With an fp32 result 65 / 128 / 256 / 512 rows 40 / 44 / 80 / 147 us (by passes of 64 rows
+// through gemm_w4_tc.cuh 62 / 84 / 170 / 340).
 //
 // Roles of a block's 24 warps (all meet on mbarriers):
 //   0             fetches codes, scales and zero points by TMA
@@ -78,14 +85,16 @@ __device__ __forceinline__ void wide_tma(uint32_t dst, const void* map, uint32_t
         : "memory");
 }
 
-// The MMAs of a unit, then the commits, to `done` and `free` of both blocks.  As tc_unit,
-// with one accumulator; `box`: the second 64 k of b, in 16 bytes.
+// The MMAs of a unit, then (LAST) the commits, to `done` and `free` of both blocks.  As
+// tc_unit, with one accumulator; `box`: the second 64 k of b, in 16 bytes.
+template <bool LAST>
 __device__ __forceinline__ void wide_unit(uint32_t d, uint32_t a, uint64_t b, uint32_t box, uint32_t idesc,
                                           uint32_t add, uint32_t done, uint32_t free) {
     asm volatile(
-        "{\n\t.reg .pred e, first, one;\n\t.reg .b32 ak;\n\t.reg .b64 bk, bx;\n\t"
+        "{\n\t.reg .pred e, first, one, last;\n\t.reg .b32 ak;\n\t.reg .b64 bk, bx;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 one, 0, 0;\n\t"
+        "setp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 one, 0, 0;\n\tsetp.ne.b32 last, %9, 0;\n\t"
+        "and.pred last, last, e;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %4, first;\n\t"
         "add.u32 ak, %1, 8;\n\tadd.u64 bk, %2, 2;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
@@ -101,12 +110,12 @@ __device__ __forceinline__ void wide_unit(uint32_t d, uint32_t a, uint64_t b, ui
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
         "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 56;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        "@last tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%6], %8;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        "@last tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%7], %8;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(box), "r"(idesc), "r"(add), "r"(done), "r"(free),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3)), "n"(LAST ? 1 : 0)
         : "memory");
 }
 
@@ -135,7 +144,7 @@ __device__ __forceinline__ P* wide_step(P* p, int64_t n) {
     return r;
 }
 // Epilogue and store of 16 tokens of row n, `most` of them.
-template <typename T>
+template <typename T, typename TC>
 __device__ __forceinline__ void wide_store(const W4Params& p, int64_t m, int64_t n, int most, float bias,
                                            float (&v)[16]) {
 #pragma unroll
@@ -151,20 +160,22 @@ __device__ __forceinline__ void wide_store(const W4Params& p, int64_t m, int64_t
             r = wide_step(r, 2 * p.ldr);
         }
     }
-    char* c = static_cast<char*>(p.C) + 2 * (m * p.ldc + n);
+    char* c = static_cast<char*>(p.C) + sizeof(TC) * (m * p.ldc + n);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        if (i < most) *reinterpret_cast<T*>(c) = op_round<T>(v[i]);
-        c = wide_step(c, 2 * p.ldc);
+        if (i < most) *reinterpret_cast<TC*>(c) = op_round<TC>(v[i]);
+        c = wide_step(c, sizeof(TC) * p.ldc);
     }
 }
 
-template <typename T, int G, bool ZERO>
+template <typename T, int G, bool ZERO, bool EXACT>
 __global__ void __launch_bounds__(kWideThreads, 1)
     tg_gemm_w4_wide(const __grid_constant__ WideLaunch q, const __grid_constant__ CUtensorMap codes,
                     const __grid_constant__ CUtensorMap scales, const __grid_constant__ CUtensorMap zeros,
                     const __grid_constant__ CUtensorMap order) {
     constexpr int kGroups = kTcK / G;
+    constexpr int kABufs = EXACT ? 2 : 4, kACols = 256 / kABufs;
+    using TC = typename std::conditional<EXACT, float, T>::type;
     extern __shared__ __align__(1024) unsigned char wide_dynamic[];
     const W4Params& p = q.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t bars = cs + kWideStages * kWideCodeBytes;
     const uint32_t c_full = bars, c_empty = c_full + 8 * kWideStages;
     const uint32_t x_full = c_empty + 8 * kWideStages, x_empty = x_full + 8 * kWideXStages;
-    const uint32_t a_full = x_empty + 8 * kWideXStages, done = a_full + 8 * kTcABufs;
+    const uint32_t a_full = x_empty + 8 * kWideXStages, done = a_full + 8 * kABufs;
     const uint32_t d_full = done + 8 * kTcDone, d_empty = d_full + 8;
     unsigned char* after = shared + (d_empty + 8 - base);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             op_bar_init(x_full + 8 * i, 1);  // of the even block: both blocks' copies
             op_bar_init(x_empty + 8 * i, 1);
         }
-        for (int i = 0; i < kTcABufs; ++i) op_bar_init(a_full + 8 * i, 8);  // of the even block
+        for (int i = 0; i < kABufs; ++i) op_bar_init(a_full + 8 * i, 8);  // of the even block
         for (int i = 0; i < kTcDone; ++i) op_bar_init(done + 8 * i, 1);
         op_bar_init(d_full, 1);
         op_bar_init(d_empty, 16);  // of the even block
@@ -210,7 +221,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_after_sync();
     // all columns are this block's, so they begin at 0
     constexpr uint32_t tmem = 0;
-    constexpr uint32_t d_cols = tmem + 64 * kTcABufs;
+    constexpr uint32_t d_cols = tmem + 256;
 
     const int64_t grains = q.units / q.grain;
     const int64_t u0 = tc_first(grains, q.clusters, cluster_no) * q.grain;
@@ -286,14 +297,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                (static_cast<uint32_t>(q.tokens >> 3) << 17) | (16u << 24);
         int issued = 0, tiles = 0;
         for (int i = 0; rank == 0 && i < n_units; ++i) {
-            const int s = i % kWideXStages, a = i % kTcABufs;
+            const int s = i % kWideXStages, a = i % kABufs;
             const bool first = i == 0 || kb == 0;
             if (!wait(x_full + 8 * s, i / kWideXStages & 1)) break;
             if (first && tiles++ > 0 && !wait(d_empty, tiles & 1)) break;
-            if (!wait(a_full + 8 * a, i / kTcABufs & 1)) break;
+            if (!wait(a_full + 8 * a, i / kABufs & 1)) break;
             tc_after_sync();
-            wide_unit(d_cols, tmem + 64 * a, tc_desc(xs + s * kWideXBytes), q.tokens / 2 * 128 / 16, idesc,
-                      first ? 0 : 1, done + 8 * (i % kTcDone), x_empty + 8 * s);
+            const uint64_t x = tc_desc(xs + s * kWideXBytes);
+            wide_unit<!EXACT>(d_cols, tmem + kACols * a, x, q.tokens / 2 * 128 / 16, idesc, first ? 0 : 1,
+                              done + 8 * (i % kTcDone), x_empty + 8 * s);
+            if (EXACT)
+                wide_unit<true>(d_cols, tmem + kACols * a + 64, x, q.tokens / 2 * 128 / 16, idesc, 1,
+                                done + 8 * (i % kTcDone), x_empty + 8 * s);
             if (kb + 1 == q.k_units || i + 1 == n_units) wide_commit(d_full);
             issued = i + 1;
             next_unit();
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         for (int i = group; i < n_units; i += kTcGroups) {
-            const int s = i % kWideStages, a = i % kTcABufs;
+            const int s = i % kWideStages, a = i % kABufs;
             if (!wait(c_full + 8 * s, i / kWideStages & 1)) break;
             const uint32_t at = cs + s * kWideCodeBytes;
             uint4 w[4];
@@ -322,22 +337,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                                        (c * kTcRows + row) * 2);
                 z[c] = ZERO ? shared[at - base + kWideZeroAt + c * kTcRows + row] & 15u : 8u;
             }
-            const int old = i - kTcABufs;
+            const int old = i - kABufs;
             if (old >= 0 && !wait(done + 8 * (old % kTcDone), old / kTcDone & 1)) break;
             tc_after_sync();
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const W4Decode<T> decode(z[c * 32 / G]);
                 const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-                uint32_t r[16];
+                uint32_t r[16], low[16];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t v[4];
                     decode(words[j], v);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[4 * j + e] = w4_scale(v[e], scale[c * 32 / G]);
+                    for (int e = 0; e < 4; ++e) {
+                        r[4 * j + e] = w4_scale(v[e], scale[c * 32 / G]);
+                        if (EXACT) low[4 * j + e] = w4_scale_rest(v[e], scale[c * 32 / G], r[4 * j + e]);
+                    }
                 }
-                tc_store16(tmem + lanes + 64 * a + 16 * c, r);
+                tc_store16(tmem + lanes + kACols * a + 16 * c, r);
+                if (EXACT) tc_store16(tmem + lanes + kACols * a + 64 + 16 * c, low);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before_sync();
@@ -376,7 +395,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     float v[16];
 #pragma unroll
                     for (int m = 0; m < 16; ++m) v[m] = __uint_as_float(r[m]);
-                    if (n < p.N) wide_store<T>(p, m0 + c, n, tokens - c, bias, v);
+                    if (n < p.N) wide_store<T, TC>(p, m0 + c, n, tokens - c, bias, v);
                 } else {
 #pragma unroll
                     for (int m = 0; m < 16; m += 4)
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 for (int m = 0; m < 16; ++m) sum[m] += w[m];
                             }
                         }
-                        if (n < p.N) wide_store<T>(p, m0 + c, n, tokens - c, bias, sum);
+                        if (n < p.N) wide_store<T, TC>(p, m0 + c, n, tokens - c, bias, sum);
                     }
                 }
             }

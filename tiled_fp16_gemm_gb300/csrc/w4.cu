@@ -275,7 +275,8 @@ double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
     double least = 1e300;
     for (int32_t tokens = 32; tokens <= tg::kWideTokens; tokens += 32) {
         const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
-        const double unit = tokens < 180 ? 0.43 : 0.0024 * tokens;
+        const double mma = 0.0024 * tokens * (p.out_f32 ? 2 : 1);
+        const double unit = mma < 0.43 ? 0.43 : mma;
         for (const int32_t grain : {q->k_units, 1}) {
             const int64_t grains = tiles * q->k_units / grain;
             const int64_t clusters = grains < limit ? grains : limit;
@@ -296,10 +297,10 @@ double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
     return 5.5 + least + 1e-6 * static_cast<double>(p.M) * static_cast<double>(p.K);
 }
 
-// Many rows of A with a 16-bit result, on tcgen05.
-template <typename T, int G, bool ZERO>
+// Many rows of A, on tcgen05.
+template <typename T, int G, bool ZERO, bool EXACT>
 tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
-    auto kernel = tg::tg_gemm_w4_wide<T, G, ZERO>;
+    auto kernel = tg::tg_gemm_w4_wide<T, G, ZERO, EXACT>;
     struct Limits {
         std::once_flag once;
         int clusters = 0;
@@ -372,7 +373,9 @@ bool prefer_tc(const W4Params& p) {
 
 template <typename T, int G, bool ZERO>
 tg_status_t launch_group(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
-    if (p.M > 64) return launch_wide<T, G, ZERO>(p, dev, s);
+    if (p.M > 64)
+        return p.out_f32 ? launch_wide<T, G, ZERO, true>(p, dev, s)
+                         : launch_wide<T, G, ZERO, false>(p, dev, s);
     if (prefer_tc(p)) {
         if (p.M <= 16) return launch_tc<T, G, 16, ZERO>(p, dev, s);
         if (p.M <= 32) return launch_tc<T, G, 32, ZERO>(p, dev, s);
@@ -388,13 +391,6 @@ tg_status_t launch_zero(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
                              : launch_group<T, G, false>(p, dev, s);
 }
 
-template <typename T>
-tg_status_t launch_few(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
-    if (p.group == 32) return launch_zero<T, 32>(p, dev, s);
-    if (p.group == 64) return launch_zero<T, 64>(p, dev, s);
-    return launch_zero<T, 128>(p, dev, s);
-}
-
 // Many rows, a 16-bit result: whether the weights are decoded to T in memory and the dense
 // GEMM runs on them.  With B MB of codes that takes about 10 us + 1.5·B and the GEMM at
 // 1800 TFLOP/s; tg_gemm_w4_wide, decoding every weight once for 256 rows, does not pass
@@ -408,23 +404,13 @@ bool prefer_dense(const W4Params& p, const tg::OpDevice& dev) {
     return 10.0 + 1.5 * nk / 2e6 + flops / 1800e6 < (wide > flops / 1600e6 ? wide : flops / 1600e6);
 }
 
-// Up to 64 rows of A, and any number with an fp32 result, which the rounding of the weights
-// would spoil, go through the exact kernels, 64 rows at a time.
 template <typename T>
 tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
                         const tg::OpDevice& dev, cudaStream_t s) {
-    if (p.M > 64 && !p.out_f32)
-        return prefer_dense(p, dev) ? launch_dense<T>(in_dtype, p, x, dev, s) : launch_few<T>(p, dev, s);
-    for (int64_t m = 0; m < p.M; m += 64) {
-        W4Params q = p;
-        q.M = p.M - m < 64 ? p.M - m : 64;
-        q.A = static_cast<const T*>(p.A) + m * p.lda;
-        q.C = static_cast<char*>(p.C) + m * p.ldc * (p.out_f32 ? 4 : 2);
-        if (p.resid != nullptr) q.resid = static_cast<const T*>(p.resid) + m * p.ldr;
-        const tg_status_t st = launch_few<T>(q, dev, s);
-        if (st != TG_OK) return st;
-    }
-    return TG_OK;
+    if (p.M > 64 && !p.out_f32 && prefer_dense(p, dev)) return launch_dense<T>(in_dtype, p, x, dev, s);
+    if (p.group == 32) return launch_zero<T, 32>(p, dev, s);
+    if (p.group == 64) return launch_zero<T, 64>(p, dev, s);
+    return launch_zero<T, 128>(p, dev, s);
 }
 
 }  // namespace
