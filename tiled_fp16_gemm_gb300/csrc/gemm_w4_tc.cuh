@@ -368,7 +368,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             if (lane == 0) {
                 tc_arrive(ready + 8 * a);
                 // not before the codes have been used: with the arrival right behind the
-                // loads a stage was refilled before the last of them had come back
+                // loads, stages were refilled before these had taken effect
                 tc_arrive(c_empty + 8 * s);
             }
         }

@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (lane == 0) {
                 wide_arrive(wide_at(a_full + 8 * a, 0));
                 // not before the codes have been used: with the arrival right behind the
-                // loads a stage was refilled before the last of them had come back
+                // loads, stages were refilled before these had taken effect
                 tc_arrive(c_empty + 8 * s);
             }
         }
