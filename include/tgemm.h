@@ -293,10 +293,10 @@ tg_status_t tg_gemm_sp24(int32_t in_dtype, const void* Ac, const void* E, const 
  *           aligned, ldbz a multiple of 16 (else TG_ERR_MISALIGNED); or NULL.
  * C, ldc, epi, stream  as tg_gemm_ex.
  * Rounding  Up to 64 rows: no weight is rounded, the group sums of A·(code - z) are
- *           scaled in fp32.  More rows: W[n][k] has to lie in the range of in_dtype;
- *           with a 16-bit result each is rounded to it, as a dense weight would be,
- *           with an fp32 result none is (the rounding's error goes into the product
- *           as a second weight).
+ *           scaled in fp32.  More rows: with a 16-bit result each W[n][k] is rounded to
+ *           in_dtype, as a dense weight would be, and has to lie in its range; with an
+ *           fp32 result none is rounded (the rounding's error goes into the product as a
+ *           second weight).
  * Memory    A in the kernels' order and the blocks' shares of sums (9 rows and
  *           more), or W decoded (K × roundup(N, 8) elements, where the dense GEMM
  *           is the faster way), in buffers that belong to the (device, stream), are

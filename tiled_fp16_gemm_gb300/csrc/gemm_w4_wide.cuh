@@ -11,7 +11,10 @@
 // EXACT, for an fp32 result: the rounding's error, (code - z) · s minus the rounded value,
 // is a T too (the product has 15 bits at most, its last place that of s or above), and one
 // fused multiplication and addition gives it.  It is the operand of a second set of MMAs on
-// the same tokens, so no weight is rounded; units take two places in tensor memory.
+// the same tokens, so no weight is rounded; units take two places in tensor memory.  Where
+// that adds up to NaN the sum is taken again from the definition (wide_again): an infinite
+// activation times a remainder of 0, or of the other sign, is NaN where the weight is not 0,
+// and a weight beyond T's range is inf minus inf.
 //
 // The blocks work in pairs (cta_group::2): the MMA takes 256 rows of W, 128 in each block's
 // tensor memory, and half of the tokens from each block's shared memory.  With blocks of
@@ -50,8 +53,9 @@ constexpr int kWideCodeBytes = 10240;    // codes 8192, scales ≤ 1024, zero po
 constexpr int kWideScaleAt = 8192;
 constexpr int kWideZeroAt = 9216;
 constexpr int kWideXBytes = kWideTokens / 2 * 256;
+constexpr int kWideNanBytes = 256 * 16;  // EXACT: which of a thread's 8 times 16 sums are NaN
 constexpr int kWideSmem =
-    1024 + kWideXStages * kWideXBytes + kWideStages * kWideCodeBytes + 512;
+    1024 + kWideXStages * kWideXBytes + kWideStages * kWideCodeBytes + 512 + kWideNanBytes;
 
 struct WideLaunch {
     W4Params p;
@@ -142,6 +146,72 @@ __device__ __forceinline__ P* wide_step(P* p, int64_t n) {
     P* r;
     asm volatile("add.s64 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(n));
     return r;
+}
+// EXACT: sums that came out NaN, by the definition: Σ a·((c - z)·s), each weight exact in
+// fp32, and their epilogue.  A row of A with NaN or infinities has the sum of their products,
+// whatever the others are.  `seen`: which 16 of each 32 tokens from m0 on, `nan`: which of them.
+// (At the end of a tile, and no call: either took registers from its loop.)  512 rows of
+// 16384×8192, fp16: one infinity in one row 0.27 ms instead of 0.15, in every row 36 ms, all
+// of A infinite or NaN 0.9 ms; every weight beyond fp16's range 0.2 s.
+template <typename T>
+__device__ __forceinline__ void wide_again(const W4Params& p, int64_t m0, int64_t n, uint32_t seen,
+                                        const uint16_t* nan) {
+    auto finite = [](float x) { return x - x == 0.0f; };
+    // 8 products, k a multiple of 8: of all activations, or of those that are not finite
+    auto eight = [&](const T* a, int64_t k, bool all, float sum) {
+        const int64_t g = k / p.group;
+        const int z = p.zero != nullptr ? p.zero[g * p.ldz + n] & 15 : 8;
+        const float s = op_to_float(static_cast<const T*>(p.scale)[g * p.lds + n]);
+        const uint8_t* codes = p.Bq + n * p.ldbq + k / 2;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k + j >= p.K) break;
+            const float x = op_to_float(a[k + j]);
+            const float w = static_cast<float>((codes[j / 2] >> (4 * (j & 1)) & 15) - z) * s;
+            if (all || !finite(x)) sum = fmaf(x, w, sum);
+        }
+        return sum;
+    };
+#pragma unroll 1
+    for (int c = 0; seen >> c != 0; ++c) {
+        if ((seen >> c & 1) == 0) continue;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            const int64_t m = m0 + 32 * c + i;
+            if ((nan[c] >> i & 1) == 0 || m >= p.M) continue;
+            const T* a = static_cast<const T*>(p.A) + m * p.lda;
+            float sum = 0.0f;
+            bool clean = true;
+#pragma unroll 1
+            for (int64_t k = 0; k < p.K && sum == sum; k += 32) {
+                bool fine = true;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    fine = finite(op_to_float(a[k + j < p.K ? k + j : k])) && fine;
+                if (fine) continue;
+                clean = false;
+#pragma unroll 1
+                for (int64_t l = k; l < k + 32 && l < p.K; l += 8) sum = eight(a, l, false, sum);
+            }
+            if (clean)
+#pragma unroll 1
+                for (int64_t k = 0; k < p.K; k += 8) sum = eight(a, k, true, sum);
+            w4_store<T>(p, m, n, sum);
+        }
+    }
+}
+// Which of 16 sums are NaN, noted for the end of the tile.
+__device__ __forceinline__ void wide_note(const float (&v)[16], int c, uint16_t* nan, uint32_t* seen) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) any = any || v[i] != v[i];
+    if (any) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bits |= (v[i] != v[i] ? 1u : 0u) << i;
+        nan[c >> 5] = static_cast<uint16_t>(bits);
+        *seen |= 1u << (c >> 5);
+    }
 }
 // Epilogue and store of 16 tokens of row n, `most` of them.
 template <typename T, typename TC>
@@ -375,6 +445,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t row = 32 * quarter + lane;
         const uint32_t at = d_cols + (static_cast<uint32_t>(32 * quarter) << 16);
         const int64_t slot = int64_t{q.tokens} * kTcRows;
+        uint16_t* const nan = reinterpret_cast<uint16_t*>(shared + (bars + 512 - base)) + (set * kTcRows + row) * 8;
         int i = 0;
         uint32_t tiles = 0;
         while (i < n_units) {
@@ -388,6 +459,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const bool whole = len == q.k_units;
             const float bias = p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
             float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
+            uint32_t seen = 0;
             for (int c = 16 * set; c < tokens; c += 32) {
                 uint32_t r[16];
                 tc_load(at + c, r);
@@ -395,6 +467,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     float v[16];
 #pragma unroll
                     for (int m = 0; m < 16; ++m) v[m] = __uint_as_float(r[m]);
+                    if constexpr (EXACT) wide_note(v, c, nan, &seen);
                     if (n < p.N) wide_store<T, TC>(p, m0 + c, n, tokens - c, bias, v);
                 } else {
 #pragma unroll
@@ -445,9 +518,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 for (int m = 0; m < 16; ++m) sum[m] += w[m];
                             }
                         }
+                        if constexpr (EXACT) wide_note(sum, c, nan, &seen);
                         if (n < p.N) wide_store<T, TC>(p, m0 + c, n, tokens - c, bias, sum);
                     }
                 }
+            }
+            if constexpr (EXACT) {
+                if (seen != 0 && n < p.N) wide_again<T>(p, m0 + 16 * set, n, seen, nan);
             }
             i += len;
             kb = 0;
