@@ -829,11 +829,13 @@ __global__ void __launch_bounds__(kNormThreads)
             }
             g.sum5(s);
             peers.add(s);
-            const float ry = in_dh.base != nullptr ? rsqrtf(s[0] * inv + p.eps) : 0.0f;
-            const float cy = ry * ry * s[1] * inv;
+            // Without dh nothing is taken of y, which need not be finite then.
+            const bool has_dh = in_dh.base != nullptr;
+            const float ry = has_dh ? rsqrtf(s[0] * inv + p.eps) : 0.0f;
+            const float cy = has_dh ? ry * ry * s[1] * inv : 0.0f;
+            const float td = has_dh ? s[2] + ry * (s[3] - cy * s[4]) : s[2];  // Σ t·dy'
             // -mean(dm·m) · rx: what dx gets of m
-            const float cx =
-                p.wpost != nullptr ? -rx * p.scale * inv * (s[2] + ry * (s[3] - cy * s[4])) : 0.0f;
+            const float cx = p.wpost != nullptr ? -rx * p.scale * inv * td : 0.0f;
             const float sx = rx * p.scale;
             const F2 ry2 = f2(ry, ry), cy2 = f2(-cy, -cy), cx2 = f2(cx, cx), sx2 = f2(sx, sx);
             const bool own_gate =
@@ -846,11 +848,15 @@ __global__ void __launch_bounds__(kNormThreads)
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
                 F2 dx[4];
+                if (has_dh)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum_pre[ch][i] = f2_fma(dh[i], f2_mul(y[i], ry2), sum_pre[ch][i]);
+                        dy[i] = f2_fma(ry2, f2_fma(cy2, y[i], f2_mul(dh[i], wp[i])), dy[i]);
+                    }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const F2 m = x[ch][i];
-                    sum_pre[ch][i] = f2_fma(dh[i], f2_mul(y[i], ry2), sum_pre[ch][i]);
-                    dy[i] = f2_fma(ry2, f2_fma(cy2, y[i], f2_mul(dh[i], wp[i])), dy[i]);
                     sum_gate[ch][i] = f2_fma(dy[i], f2_mul(m, wo[i]), sum_gate[ch][i]);
                     const F2 dg = f2_mul(dy[i], gt[i]);
                     sum_post[ch][i] = f2_fma(dg, m, sum_post[ch][i]);
