@@ -16,6 +16,7 @@
 // when they are stored (h comes from the unrounded y).
 #pragma once
 
+#include "granules.h"
 #include "op_device.cuh"
 
 namespace tg {
@@ -377,18 +378,19 @@ struct NormInput {
                         norm_copy16(dst + piece(c, ch, (c.tid & 31) + 32 * h) * 16,
                                     src + piece_col(c, ch, h) * static_cast<int>(sizeof(T)));
         } else {
-            // of the last granule, the row's bytes only; the first row's first
-            // granule may begin before the matrix does, and is read value by value
-            const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
-            const int end = skip + c.cols * static_cast<int>(sizeof(T));
-            for (int b = c.tid * 16; b < end; b += c.threads * 16) {
-                const int n = end - b < 16 ? end - b : 16;
-                if (b == 0 && skip != 0 && row == 0) {
-                    for (int i = skip; i < n; i += static_cast<int>(sizeof(T)))
+            // of the last granule, the row's bytes only; a first granule that begins
+            // before the matrix does is read value by value
+            const Granules g = granules(reinterpret_cast<uint64_t>(base),
+                                        static_cast<uint64_t>(row) * ld * sizeof(T),
+                                        c.cols * static_cast<int>(sizeof(T)));
+            for (int b = c.tid * 16; b < g.end; b += c.threads * 16) {
+                const int n = g.end - b < 16 ? g.end - b : 16;
+                if (b == 0 && g.outside) {
+                    for (int i = g.skip; i < n; i += static_cast<int>(sizeof(T)))
                         *reinterpret_cast<T*>(place + offset + i) =
-                            *reinterpret_cast<const T*>(src - skip + i);
+                            *reinterpret_cast<const T*>(src - g.skip + i);
                 } else {
-                    norm_copy16(dst + b, src - skip + b, n);
+                    norm_copy16(dst + b, src - g.skip + b, n);
                 }
             }
         }
