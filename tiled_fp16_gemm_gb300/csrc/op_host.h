@@ -62,6 +62,17 @@ int32_t op_take_inject();
 bool w4_take_timeout();
 bool norm_take_timeout();
 
+// Whether `encode`, a call of cuTensorMapEncodeTiled, succeeds.  That needs a current context,
+// which a host thread does not have before its first call that binds one: then it is bound here.
+template <typename F>
+bool op_encode(F encode) {
+    CUresult r = encode();
+    int d = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&d) == cudaSuccess && cudaSetDevice(d) == cudaSuccess)
+        r = encode();
+    return r == CUDA_SUCCESS;
+}
+
 // The 2-D tensor map of rows of `inner` elements, `row_bytes` apart, read in boxes of
 // box_inner × box_outer; zero outside.
 inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType type, uint64_t inner,
@@ -81,9 +92,11 @@ inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType typ
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t steps[2] = {1, 1};
-    return encode(map, type, 2, const_cast<void*>(ptr), dims, strides, box, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return op_encode([&] {
+        return encode(map, type, 2, const_cast<void*>(ptr), dims, strides, box, steps,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
 }
 
 // Device memory per (device, stream), grown on demand.  A buffer that became

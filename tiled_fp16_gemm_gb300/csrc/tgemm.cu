@@ -403,10 +403,12 @@ bool encode_2d_sw(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t ou
     cuuint64_t strides[1] = {row_bytes};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return false;
+    if (!tg::op_encode([&] {
+            return enc(map, dtype, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        }))
+        return false;
     g_map_misses.fetch_add(1, std::memory_order_relaxed);
     std::lock_guard<std::mutex> lk(g_map_mutex);
     MapEntry& e = g_map_cache[slot];
