@@ -1,0 +1,80 @@
+// Host-side check of the workspaces in op_host.h, on stand-ins for the CUDA calls that they
+// make (compiled and run by test_threads.py with the system C++ compiler).  "Launches" are
+// entries of a log.
+#include <cstdio>
+#include <cstdlib>
+#include <thread>
+#include <vector>
+
+#include "op_host.h"
+
+extern "C" {
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+cudaError_t cudaMalloc(void** p, size_t bytes) {
+    *p = std::malloc(bytes);
+    return cudaSuccess;
+}
+cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) {
+    *s = cudaStreamCaptureStatusNone;
+    return cudaSuccess;
+}
+}
+
+namespace {
+
+cudaStream_t stream(int i) { return reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(64 * i)); }
+
+struct Launch {
+    int stream, thread;
+};
+std::mutex g_log_mutex;
+std::vector<Launch> g_log;
+
+void launch(int stream, int thread) {
+    {
+        std::lock_guard<std::mutex> lk(g_log_mutex);
+        g_log.push_back({stream, thread});
+    }
+    std::this_thread::yield();
+}
+
+}  // namespace
+
+int main() {
+    tg::OpWorkspace ws;
+    // Two threads on each of two streams, two launches a call, sizes that grow: on a stream
+    // the launches of a call follow one another.
+    std::vector<std::thread> threads;
+    for (int t = 0; t < 4; ++t)
+        threads.emplace_back([&, t] {
+            const int s = 1 + t % 2;
+            for (int i = 0; i < 5000; ++i) {
+                tg::OpWorkspace::Hold hold;
+                void* p = nullptr;
+                if (ws.get(0, stream(s), static_cast<size_t>(1 + i / 1000) << 10, &p, &hold) != TG_OK || p == nullptr)
+                    std::abort();
+                launch(s, t);
+                launch(s, t);
+            }
+        });
+    for (auto& t : threads) t.join();
+    for (int s = 1; s <= 2; ++s) {
+        std::vector<int> of;
+        for (const Launch& l : g_log)
+            if (l.stream == s) of.push_back(l.thread);
+        for (size_t i = 0; i + 1 < of.size(); i += 2)
+            if (of[i] != of[i + 1]) {
+                std::printf("FAIL stream %d: launch %zu is thread %d's, the next one thread %d's\n", s, i, of[i], of[i + 1]);
+                return 1;
+            }
+    }
+    // A call under way on one stream keeps no other stream waiting.
+    tg::OpWorkspace::Hold one, two;
+    void *p = nullptr, *q = nullptr;
+    if (ws.get(0, stream(1), 64, &p, &one) != TG_OK || ws.get(0, stream(2), 64, &q, &two) != TG_OK || p == q) {
+        std::printf("FAIL two streams\n");
+        return 1;
+    }
+    std::printf("OK\n");
+    return 0;
+}

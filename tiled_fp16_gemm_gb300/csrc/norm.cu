@@ -374,9 +374,10 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
                                                     : blocks;
         const int64_t slots = (q.dwpost != nullptr ? blocks : 0) +
                               (q.dwpre != nullptr ? blocks : 0) + gate_slots;
+        tg::OpWorkspace::Hold hold;  // until the shares' sums are launched
         if (slots > 0) {
             void* ws = nullptr;
-            st = g_workspace.get(dev.dev, s, static_cast<size_t>(slots * cols) * 4, &ws);
+            st = g_workspace.get(dev.dev, s, static_cast<size_t>(slots * cols) * 4, &ws, &hold);
             if (st != TG_OK) return st;
             float* next = static_cast<float*>(ws);
             if (q.dwpost != nullptr) q.ws_post = next, next += blocks * cols;

@@ -105,16 +105,26 @@ inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType typ
 // together hold less than twice the largest.  Growth allocates, which a
 // stream capture forbids: there it fails with TG_ERR_NO_MEMORY before
 // anything is enqueued, and the capture stays valid.
+//
+// A call's launches hand each other what lies there, so no launch of another host
+// thread's call on the stream may come between them: the caller keeps `hold` until
+// its last one.  Other streams do not wait.
 class OpWorkspace {
   public:
+    using Hold = std::unique_lock<std::mutex>;
     // `fresh` (if given): whether this is the buffer's first use since `epoch` changed.
-    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, bool* fresh = nullptr,
-                    uint64_t epoch = 0) {
+    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, Hold* hold,
+                    bool* fresh = nullptr, uint64_t epoch = 0) {
         // the per-thread default stream is one handle for a stream per thread
         const size_t thread =
             s == cudaStreamPerThread ? std::hash<std::thread::id>{}(std::this_thread::get_id()) : 0;
-        std::lock_guard<std::mutex> lk(m_);
-        Buffer& b = of_[std::make_tuple(dev, s, thread)];
+        Buffer* found;
+        {
+            std::lock_guard<std::mutex> lk(m_);
+            found = &of_[std::make_tuple(dev, s, thread)];  // (entries stay where they are)
+        }
+        Buffer& b = *found;
+        *hold = Hold(b.m);
         if (b.bytes < bytes) {
             cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
             if (cudaStreamIsCapturing(s, &capture) != cudaSuccess ||
@@ -145,6 +155,7 @@ class OpWorkspace {
 
   private:
     struct Buffer {
+        std::mutex m;
         void* p = nullptr;
         size_t bytes = 0;
         bool used = false;

@@ -27,7 +27,8 @@ tg_status_t launch_dense(int32_t in_dtype, const W4Params& p, const tg_epilogue_
                          const tg::OpDevice& dev, cudaStream_t s) {
     const int64_t ldo = (p.N + 7) / 8 * 8;
     void* ws = nullptr;
-    tg_status_t st = g_workspace.get(dev.dev, s, static_cast<size_t>(p.K * ldo) * 2, &ws);
+    tg::OpWorkspace::Hold hold;  // until the product is launched
+    tg_status_t st = g_workspace.get(dev.dev, s, static_cast<size_t>(p.K * ldo) * 2, &ws, &hold);
     if (st != TG_OK) return st;
     const int64_t tiles = (p.K + 127) / 128 * ((p.N + 63) / 64);
     const int64_t grid = tiles < 8 * dev.num_sms ? tiles : 8 * dev.num_sms;
@@ -230,8 +231,9 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
     const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
     void* ws = nullptr;
     bool fresh = false;
+    tg::OpWorkspace::Hold hold;  // until the product is launched
     tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
-                              &ws, &fresh, g_timeouts.load());
+                              &ws, &hold, &fresh, g_timeouts.load());
     if (st != TG_OK) return st;
     if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
         cudaGetLastError();
@@ -326,8 +328,9 @@ tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
     const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
     void* ws = nullptr;
     bool fresh = false;
+    tg::OpWorkspace::Hold hold;  // until the product is launched
     tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
-                              &ws, &fresh, g_timeouts.load());
+                              &ws, &hold, &fresh, g_timeouts.load());
     if (st != TG_OK) return st;
     if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
         cudaGetLastError();
