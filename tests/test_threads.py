@@ -103,3 +103,34 @@ def test_gradients_of_two_threads(tg):
         for grads in mine:
             for a, b in zip(grads, want):
                 assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,mx", [(200, 512, 1032, False), (40, 512, 1032, False), (200, 512, 1024, True),
+                                      (40, 512, 1024, True)])
+def test_staged_products_of_two_threads(tg, M, N, K, mx):
+    """Rows of A off 16 bytes go through the stream's staging buffer; MXFP4 weights for many
+    rows of A through its decoded weights."""
+    import torch
+    stream = torch.cuda.Stream()
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    calls, results, wanted = [], [], []
+    for _ in range(2):
+        a = torch.randn(M, K + 1, generator=g, device="cuda").half()[:, :K]
+        if mx:
+            bq = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+            scale = torch.full((K // 32, N), 120, device="cuda", dtype=torch.uint8)
+            call = lambda a=a, bq=bq, scale=scale, **kw: tg.gemm_mxfp4(a, bq, scale, N, **kw)  # noqa: E731
+        else:
+            b = torch.randn(K, N, generator=g, device="cuda").half()
+            call = lambda a=a, b=b, **kw: tg.gemm(a, b, **kw)  # noqa: E731
+        wanted.append(call())
+        out = torch.zeros(300, M, N, device="cuda", dtype=torch.half)
+        results.append(out)
+        calls.append(lambda i, call=call, out=out: call(out=out[i % 300], stream=stream))
+    torch.cuda.synchronize()
+    in_threads(calls, 600)
+    torch.cuda.synchronize()
+    tg.sync_status()
+    for out, want in zip(results, wanted):
+        assert torch.equal(out, want.expand_as(out))

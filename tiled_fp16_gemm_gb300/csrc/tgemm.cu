@@ -630,17 +630,26 @@ int64_t round_up8(int64_t x) { return (x + 7) / 8 * 8; }
 
 // Per-(device, stream) staging buffer for operands in layouts the tensor
 // memory-access unit cannot address; grown on demand (growth waits for the
-// stream, so it cannot happen inside a stream capture).
+// stream, so it cannot happen inside a stream capture).  A call fills the
+// buffer in one launch and reads it in another: it keeps `hold` until its last
+// launch, so that no other host thread's call on the stream comes between.
+using StagingHold = std::unique_lock<std::mutex>;
 struct Staging {
+    std::mutex m;
     void* ptr = nullptr;
     size_t bytes = 0;
 };
+using StagingMap = std::map<std::pair<int, cudaStream_t>, Staging>;
 std::mutex g_staging_mutex;
-std::map<std::pair<int, cudaStream_t>, Staging> g_staging;
+StagingMap g_staging;
 
-tg_status_t staging_buffer(int dev, cudaStream_t s, size_t bytes, void** out) {
-    std::lock_guard<std::mutex> lk(g_staging_mutex);
-    Staging& st = g_staging[std::make_pair(dev, s)];
+Staging& staging_of(std::mutex& m, StagingMap& of, int dev, cudaStream_t s) {
+    std::lock_guard<std::mutex> lk(m);
+    return of[std::make_pair(dev, s)];  // (entries stay where they are)
+}
+
+tg_status_t staging_get(Staging& st, cudaStream_t s, size_t bytes, void** out, StagingHold* hold) {
+    *hold = StagingHold(st.m);
     if (st.bytes < bytes) {
         if (st.ptr) {
             if (cudaStreamSynchronize(s) != cudaSuccess || cudaFree(st.ptr) != cudaSuccess) {
@@ -659,6 +668,10 @@ tg_status_t staging_buffer(int dev, cudaStream_t s, size_t bytes, void** out) {
     }
     *out = st.ptr;
     return TG_OK;
+}
+
+tg_status_t staging_buffer(int dev, cudaStream_t s, size_t bytes, void** out, StagingHold* hold) {
+    return staging_get(staging_of(g_staging_mutex, g_staging, dev, s), s, bytes, out, hold);
 }
 
 // Copy a rows×cols matrix of `elem_bytes` (2 or 4) byte elements.
@@ -765,7 +778,8 @@ tg_status_t gemm_impl(const void* A, const void* B, void* C, int64_t M, int64_t 
     const int64_t bytes_b = b_ok ? 0 : align256(K * ldb2 * 2);
     const int64_t bytes_c = c_ok ? 0 : align256(M * ldc2 * elem_c);
     void* buf = nullptr;
-    st = staging_buffer(dev, s, static_cast<size_t>(bytes_a + bytes_b + bytes_c), &buf);
+    StagingHold hold;
+    st = staging_buffer(dev, s, static_cast<size_t>(bytes_a + bytes_b + bytes_c), &buf, &hold);
     if (st != TG_OK) return st;
     char* p = static_cast<char*>(buf);
     const void* A2 = a_ok ? A : p;
@@ -805,29 +819,10 @@ tg_status_t validate_ex(int32_t in_dtype, const void* C, int64_t M, int64_t N,
 // Per-(device, stream) fp16 buffer for dequantised MXFP4 weights (M > 128
 // path); grown on demand like the staging buffer.
 std::mutex g_deq_mutex;
-std::map<std::pair<int, cudaStream_t>, Staging> g_deq;
+StagingMap g_deq;
 
-tg_status_t dequant_buffer(int dev, cudaStream_t s, size_t bytes, void** out) {
-    std::lock_guard<std::mutex> lk(g_deq_mutex);
-    Staging& st = g_deq[std::make_pair(dev, s)];
-    if (st.bytes < bytes) {
-        if (st.ptr) {
-            if (cudaStreamSynchronize(s) != cudaSuccess || cudaFree(st.ptr) != cudaSuccess) {
-                cudaGetLastError();
-                return TG_ERR_LAUNCH;
-            }
-            st.ptr = nullptr;
-            st.bytes = 0;
-        }
-        if (cudaMalloc(&st.ptr, bytes) != cudaSuccess) {
-            cudaGetLastError();
-            st.ptr = nullptr;
-            return TG_ERR_NO_MEMORY;
-        }
-        st.bytes = bytes;
-    }
-    *out = st.ptr;
-    return TG_OK;
+tg_status_t dequant_buffer(int dev, cudaStream_t s, size_t bytes, void** out, StagingHold* hold) {
+    return staging_get(staging_of(g_deq_mutex, g_deq, dev, s), s, bytes, out, hold);
 }
 
 // Whether TGEMM_FORCE_CFG names one of the dense tile kernels (the MXFP4
@@ -1187,10 +1182,11 @@ tg_status_t tg_gemm_mxfp4(const void* A, const void* Bq, const void* Bscale, voi
         tg::skinny_mx_plan(M, N, K, ds->num_sms, &pl);
         const void* A2 = A;
         int64_t lda2 = lda;
+        StagingHold hold;
         if (!tma_layout_ok(A, lda)) {  // A in the staging buffer, rows 16-byte aligned
             lda2 = round_up8(K);
             void* buf = nullptr;
-            st = staging_buffer(dev, s, static_cast<size_t>(M * lda2 * 2), &buf);
+            st = staging_buffer(dev, s, static_cast<size_t>(M * lda2 * 2), &buf, &hold);
             if (st != TG_OK) return st;
             if ((st = copy_matrix(A, lda, buf, lda2, M, K, 2, ds->num_sms, s)) != TG_OK) return st;
             A2 = buf;
@@ -1202,7 +1198,8 @@ tg_status_t tg_gemm_mxfp4(const void* A, const void* Bq, const void* Bscale, voi
     // Compute-bound sizes: dequantise once to fp16, then the dense GEMM.
     const int64_t ldd = round_up8(N);
     void* deq = nullptr;
-    st = dequant_buffer(dev, s, static_cast<size_t>(K * ldd * 2), &deq);
+    StagingHold hold;
+    st = dequant_buffer(dev, s, static_cast<size_t>(K * ldd * 2), &deq, &hold);
     if (st != TG_OK) return st;
     const int64_t tiles = ((K + 63) / 64) * ((N + 63) / 64);  // 64 × 64 per block iteration
     const unsigned grid = static_cast<unsigned>(tiles < 8 * ds->num_sms ? tiles : 8 * ds->num_sms);
