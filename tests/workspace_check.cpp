@@ -3,6 +3,7 @@
 // entries of a log.
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <thread>
 #include <vector>
 
@@ -14,6 +15,16 @@ cudaError_t cudaMalloc(void** p, size_t bytes) {
     *p = std::malloc(bytes);
     return cudaSuccess;
 }
+cudaError_t cudaFree(void* p) {
+    std::free(p);
+    return cudaSuccess;
+}
+cudaError_t cudaMemset(void* p, int v, size_t bytes) {
+    std::memset(p, v, bytes);
+    return cudaSuccess;
+}
+cudaError_t cudaMemsetAsync(void* p, int v, size_t bytes, cudaStream_t) { return cudaMemset(p, v, bytes); }
+cudaError_t cudaDeviceSynchronize() { return cudaSuccess; }
 cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) {
     *s = cudaStreamCaptureStatusNone;
     return cudaSuccess;
@@ -75,6 +86,29 @@ int main() {
         std::printf("FAIL two streams\n");
         return 1;
     }
+    // Counters: zero at first, cleared in every buffer of the device, one that became too
+    // small among them, and on no other device.
+    tg::OpWorkspace counted(256);
+    unsigned char* at[4];
+    for (int i = 0; i < 4; ++i) {
+        tg::OpWorkspace::Hold hold;
+        void* r = nullptr;
+        if (counted.get(i == 3, stream(i == 2 ? 2 : 1), i == 1 ? 4096 : 512, &r, &hold) != TG_OK) std::abort();
+        at[i] = static_cast<unsigned char*>(r);
+        for (int j = 0; j < 256; ++j)
+            if (at[i][j] != 0) {
+                std::printf("FAIL buffer %d is not zero at first\n", i);
+                return 1;
+            }
+        std::memset(at[i], i + 1, 512);
+    }
+    bool also = false;
+    counted.clear(0, [&] { also = true; });
+    for (int i = 0; i < 4; ++i)
+        if (at[i][0] != (i == 3 ? 4 : 0) || at[i][255] != at[i][0] || at[i][256] != i + 1 || !also) {
+            std::printf("FAIL buffer %d after the clearing: %d %d\n", i, at[i][0], at[i][256]);
+            return 1;
+        }
     std::printf("OK\n");
     return 0;
 }

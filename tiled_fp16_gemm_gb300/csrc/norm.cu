@@ -190,12 +190,13 @@ int64_t max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg
 
 }  // namespace
 
-bool tg::norm_take_timeout() {
+bool tg::norm_take_timeout(int) {
     unsigned int n = 0;
     if (cudaMemcpyFromSymbol(&n, tg::g_norm_timeouts, sizeof(n)) != cudaSuccess || n == 0) {
         cudaGetLastError();
         return false;
     }
+    cudaDeviceSynchronize();  // (other streams' launches are in this report)
     n = 0;
     cudaMemcpyToSymbol(tg::g_norm_timeouts, &n, sizeof(n));
     cudaGetLastError();

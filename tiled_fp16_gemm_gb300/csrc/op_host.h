@@ -12,6 +12,7 @@
 #include <mutex>
 #include <thread>
 #include <tuple>
+#include <vector>
 
 #include "tgemm.h"
 
@@ -58,9 +59,10 @@ uint64_t op_wait_limit_ns();
 int32_t op_take_inject();
 
 // Whether a kernel of w4.cu or norm.cu gave up on a wait since the last call, on the
-// current device, which has to be idle.
-bool w4_take_timeout();
-bool norm_take_timeout();
+// current device `dev`.  Where one did, everything queued on the device is let end first,
+// and counters that it may have left are cleared.
+bool w4_take_timeout(int dev);
+bool norm_take_timeout(int dev);
 
 // Whether `encode`, a call of cuTensorMapEncodeTiled, succeeds.  That needs a current context,
 // which a host thread does not have before its first call that binds one: then it is bound here.
@@ -109,12 +111,15 @@ inline bool op_map_2d(CUtensorMap* map, const void* ptr, CUtensorMapDataType typ
 // A call's launches hand each other what lies there, so no launch of another host
 // thread's call on the stream may come between them: the caller keeps `hold` until
 // its last one.  Other streams do not wait.
+//
+// The first `counters` bytes of a buffer are zero when it is made, and every launch
+// leaves them at zero, but for one that gives up on a wait: then clear() is needed.
 class OpWorkspace {
   public:
     using Hold = std::unique_lock<std::mutex>;
-    // `fresh` (if given): whether this is the buffer's first use since `epoch` changed.
-    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, Hold* hold,
-                    bool* fresh = nullptr, uint64_t epoch = 0) {
+    explicit OpWorkspace(size_t counters = 0) : counters_(counters) {}
+
+    tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, Hold* hold) {
         // the per-thread default stream is one handle for a stream per thread
         const size_t thread =
             s == cudaStreamPerThread ? std::hash<std::thread::id>{}(std::this_thread::get_id()) : 0;
@@ -142,25 +147,43 @@ class OpWorkspace {
                     return TG_ERR_NO_MEMORY;
                 }
             }
-            b.p = p;
+            if (counters_ > 0 && cudaMemsetAsync(p, 0, counters_, s) != cudaSuccess) {
+                cudaGetLastError();
+                cudaFree(p);
+                return TG_ERR_LAUNCH;
+            }
+            b.all.push_back(p);
             b.bytes = want;
-            b.used = false;
         }
-        if (fresh != nullptr) *fresh = !b.used || b.epoch != epoch;
-        b.used = true;
-        b.epoch = epoch;
-        *out = b.p;
+        *out = b.all.back();
         return TG_OK;
+    }
+
+    // Zeroes the counters of all buffers of `dev`, the current device, those that became
+    // too small too (captured graphs may use them), and calls `also`, once everything
+    // queued there has ended.  No call is between get() and its last launch meanwhile.
+    template <typename F>
+    void clear(int dev, F also) {
+        std::lock_guard<std::mutex> lk(m_);
+        std::vector<Hold> holds;
+        for (auto& of : of_)
+            if (std::get<0>(of.first) == dev) holds.emplace_back(of.second.m);
+        cudaDeviceSynchronize();
+        also();
+        for (auto& of : of_)
+            if (std::get<0>(of.first) == dev)
+                for (void* p : of.second.all) cudaMemset(p, 0, counters_);
+        cudaDeviceSynchronize();
+        cudaGetLastError();
     }
 
   private:
     struct Buffer {
         std::mutex m;
-        void* p = nullptr;
-        size_t bytes = 0;
-        bool used = false;
-        uint64_t epoch = 0;
+        std::vector<void*> all;  // the last one is in use
+        size_t bytes = 0;        // of that one
     };
+    const size_t counters_;
     std::mutex m_;
     std::map<std::tuple<int, cudaStream_t, size_t>, Buffer> of_;
 };

@@ -1295,11 +1295,11 @@ tg_status_t tg_sync_status(void* stream) {
         tg::splitk_reset_counters(dev);
         noalloc_reset_counters(dev);
         cudaGetLastError();
-        tg::w4_take_timeout();
-        tg::norm_take_timeout();
+        tg::w4_take_timeout(dev);
+        tg::norm_take_timeout(dev);
         return TG_ERR_TIMEOUT;
     }
-    const bool w4 = tg::w4_take_timeout(), norm = tg::norm_take_timeout();
+    const bool w4 = tg::w4_take_timeout(dev), norm = tg::norm_take_timeout(dev);
     return w4 || norm ? TG_ERR_TIMEOUT : TG_OK;
 }
 

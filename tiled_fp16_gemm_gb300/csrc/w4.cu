@@ -3,8 +3,6 @@
 #include <cstring>
 #include <set>
 
-#include <atomic>
-
 #include "gemm_w4.cuh"
 #include "gemm_w4_tc.cuh"
 #include "gemm_w4_wide.cuh"
@@ -15,8 +13,10 @@ namespace {
 using tg::W4Params;
 
 tg::OpWorkspace g_workspace;  // 16-bit weights of the dense path
-tg::OpWorkspace g_tc;         // of tg_gemm_w4_tc: counters, sums of shares, A in order
-std::atomic<uint64_t> g_timeouts{0};  // how often a wait ran out: counters are then cleared
+// Of tg_gemm_w4_tc and tg_gemm_w4_wide: counters, sums of shares, A in order.  The counters'
+// place is the same for every shape: each launch leaves them at zero for the stream's next.
+constexpr int64_t kCounterBytes = 64 * 1024;
+tg::OpWorkspace g_tc(kCounterBytes);
 
 bool misaligned(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
@@ -223,25 +223,17 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
     q.k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     q.units = (p.N + tg::kTcRows - 1) / tg::kTcRows * q.k_units;
     const int64_t blocks = q.units < dev.num_sms ? q.units : dev.num_sms;
-    // the counters' place is the same for every shape: each launch leaves them at zero
-    // for the stream's next one
-    constexpr int64_t counter_bytes = 64 * 1024;
-    if (blocks * 32 > counter_bytes) return TG_ERR_UNSUPPORTED_DEVICE;
+    if (blocks * 32 > kCounterBytes) return TG_ERR_UNSUPPORTED_DEVICE;
     const int64_t slot_bytes = 2 * blocks * NP * tg::kTcRows * 4;
     const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
     void* ws = nullptr;
-    bool fresh = false;
     tg::OpWorkspace::Hold hold;  // until the product is launched
-    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
-                              &ws, &hold, &fresh, g_timeouts.load());
+    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(kCounterBytes + slot_bytes + p.M * ldo * 2),
+                              &ws, &hold);
     if (st != TG_OK) return st;
-    if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
     q.counters = static_cast<uint32_t*>(ws);
-    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + counter_bytes);
-    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + counter_bytes + slot_bytes);
+    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kCounterBytes + slot_bytes);
     constexpr CUtensorMapDataType type =
         std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t groups = (p.K + G - 1) / G;
@@ -322,23 +314,17 @@ tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
     q.limit_ns = tg::op_wait_limit_ns();
     plan_wide(p, lim.clusters, &q);
     const int64_t blocks = int64_t{q.clusters} * tg::kWideCluster;
-    constexpr int64_t counter_bytes = 64 * 1024;  // as in launch_tc
-    if (blocks * 32 > counter_bytes) return TG_ERR_UNSUPPORTED_DEVICE;
+    if (blocks * 32 > kCounterBytes) return TG_ERR_UNSUPPORTED_DEVICE;
     const int64_t slot_bytes = 2 * blocks * q.tokens * tg::kTcRows * 4;
     const int64_t ldo = int64_t{q.k_units} * tg::kTcK;
     void* ws = nullptr;
-    bool fresh = false;
     tg::OpWorkspace::Hold hold;  // until the product is launched
-    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(counter_bytes + slot_bytes + p.M * ldo * 2),
-                              &ws, &hold, &fresh, g_timeouts.load());
+    tg_status_t st = g_tc.get(dev.dev, s, static_cast<size_t>(kCounterBytes + slot_bytes + p.M * ldo * 2),
+                              &ws, &hold);
     if (st != TG_OK) return st;
-    if (fresh && cudaMemsetAsync(ws, 0, static_cast<size_t>(counter_bytes), s) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
     q.counters = static_cast<uint32_t*>(ws);
-    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + counter_bytes);
-    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + counter_bytes + slot_bytes);
+    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kCounterBytes + slot_bytes);
     constexpr CUtensorMapDataType type =
         std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const uint64_t groups = (p.K + G - 1) / G;
@@ -418,16 +404,17 @@ tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_e
 
 }  // namespace
 
-bool tg::w4_take_timeout() {
+bool tg::w4_take_timeout(int dev) {
     unsigned int n = 0;
     if (cudaMemcpyFromSymbol(&n, tg::g_w4_timeouts, sizeof(n)) != cudaSuccess || n == 0) {
         cudaGetLastError();
         return false;
     }
-    n = 0;
-    ++g_timeouts;
-    cudaMemcpyToSymbol(tg::g_w4_timeouts, &n, sizeof(n));
-    cudaGetLastError();
+    // shared tiles of the launch may not have had all of their shares
+    g_tc.clear(dev, [&] {
+        n = 0;
+        cudaMemcpyToSymbol(tg::g_w4_timeouts, &n, sizeof(n));
+    });
     return true;
 }
 
