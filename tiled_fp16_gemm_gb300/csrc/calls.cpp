@@ -301,4 +301,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__calls() {
+    PyObject* m = PyModule_Create(&g_module);
+    // also how build.py tells that the file is another PyTorch's
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_against", TG_BUILT_AGAINST) != 0) Py_CLEAR(m);
+    return m;
+}
