@@ -90,15 +90,13 @@ struct W4Step {
     static_assert(kScaleBytes <= 256 && kZeroAt + kZeroBytes <= kBytes, "a step's place");
 };
 
-// Warps that gave up on a wait.
-static __device__ unsigned int g_w4_timeouts;
-
 // What copies under way get to land before a block that gave up on them ends.
 constexpr uint64_t kW4LandNs = 1000000000ull;
 
 struct W4Launch {
     W4Params p;
     uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a warp gives up on a wait
     int32_t inject;    // 1: block 0's first fetch is left out (for tests of the limit)
     int32_t wn, wk;    // tiles of a block at a time, k-pieces
     int32_t tokens;    // rows of A per block
@@ -437,7 +435,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
                     }
         }
     }
-    if (given_up && lane == 0) atomicOr(&g_w4_timeouts, 1u);
+    if (given_up && lane == 0) atomicOr(q.timeouts, kOpTimeoutW4);
     if (q.cluster > 1) {
         w4_cluster_sync();
         const uint32_t from = op_smem(results);

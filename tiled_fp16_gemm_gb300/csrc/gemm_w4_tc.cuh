@@ -66,6 +66,7 @@ struct TcShape {
 struct TcLaunch {
     W4Params p;
     uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a warp gives up on a wait
     int32_t inject;     // 1: block 0's first codes are left out (for tests of the limit)
     int64_t units;      // in all
     int32_t k_units;    // per row block
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
     const uint32_t ready = c_empty + 8 * kTcCodeStages, done = ready + 8 * kTcABufs;
     unsigned char* after = tc_shared + (done + 8 * kTcDone - base);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
-    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out
+    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out: reported at the end
 
     op_release_next();
     if (warp == 0 && lane == 0) {
@@ -251,10 +252,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
         if (__all_sync(0xffffffffu, op_bar_try(bar, parity))) return true;
         const bool ok = *dead == 0 && op_bar_wait_slow(bar, parity, q.limit_ns);
         if (__all_sync(0xffffffffu, ok)) return true;
-        if (lane == 0) {
-            *dead = 1;
-            atomicOr(&g_w4_timeouts, 1u);
-        }
+        if (lane == 0) *dead = 1;
         __syncwarp();
         return false;
     };
@@ -476,6 +474,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
     }
     tc_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && *dead != 0) atomicOr(q.timeouts, kOpTimeoutW4);
     if (warp == 1) {
         tc_after_sync();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tmem_at)

@@ -60,6 +60,7 @@ constexpr int kWideSmem =
 struct WideLaunch {
     W4Params p;
     uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a warp gives up on a wait
     int32_t inject;      // 1: block 0's first codes are left out (for tests of the limit)
     int32_t tokens;      // of a tile: a multiple of 32
     int32_t m_tiles;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t d_full = done + 8 * kTcDone, d_empty = d_full + 8;
     unsigned char* after = shared + (d_empty + 8 - base);
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
-    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out
+    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out: reported at the end
 
     op_release_next();
     if (warp == 0 && lane == 0) {
@@ -304,10 +305,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (__all_sync(0xffffffffu, op_bar_try(bar, parity))) return true;
         const bool ok = *dead == 0 && op_bar_wait_slow(bar, parity, q.limit_ns);
         if (__all_sync(0xffffffffu, ok)) return true;
-        if (lane == 0) {
-            *dead = 1;
-            atomicOr(&g_w4_timeouts, 1u);
-        }
+        if (lane == 0) *dead = 1;
         __syncwarp();
         return false;
     };
@@ -533,6 +531,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     tc_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && *dead != 0) atomicOr(q.timeouts, kOpTimeoutW4);
+    __syncwarp();
     w4_cluster_sync();  // neither block's memory or barriers are used by the other any more
     if (warp == 1) {
         __syncwarp();

@@ -190,19 +190,6 @@ int64_t max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg
 
 }  // namespace
 
-bool tg::norm_take_timeout(int) {
-    unsigned int n = 0;
-    if (cudaMemcpyFromSymbol(&n, tg::g_norm_timeouts, sizeof(n)) != cudaSuccess || n == 0) {
-        cudaGetLastError();
-        return false;
-    }
-    cudaDeviceSynchronize();  // (other streams' launches are in this report)
-    n = 0;
-    cudaMemcpyToSymbol(tg::g_norm_timeouts, &n, sizeof(n));
-    cudaGetLastError();
-    return true;
-}
-
 extern "C" {
 
 tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh,
@@ -390,7 +377,7 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
             auto run = [&](auto kernel) {
                 if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
                 return launch(kernel, grid, r.threads * r.groups, r.smem, split, s, q, r.threads, r.stages,
-                              r.stage_bytes, split, part, tg::op_wait_limit_ns(),
+                              r.stage_bytes, split, part, tg::op_wait_limit_ns(), dev.timeouts,
                               split > 1 ? tg::op_take_inject() : 0);
             };
             if (split > 1)

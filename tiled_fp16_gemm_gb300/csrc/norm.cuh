@@ -241,7 +241,6 @@ __device__ __forceinline__ void norm_commit() {
 
 constexpr int kNormThreads = 512;  // of a block
 constexpr int kNormSplit = 8;      // blocks that share a row, at most
-__device__ unsigned int g_norm_timeouts;  // not 0: a wait for another block ran out
 
 // Until the oldest of the stages - 1 groups under way is there (2 to 4 stages).
 __device__ __forceinline__ void norm_wait(int stages) {
@@ -569,7 +568,7 @@ __device__ __forceinline__ const void* norm_at(const void* p, int col) {
 // before, 0.85 (2048×8192 bf16 92 us against 104).
 template <bool MULTI>
 struct NormPeers {
-    __device__ __forceinline__ NormPeers(int, int, uint64_t, bool) {}
+    __device__ __forceinline__ NormPeers(int, int, uint64_t, unsigned int*, bool) {}
     template <int N>
     __device__ __forceinline__ void add(float (&)[N]) {}
     __device__ __forceinline__ void end() {}
@@ -580,13 +579,15 @@ struct NormPeers<true> {
     uint32_t bars;  // [2]
     int rank, count;
     uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a wait for another block runs out
     bool silent;          // for tests of the limit: the first values are not sent
     bool lost = false;    // a wait ran out: reported; nothing more is sent or waited for
     int turn = 0;         // one exchange's values are still read when the next one's come
     uint32_t parity = 0;  // of both barriers
 
-    __device__ __forceinline__ NormPeers(int rank, int count, uint64_t limit_ns, bool silent)
-        : rank(rank), count(count), limit_ns(limit_ns), silent(silent) {
+    __device__ __forceinline__ NormPeers(int rank, int count, uint64_t limit_ns, unsigned int* timeouts,
+                                         bool silent)
+        : rank(rank), count(count), limit_ns(limit_ns), timeouts(timeouts), silent(silent) {
         __shared__ __align__(16) float room[2 * kNormSplit * 8];
         __shared__ __align__(8) unsigned long long two[2];
         values = room;
@@ -623,7 +624,7 @@ struct NormPeers<true> {
         silent = false;
         if (!lost && !op_bar_wait(bar, parity, limit_ns)) {
             lost = true;
-            atomicOr(&g_norm_timeouts, 1u);
+            atomicOr(timeouts, kOpTimeoutNorm);
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = all[k];
@@ -660,7 +661,7 @@ struct NormPeers<true> {
 template <typename TX, typename TR, bool VEC, bool MULTI>
 __global__ void __launch_bounds__(kNormThreads)
     tg_norm_grad_rows(const NormGradParams q, int threads, int stages, int stage_bytes, int split,
-                      int part, uint64_t limit_ns, int inject) {
+                      int part, uint64_t limit_ns, unsigned int* timeouts, int inject) {
     constexpr int CH = 1;
     extern __shared__ __align__(16) unsigned char norm_stage[];
     __shared__ __align__(16) float red[8 * 160];
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(kNormThreads)
     int cols = static_cast<int>(p.cols) - c0;
     if (MULTI && cols > part) cols = part;
     const NormCols<CH, VEC> c{g.tid, g.threads, cols};
-    NormPeers<MULTI> peers(rank, split, limit_ns, inject == 1 && blockIdx.x == 1);
+    NormPeers<MULTI> peers(rank, split, limit_ns, timeouts, inject == 1 && blockIdx.x == 1);
     const float* const wpost = p.wpost != nullptr ? p.wpost + c0 : nullptr;
     const float* const wpre = p.wpre != nullptr ? p.wpre + c0 : nullptr;
     const float inv = 1.0f / static_cast<float>(p.cols);

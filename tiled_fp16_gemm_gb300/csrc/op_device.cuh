@@ -39,6 +39,10 @@ __device__ __forceinline__ void op_release_next() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Bits of the device's word for waits that ran out (the GEMM's kernels have the low ones).
+constexpr unsigned int kOpTimeoutW4 = 1u << 16;
+constexpr unsigned int kOpTimeoutNorm = 1u << 17;
+
 // ------------------------------------------------------------------ mbarriers and TMA
 
 __device__ __forceinline__ uint32_t op_smem(const void* p) {

@@ -24,12 +24,17 @@ constexpr int64_t kOpMaxDim = 2147483647LL;
 struct OpDevice {
     int dev = 0;
     int num_sms = 0;
+    unsigned int* timeouts = nullptr;  // the device's word for waits that ran out
 };
+
+// That word of the current device, which tg_sync_status reads; null on an error.  In tgemm.cu.
+unsigned int* op_timeout_word();
 
 // The current device, if it is an sm_103 one (probed once per device).
 inline tg_status_t op_device(OpDevice* out) {
     static std::mutex m;
     static int sms[kOpMaxDevices] = {};  // 0: not probed, -1: another architecture
+    static unsigned int* words[kOpMaxDevices] = {};
     int d = -1;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kOpMaxDevices) {
         cudaGetLastError();
@@ -47,8 +52,10 @@ inline tg_status_t op_device(OpDevice* out) {
         sms[d] = major == 10 && minor == 3 ? n : -1;
     }
     if (sms[d] < 0) return TG_ERR_UNSUPPORTED_DEVICE;
+    if (words[d] == nullptr && (words[d] = op_timeout_word()) == nullptr) return TG_ERR_LAUNCH;
     out->dev = d;
     out->num_sms = sms[d];
+    out->timeouts = words[d];
     return TG_OK;
 }
 
@@ -58,11 +65,9 @@ uint64_t op_wait_limit_ns();
 // The mode that tg_debug_inject set for the next launch, which is then 0 again.
 int32_t op_take_inject();
 
-// Whether a kernel of w4.cu or norm.cu gave up on a wait since the last call, on the
-// current device `dev`.  Where one did, everything queued on the device is let end first,
-// and counters that it may have left are cleared.
-bool w4_take_timeout(int dev);
-bool norm_take_timeout(int dev);
+// After a wait ran out on `dev`, the current device: clears counters that a kernel of w4.cu
+// may have left, once everything queued there has ended.
+void w4_clear_counters(int dev);
 
 // Whether `encode`, a call of cuTensorMapEncodeTiled, succeeds.  That needs a current context,
 // which a host thread does not have before its first call that binds one: then it is bound here.
@@ -160,16 +165,14 @@ class OpWorkspace {
     }
 
     // Zeroes the counters of all buffers of `dev`, the current device, those that became
-    // too small too (captured graphs may use them), and calls `also`, once everything
-    // queued there has ended.  No call is between get() and its last launch meanwhile.
-    template <typename F>
-    void clear(int dev, F also) {
+    // too small too (captured graphs may use them), once everything queued there has
+    // ended.  No call is between get() and its last launch meanwhile.
+    void clear(int dev) {
         std::lock_guard<std::mutex> lk(m_);
         std::vector<Hold> holds;
         for (auto& of : of_)
             if (std::get<0>(of.first) == dev) holds.emplace_back(of.second.m);
         cudaDeviceSynchronize();
-        also();
         for (auto& of : of_)
             if (std::get<0>(of.first) == dev)
                 for (void* p : of.second.all) cudaMemset(p, 0, counters_);

@@ -997,6 +997,14 @@ tg_status_t plan_limited(int64_t M, int64_t N, int64_t K, const PlanLimits& lim,
 
 uint64_t tg::op_wait_limit_ns() { return g_timeout_ns.load(); }
 int32_t tg::op_take_inject() { return g_inject.exchange(0); }
+unsigned int* tg::op_timeout_word() {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, tg::g_wait_timeout_flags) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return static_cast<unsigned int*>(p);
+}
 
 // ====================================================================== C ABI
 
@@ -1288,19 +1296,17 @@ tg_status_t tg_sync_status(void* stream) {
     }
     if (flags != 0) {
         // A kernel gave up early: let every queued kernel finish, then clear
-        // the split-K counters it may have left non-zero before anything reuses them.
+        // the counters it may have left non-zero before anything reuses them.
         cudaDeviceSynchronize();
         const unsigned int zero = 0;
         cudaMemcpyToSymbol(tg::g_wait_timeout_flags, &zero, sizeof(zero));
         tg::splitk_reset_counters(dev);
         noalloc_reset_counters(dev);
         cudaGetLastError();
-        tg::w4_take_timeout(dev);
-        tg::norm_take_timeout(dev);
+        tg::w4_clear_counters(dev);
         return TG_ERR_TIMEOUT;
     }
-    const bool w4 = tg::w4_take_timeout(dev), norm = tg::norm_take_timeout(dev);
-    return w4 || norm ? TG_ERR_TIMEOUT : TG_OK;
+    return TG_OK;
 }
 
 }  // extern "C"

@@ -174,6 +174,7 @@ tg_status_t launch_tiles(const W4Params& p, const tg::OpDevice& dev, cudaStream_
     }
     by_m = (p.M + best.tokens - 1) / best.tokens;
     best.limit_ns = tg::op_wait_limit_ns();
+    best.timeouts = dev.timeouts;
     best.inject = tg::op_take_inject();
     using Step = tg::W4Step<G>;
     constexpr CUtensorMapDataType type =
@@ -219,6 +220,7 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
     tg::TcLaunch q;
     q.p = p;
     q.limit_ns = tg::op_wait_limit_ns();
+    q.timeouts = dev.timeouts;
     q.inject = 0;
     q.k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     q.units = (p.N + tg::kTcRows - 1) / tg::kTcRows * q.k_units;
@@ -312,6 +314,7 @@ tg_status_t launch_wide(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
     std::memset(&q, 0, sizeof(q));
     q.p = p;
     q.limit_ns = tg::op_wait_limit_ns();
+    q.timeouts = dev.timeouts;
     plan_wide(p, lim.clusters, &q);
     const int64_t blocks = int64_t{q.clusters} * tg::kWideCluster;
     if (blocks * 32 > kCounterBytes) return TG_ERR_UNSUPPORTED_DEVICE;
@@ -404,19 +407,7 @@ tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_e
 
 }  // namespace
 
-bool tg::w4_take_timeout(int dev) {
-    unsigned int n = 0;
-    if (cudaMemcpyFromSymbol(&n, tg::g_w4_timeouts, sizeof(n)) != cudaSuccess || n == 0) {
-        cudaGetLastError();
-        return false;
-    }
-    // shared tiles of the launch may not have had all of their shares
-    g_tc.clear(dev, [&] {
-        n = 0;
-        cudaMemcpyToSymbol(tg::g_w4_timeouts, &n, sizeof(n));
-    });
-    return true;
-}
+void tg::w4_clear_counters(int dev) { g_tc.clear(dev); }
 
 extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* Bq,
                                   const void* Bscale, const void* Bzero, void* C, int64_t M,
