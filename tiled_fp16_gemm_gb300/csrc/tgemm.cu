@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <map>
 #include <cstdint>
@@ -336,8 +337,10 @@ constexpr CUtensorMapDataType tensor_map_type() {
 // (no device or allocation state), so an entry stays valid for any later
 // call with the same key, whatever happened to the memory in between.  A
 // repeated call (same pointers, shape and leading dimensions) then skips the
-// encoding of its maps.  The table is direct-mapped: a colliding key
-// replaces the entry, so its size is fixed.
+// encoding of its maps.  The table has a fixed size: a key may be in any of the
+// kMapCacheWays entries of its set, and a new one replaces the one that was
+// not used for longest.  (A call makes up to four maps: with one place for
+// each they could push one another out at every call.)
 struct MapKey {
     const void* ptr;
     uint64_t inner, outer, row_bytes;
@@ -351,24 +354,28 @@ struct MapKey {
 };
 
 struct MapEntry {
-    bool used = false;
+    uint64_t used = 0;  // when, counted in the set's uses; 0: empty
     MapKey key{};
     CUtensorMap map{};
 };
 
-constexpr int kMapCacheSlots = 1024;
+constexpr int kMapCacheSets = 256, kMapCacheWays = 4;
+struct MapSet {
+    MapEntry way[kMapCacheWays];
+    uint64_t uses = 0;
+};
 std::mutex g_map_mutex;
-MapEntry g_map_cache[kMapCacheSlots];
+MapSet g_map_cache[kMapCacheSets];
 std::atomic<uint64_t> g_map_hits{0}, g_map_misses{0};
 
-uint32_t map_slot(const MapKey& k) {
+uint32_t map_set(const MapKey& k) {
     uint64_t h = reinterpret_cast<uintptr_t>(k.ptr) * 0x9E3779B97F4A7C15ull;
     const uint64_t f[] = {k.inner, k.outer, k.row_bytes,
                           (uint64_t{k.box_inner} << 32) | k.box_outer,
                           (static_cast<uint64_t>(static_cast<uint32_t>(k.dtype)) << 32) |
                               static_cast<uint32_t>(k.swizzle)};
     for (uint64_t v : f) h = (h ^ v) * 0x100000001B3ull + (h >> 29);
-    return static_cast<uint32_t>((h ^ (h >> 32)) % kMapCacheSlots);
+    return static_cast<uint32_t>((h ^ (h >> 32)) % kMapCacheSets);
 }
 
 // 2-D tensor map: inner (contiguous) extent, outer extent, row stride in
@@ -387,15 +394,16 @@ bool encode_2d_sw(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t ou
     key.box_outer = box_outer;
     key.dtype = static_cast<int32_t>(dtype);
     key.swizzle = static_cast<int32_t>(swizzle);
-    const uint32_t slot = map_slot(key);
+    MapSet& set = g_map_cache[map_set(key)];
     {
         std::lock_guard<std::mutex> lk(g_map_mutex);
-        const MapEntry& e = g_map_cache[slot];
-        if (e.used && e.key == key) {
-            *map = e.map;
-            g_map_hits.fetch_add(1, std::memory_order_relaxed);
-            return true;
-        }
+        for (MapEntry& e : set.way)
+            if (e.used != 0 && e.key == key) {
+                e.used = ++set.uses;
+                *map = e.map;
+                g_map_hits.fetch_add(1, std::memory_order_relaxed);
+                return true;
+            }
     }
     auto enc = get_encode();
     if (!enc) return false;
@@ -411,8 +419,9 @@ bool encode_2d_sw(CUtensorMap* map, const void* ptr, uint64_t inner, uint64_t ou
         return false;
     g_map_misses.fetch_add(1, std::memory_order_relaxed);
     std::lock_guard<std::mutex> lk(g_map_mutex);
-    MapEntry& e = g_map_cache[slot];
-    e.used = true;
+    MapEntry& e = *std::min_element(set.way, set.way + kMapCacheWays,
+                                    [](const MapEntry& a, const MapEntry& b) { return a.used < b.used; });
+    e.used = ++set.uses;
     e.key = key;
     e.map = *map;
     return true;
