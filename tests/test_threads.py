@@ -134,3 +134,60 @@ def test_staged_products_of_two_threads(tg, M, N, K, mx):
     tg.sync_status()
     for out, want in zip(results, wanted):
         assert torch.equal(out, want.expand_as(out))
+
+
+PER_THREAD = 2  # cudaStreamPerThread: one handle, a stream for each thread
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(16, 512, 8192), (40, 512, 1031), (2048, 2048, 1024)])
+def test_products_on_the_threads_own_streams(tg, M, N, K):
+    """Streams of two threads overlap, though their handle is the same: each has buffers of its
+    own (partial sums of k-pieces, staged operands)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    calls, results, wanted = [], [], []
+    for _ in range(2):
+        a = torch.randn(M, K, generator=g, device="cuda").half()
+        b = torch.randn(K, N, generator=g, device="cuda").half()
+        wanted.append(tg.gemm(a, b))
+        out = torch.zeros(50, M, N, device="cuda", dtype=torch.half)
+        results.append(out)
+
+        def call(i, a=a, b=b, out=out):
+            st = tg.tg_gemm_f16(a.data_ptr(), b.data_ptr(), out[i % 50].data_ptr(), M, N, K, K, N, N, 0, PER_THREAD)
+            assert st == tg.TG_OK
+
+        calls.append(call)
+    torch.cuda.synchronize()
+    in_threads(calls, 500)
+    torch.cuda.synchronize()
+    tg.sync_status()
+    for out, want in zip(results, wanted):
+        assert torch.equal(out, want.expand_as(out))
+
+
+@pytest.mark.gpu
+def test_host_products_on_the_threads_own_streams(tg):
+    import numpy as np
+    import torch
+    M, N, K = 64, 1500, 512
+    calls, results, wanted = [], [], []
+    for seed in range(2):
+        r = np.random.RandomState(seed)
+        a, b = (r.uniform(-1, 1, s).astype(np.float16) for s in ((M, K), (K, N)))
+        wanted.append(tg.gemm(torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda()).cpu().numpy())
+        out = np.zeros((20, M, N), np.float16)
+        results.append(out)
+
+        def call(i, a=a, b=b, out=out):
+            c = out[i % 20]
+            st = tg.tg_gemm_f16_host(a.ctypes.data, b.ctypes.data, c.ctypes.data, M, N, K, K, N, N, 0, PER_THREAD)
+            assert st == tg.TG_OK
+
+        calls.append(call)
+    in_threads(calls, 100)
+    torch.cuda.synchronize()
+    tg.sync_status()
+    for out, want in zip(results, wanted):
+        assert all(np.array_equal(c, want) for c in out)

@@ -52,6 +52,7 @@
 #include "gemm_persistent.cuh"
 #include "mxfp4.cuh"
 #include "sm103_ptx.cuh"
+#include "stream_key.h"
 #include "tile_schedule.h"
 #include "tgemm.h"
 
@@ -1069,8 +1070,8 @@ inline std::mutex& splitk_ws_mutex() {
     return m;
 }
 
-inline std::map<std::pair<int, cudaStream_t>, SplitkWorkspace>& splitk_ws_map() {
-    static std::map<std::pair<int, cudaStream_t>, SplitkWorkspace> m;
+inline std::map<StreamKey, SplitkWorkspace>& splitk_ws_map() {
+    static std::map<StreamKey, SplitkWorkspace> m;
     return m;
 }
 
@@ -1080,7 +1081,7 @@ inline std::map<std::pair<int, cudaStream_t>, SplitkWorkspace>& splitk_ws_map() 
 inline void splitk_reset_counters(int dev) {
     std::lock_guard<std::mutex> lk(splitk_ws_mutex());
     for (auto& kv : splitk_ws_map())
-        if (kv.first.first == dev && kv.second.counters != nullptr)
+        if (std::get<0>(kv.first) == dev && kv.second.counters != nullptr)
             cudaMemset(kv.second.counters, 0, 4 * kv.second.ctas * sizeof(uint32_t));
 }
 
@@ -1093,7 +1094,7 @@ inline tg_status_t splitk_workspace(int dev, cudaStream_t stream, int64_t grid, 
                                     SkinnyParams* prm) {
     {
         std::lock_guard<std::mutex> lk(splitk_ws_mutex());
-        SplitkWorkspace& ws = splitk_ws_map()[std::make_pair(dev, stream)];
+        SplitkWorkspace& ws = splitk_ws_map()[stream_key(dev, stream)];
         if (ws.ctas < grid) {
             // First use on this stream: room for the largest grid (one CTA
             // per SM), so later calls, graph captures included, never grow it.

@@ -7,13 +7,12 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <functional>
 #include <map>
 #include <mutex>
-#include <thread>
 #include <tuple>
 #include <vector>
 
+#include "stream_key.h"
 #include "tgemm.h"
 
 namespace tg {
@@ -125,13 +124,10 @@ class OpWorkspace {
     explicit OpWorkspace(size_t counters = 0) : counters_(counters) {}
 
     tg_status_t get(int dev, cudaStream_t s, size_t bytes, void** out, Hold* hold) {
-        // the per-thread default stream is one handle for a stream per thread
-        const size_t thread =
-            s == cudaStreamPerThread ? std::hash<std::thread::id>{}(std::this_thread::get_id()) : 0;
         Buffer* found;
         {
             std::lock_guard<std::mutex> lk(m_);
-            found = &of_[std::make_tuple(dev, s, thread)];  // (entries stay where they are)
+            found = &of_[stream_key(dev, s)];  // (entries stay where they are)
         }
         Buffer& b = *found;
         *hold = Hold(b.m);
@@ -188,7 +184,7 @@ class OpWorkspace {
     };
     const size_t counters_;
     std::mutex m_;
-    std::map<std::tuple<int, cudaStream_t, size_t>, Buffer> of_;
+    std::map<StreamKey, Buffer> of_;
 };
 
 }  // namespace tg

@@ -648,13 +648,13 @@ struct Staging {
     void* ptr = nullptr;
     size_t bytes = 0;
 };
-using StagingMap = std::map<std::pair<int, cudaStream_t>, Staging>;
+using StagingMap = std::map<tg::StreamKey, Staging>;
 std::mutex g_staging_mutex;
 StagingMap g_staging;
 
 Staging& staging_of(std::mutex& m, StagingMap& of, int dev, cudaStream_t s) {
     std::lock_guard<std::mutex> lk(m);
-    return of[std::make_pair(dev, s)];  // (entries stay where they are)
+    return of[tg::stream_key(dev, s)];  // (entries stay where they are)
 }
 
 tg_status_t staging_get(Staging& st, cudaStream_t s, size_t bytes, void** out, StagingHold* hold) {
@@ -1344,7 +1344,7 @@ struct HostPipeline {
 };
 
 std::mutex g_host_mutex;
-std::map<std::pair<int, cudaStream_t>, HostPipeline> g_host;
+std::map<tg::StreamKey, HostPipeline> g_host;
 
 // Grow one device copy to `need` bytes.  Earlier calls on this pipeline may
 // still read or write the old buffer: `stream` (which every call leaves
@@ -1399,7 +1399,7 @@ extern "C" tg_status_t tg_gemm_f16_host(const void* A, const void* B, void* C, i
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
     std::lock_guard<std::mutex> lk(g_host_mutex);
-    HostPipeline& hp = g_host[std::make_pair(dev, s)];
+    HostPipeline& hp = g_host[tg::stream_key(dev, s)];
     if ((st = host_pipeline_init(hp)) != TG_OK) return st;
     // Device copies: row strides rounded up to 8 elements (16-byte rows).
     const int64_t Kp = round_up8(K), Np = round_up8(N);
