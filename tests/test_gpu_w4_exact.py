@@ -64,7 +64,7 @@ def check_integers(tg, M, N, K, dtype, group, zeros, pad=0):
 @pytest.mark.parametrize("M,N,K", [(1, 28672, 4096), (1, 4096, 28672), (8, 16384, 8192), (16, 4096, 28672),
                                    (33, 16384, 8192), (64, 16384, 8192), (65, 16384, 8192),
                                    (200, 16384, 8192), (512, 16384, 8192), (700, 4096, 28672),
-                                   (7000, 16384, 8192), (100, 512, 2048)])
+                                   (7000, 16384, 8192), (4096, 512, 2048)])
 def test_integers_at_layer_sizes(tg, M, N, K, dtype, group, zeros):
     """The last two take the way over decoded weights with a 16-bit result."""
     check_integers(tg, M, N, K, dtype, group, zeros)
@@ -96,3 +96,18 @@ def test_a_single_one_gives_a_weight(tg, M, dtype, group, zeros):
         c = tg.gemm_w4(a, bq, bscale, N, group, bzero=bzero, out_dtype=out_dtype)
         assert torch.equal(c, want.to(c.dtype))
     tg.sync_status()
+
+
+@pytest.mark.parametrize("M,N,K,decoded", [(100, 512, 2048, False), (257, 600, 4096, False), (1500, 512, 4096, False),
+                                           (5000, 512, 4096, True), (6000, 1024, 1024, True)])
+def test_which_products_decode_their_weights_to_memory(tg, M, N, K, decoded):
+    """Those of very many rows: their product is a dense GEMM launch."""
+    a = torch.zeros(M, K, device="cuda", dtype=HALF)
+    bq = torch.zeros(N, K // 2, device="cuda", dtype=torch.uint8)
+    scale = torch.ones(K // 128, N, device="cuda", dtype=HALF)
+    x = torch.zeros(8, 8, device="cuda", dtype=HALF)
+    tg.gemm(x, x)
+    before = tg.tg_debug_last_launch()
+    tg.gemm_w4(a, bq, scale, N, 128)
+    after = tg.tg_debug_last_launch()
+    assert (bytes(after) != bytes(before)) == decoded

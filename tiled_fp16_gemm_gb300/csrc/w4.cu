@@ -383,12 +383,15 @@ tg_status_t launch_zero(const W4Params& p, const tg::OpDevice& dev, cudaStream_t
                              : launch_group<T, G, false>(p, dev, s);
 }
 
-// Many rows, a 16-bit result: whether the weights are decoded to T in memory and the dense
-// GEMM runs on them.  With B MB of codes that takes about 10 us + 1.5·B and the GEMM at
-// 1800 TFLOP/s; tg_gemm_w4_wide, decoding every weight once for 256 rows, does not pass
-// 1600 in long runs (4096 rows of 1024×1024: 13 us against 17, of 16384×8192: 712 against
-// 700).
+// Very many rows, a 16-bit result: whether the weights are decoded to T in memory and the
+// dense GEMM runs on them.  With B MB of codes that takes about 10 us + 1.5·B and the GEMM at
+// 1800 TFLOP/s; tg_gemm_w4_wide decodes every weight once for 256 rows, which costs it a tenth
+// of that rate.  Measured, dense / wide: 16384×8192 with 2048 / 4096 / 6000 / 8192 rows
+// 437 / 791 / 1156 / 1508 us against 386 / 801 / 1208 / 1653, 512×4096 with 3000 22.5 us against
+// 25.2, 1024×1024 with 6000 17.0 against 21.3.  Below 2048 rows the model does not hold for the
+// dense GEMM of small weights (512×2048 with 100 rows 30 us against 11).
 bool prefer_dense(const W4Params& p, const tg::OpDevice& dev) {
+    if (p.M < 2048) return false;
     tg::WideLaunch q;
     const double nk = static_cast<double>(p.N) * static_cast<double>(p.K);
     const double flops = 2.0 * nk * static_cast<double>(p.M);
@@ -399,7 +402,7 @@ bool prefer_dense(const W4Params& p, const tg::OpDevice& dev) {
 template <typename T>
 tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
                         const tg::OpDevice& dev, cudaStream_t s) {
-    if (p.M > 64 && !p.out_f32 && prefer_dense(p, dev)) return launch_dense<T>(in_dtype, p, x, dev, s);
+    if (!p.out_f32 && prefer_dense(p, dev)) return launch_dense<T>(in_dtype, p, x, dev, s);
     if (p.group == 32) return launch_zero<T, 32>(p, dev, s);
     if (p.group == 64) return launch_zero<T, 64>(p, dev, s);
     return launch_zero<T, 128>(p, dev, s);
