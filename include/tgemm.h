@@ -20,8 +20,9 @@
  *     warp-specialised producer and consumer.
  *
  * Threading: every entry point is thread-safe.  Calls on the same stream are
- * ordered; calls on different streams may overlap (each stream gets its own
- * split-K workspace).
+ * ordered, and the launches of one call stay together; calls on different
+ * streams may overlap (each stream gets its own workspaces, and so does each
+ * host thread's cudaStreamPerThread).
  */
 #ifndef TGEMM_H
 #define TGEMM_H

@@ -743,7 +743,9 @@ def norm_residual(x, residual=None, *, post_weight=None, gate=None, scale: float
     optional tensor of x's dtype, cols values for all rows or G rows of them,
     each for rows / G consecutive rows of x.  y is written to ``out`` (which may
     be ``residual`` itself) and h to ``normed`` where given.  Runs on ``stream``
-    (default: torch's current stream of x's device).
+    (default: torch's current stream of x's device).  Like every result of this
+    library y and h carry no autograd graph: their gradient is
+    ``norm_residual_backward``.
     """
     if _torch is None:
         _bind()

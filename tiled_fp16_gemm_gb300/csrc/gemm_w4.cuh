@@ -68,9 +68,11 @@ __device__ __forceinline__ void w4_store(const W4Params& p, int64_t m, int64_t n
 // the tiles and split k, and join over distributed shared memory at the end.  All sums
 // are joined in a fixed order, with no scratch in global memory.
 //
-// Measured, one row: 28672×4096 bf16, G = 128, 18.3 us; 16384×8192 fp16 18.1 us (3.4 and
-// 3.8 TB/s); 4096×28672 fp16, G = 32, 21.1 us; 1024×1024 3.6 us.  8 rows of 16384×8192
-// 24.6 us.  Bound by issue: some 350 instructions for 4096 codes at 2.1 to 2.3 a cycle.
+// Measured, one row: 28672×4096 bf16, G = 128, 18.5 us; 16384×8192 fp16 18.5 us (3.3 and
+// 3.8 TB/s); 4096×28672 fp16, G = 32, 18.4 us; 1024×1024 3.7 us.  8 rows of 16384×8192
+// 23.8 us.  Bound by latency: some 350 instructions for 4096 codes, issued at 2.1 to 2.3 of
+// the 4 a cycle that an SM could; its 16 warps (96 to 128 registers) do not cover the way
+// from a load over the decoding to the MMA.
 
 constexpr int kW4Warps = 16;
 constexpr int kW4Threads = 32 * kW4Warps;

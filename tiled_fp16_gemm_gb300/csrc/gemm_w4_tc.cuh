@@ -27,8 +27,8 @@
 // back, release), about 0.4 us with 16 columns, where an SM could get the unit's codes in
 // 0.19.  A wait costs 80 to 110 cycles even when there is nothing to wait for, so the MMA
 // warp has one barrier for all that a unit needs.  Measured: 16384×8192, G = 128, 16 / 32 /
-// 64 rows 28.6 / 32.9 / 41.8 us (2.5 / 2.1 / 1.7 TB/s; with three barriers per unit 31.0 /
-// 34.3 / 45.4), G = 32 with 64 rows 53 us (one accumulator only).
+// 64 rows 28.8 / 32.8 / 41.4 us (2.5 / 2.1 / 1.7 TB/s; with three barriers per unit 31.0 /
+// 34.3 / 45.4), G = 32 with 64 rows 52 us (one accumulator only).
 #pragma once
 
 #include "gemm_w4.cuh"

@@ -23,11 +23,11 @@
 // 1070 with 256 tokens (the MMAs bound it) and 780 with 128 (the codes' arrival does).  An
 // arrival at the even block with release.cluster cost 1900 cycles; the plain form does not.
 //
-// Measured, 16384×8192, fp16, G = 128: 65 / 128 / 256 / 512 / 2048 rows 34 / 35 / 45 / 85 /
-// 329 us; the last two are 1600 and 1670 TFLOP/s.  (Decoding to memory, then the dense GEMM:
-// 160 us for 256 rows, 193 for 512.)  At 512 rows 64 of the 76 pairs work, on whole tiles.
-// With an fp32 result 65 / 128 / 256 / 512 rows 40 / 44 / 80 / 147 us (by passes of 64 rows
-// through gemm_w4_tc.cuh 62 / 84 / 170 / 340).
+// Measured, 16384×8192, fp16, G = 128: 65 / 128 / 256 / 512 / 2048 rows 34 / 35 / 47 / 87 /
+// 324 us; the last two are 1580 and 1700 TFLOP/s.  (In long runs, under the power cap, 91 and
+// 365 us.  Decoding to memory, then the dense GEMM: 160 us for 256 rows, 193 for 512.)  At 512
+// rows 64 of the 76 pairs work, on whole tiles.  With an fp32 result 65 / 128 / 256 / 512 rows
+// 41 / 46 / 81 / 149 us (by passes of 64 rows through gemm_w4_tc.cuh 62 / 84 / 170 / 340).
 //
 // Roles of a block's 24 warps (all meet on mbarriers):
 //   0             fetches codes, scales and zero points by TMA

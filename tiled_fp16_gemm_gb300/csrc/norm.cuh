@@ -649,10 +649,10 @@ struct NormPeers<true> {
 // itself.  Else the groups of a block take its rows in turn, and the block's share
 // of a gate's gradient is joined whenever a gate's rows end.
 //
-// Bound by issue and by the reductions' latency, one block of 512 threads on an SM: its
-// registers hold the sums.  8192×4096 bf16 112 us (3.6 TB/s), fp32 stream 131 us (4.6);
-// 1021×5119 fp16, unaligned, a gate per row, 62 us; 2048×8192 and 2048×16000 bf16 92 and
-// 194 us.
+// Bound by latency, that of the reductions above all: one block of 512 threads on an SM (its
+// registers hold the sums) issues 2.2 of 4 instructions a cycle.  8192×4096 bf16 112 us
+// (3.6 TB/s), fp32 stream 132 us (4.6); 1021×5119 fp16, unaligned, a gate per row, 63 us;
+// 2048×8192 and 2048×16000 bf16 91 and 192 us.
 //
 // MULTI: the `split` blocks of a cluster share their rows, `part` columns each (the last
 // one the rest), and add up their sums: for rows of more columns than a block's threads
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(kNormThreads)
 //
 // What the rings do not hold: a forward row of more than 16384 columns, or of fp32 values
 // that do not fit twice; strides of 2^32 elements; 2^31 rows.  Values are read again for
-// each pass, from L2 (2048×16000 bf16, gradient: 1.8 ms, 194 us by the rings).
+// each pass, from L2 (2048×16000 bf16, gradient: 1.8 ms, 192 us by the rings).
 
 // Row by row, the unrounded y of the row in shared memory.
 template <typename TX, typename TR>

@@ -263,7 +263,7 @@ tg_status_t launch_tc(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s
 // that time in us.  Measured: a unit takes 2.4 ns per token, and 0.43 us at least (what the
 // codes take to come and be decoded); a tile that is shared 4 us + 18 ns per token and share
 // more; A in order 4 bytes an element at 4 TB/s.  16384×8192 with 65 / 128 / 192 / 256 / 512
-// rows: 34 / 36 / 38 / 46 / 86 us, on 64 of 76 pairs, with whole tiles.
+// rows: 34 / 35 / 38 / 47 / 87 us, on 64 of 76 pairs, with whole tiles.
 double plan_wide(const W4Params& p, int64_t limit, tg::WideLaunch* q) {
     q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
@@ -363,6 +363,9 @@ bool prefer_tc(const W4Params& p) {
     return 7.0 + (p.M <= 32 ? 0.3 : 0.5) * mb < 3.0 + 0.53 * static_cast<double>((p.M + 15) / 16) * mb;
 }
 
+// Up to 64 rows no weight is rounded, and the kernels are those that need not.  (64 is not where
+// the times cross: the pair kernel without rounding takes 65 rows of 16384×8192 in 41 us with
+// G = 128 and 45 with G = 32, tg_gemm_w4_tc 64 rows in 41 and 52.)
 template <typename T, int G, bool ZERO>
 tg_status_t launch_group(const W4Params& p, const tg::OpDevice& dev, cudaStream_t s) {
     if (p.M > 64)
