@@ -111,3 +111,20 @@ def test_which_products_decode_their_weights_to_memory(tg, M, N, K, decoded):
     tg.gemm_w4(a, bq, scale, N, 128)
     after = tg.tg_debug_last_launch()
     assert (bytes(after) != bytes(before)) == decoded
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 8192, 8192), (5, 4096, 8192), (8, 8192, 4096), (16, 1024, 4096),
+                                   (40, 512, 2048)])
+@pytest.mark.parametrize("dtype,group,zeros", KINDS)
+def test_weights_in_turn(tg, M, N, K, dtype, group, zeros):
+    """Two weights in turn, again and again: a stage of a warp's ring that is filled again
+    before all lanes have read it would show in some sum."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a = torch.randint(-2, 3, (M, K), generator=g, device="cuda").to(dtype)
+    both = [weights(N, K, dtype, group, zeros, g,
+                    lambda r, c: 2.0 ** torch.randint(-3, 1, (r, c), generator=g, device="cuda").float())
+            for _ in range(2)]
+    want = [(a.double() @ ops64.w4_weight(*w, N, K, group).T).float() for w in both]
+    got = [tg.gemm_w4(a, bq, s, N, group, bzero=z, out_dtype=F32) for _ in range(25) for bq, s, z in both]
+    for i, c in enumerate(got):
+        assert torch.equal(c, want[i % 2])

@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
                     given_up = true;
                     lost = !op_bar_wait(bars + 8 * slot, parity, kW4LandNs);
                 }
-                lost = __any_sync(0xffffffffu, lost);  // (and all lanes have read the slot before)
+                lost = __any_sync(0xffffffffu, lost);
+                __syncwarp();  // all lanes have read the slot before, which is filled again
                 if (!lost) fetch();
                 const uint32_t at = ring + slot * Step::kBytes;
                 const uint32_t wl = at + w_lane;
