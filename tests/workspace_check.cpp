@@ -9,6 +9,15 @@
 
 #include "op_host.h"
 
+static thread_local bool g_fail_new = false;
+void* operator new(size_t n) {
+    void* p = g_fail_new ? nullptr : std::malloc(n);
+    if (p == nullptr) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, size_t) noexcept { std::free(p); }
+
 extern "C" {
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 cudaError_t cudaMalloc(void** p, size_t bytes) {
@@ -108,6 +117,30 @@ int main() {
             std::printf("FAIL buffer %d after the clearing: %d %d\n", i, at[i][0], at[i][256]);
             return 1;
         }
+    // No exception leaves an entry point.
+    if (tg::op_entry([]() -> tg_status_t { throw std::bad_alloc(); }) != TG_ERR_NO_MEMORY ||
+        tg::op_entry([]() -> tg_status_t { throw 1; }) != TG_ERR_LAUNCH ||
+        tg::op_entry([] { return TG_ERR_MISALIGNED; }) != TG_ERR_MISALIGNED) {
+        std::printf("FAIL exceptions\n");
+        return 1;
+    }
+    // Nor that of a workspace whose bookkeeping finds no host memory: later calls go on.
+    tg::OpWorkspace poor;
+    void* r = nullptr;
+    g_fail_new = true;
+    const tg_status_t none = tg::op_entry([&] {
+        tg::OpWorkspace::Hold hold;
+        return poor.get(0, stream(1), 64, &r, &hold);
+    });
+    g_fail_new = false;
+    const tg_status_t then = tg::op_entry([&] {
+        tg::OpWorkspace::Hold hold;
+        return poor.get(0, stream(1), 64, &r, &hold);
+    });
+    if (none != TG_ERR_NO_MEMORY || then != TG_OK || r == nullptr) {
+        std::printf("FAIL without host memory: %d, then %d\n", none, then);
+        return 1;
+    }
     std::printf("OK\n");
     return 0;
 }

@@ -190,10 +190,8 @@ int64_t max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg
 
 }  // namespace
 
-extern "C" {
-
-tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh,
-                             void* stream) {
+static tg_status_t norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh,
+                                 void* stream) {
     NormParams p;
     tg_status_t st = check_norm(a, &p);
     if (st != TG_OK) return st;
@@ -254,7 +252,7 @@ tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, 
     });
 }
 
-tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* b, void* stream) {
+static tg_status_t norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* b, void* stream) {
     NormGradParams q;
     std::memset(&q, 0, sizeof(q));
     if (b == nullptr) return TG_ERR_INVALID_VALUE;
@@ -399,6 +397,17 @@ tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* 
                            static_cast<unsigned>(jobs < 1024 ? jobs : 1024)),
                       512, 0, 1, s, q, blocks, jobs);
     });
+}
+
+extern "C" {
+
+tg_status_t tg_norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh,
+                             void* stream) {
+    return tg::op_entry([&] { return norm_residual(a, y, ldy, h, ldh, stream); });
+}
+
+tg_status_t tg_norm_residual_backward(const tg_norm_t* a, const tg_norm_grad_t* b, void* stream) {
+    return tg::op_entry([&] { return norm_residual_backward(a, b, stream); });
 }
 
 }  // extern "C"

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 #include <vector>
 
@@ -16,6 +17,19 @@
 #include "tgemm.h"
 
 namespace tg {
+
+// The body of a C entry point: no exception leaves it (a host allocation that fails, in a
+// workspace's bookkeeping, is one).
+template <typename F>
+tg_status_t op_entry(F body) noexcept {
+    try {
+        return body();
+    } catch (const std::bad_alloc&) {
+        return TG_ERR_NO_MEMORY;
+    } catch (...) {
+        return TG_ERR_LAUNCH;
+    }
+}
 
 constexpr int kOpMaxDevices = 64;
 constexpr int64_t kOpMaxDim = 2147483647LL;
@@ -138,6 +152,7 @@ class OpWorkspace {
                 cudaGetLastError();
                 return TG_ERR_NO_MEMORY;
             }
+            b.all.reserve(b.all.size() + 1);  // (what may throw, before there is memory to lose)
             size_t want = bytes > 2 * b.bytes ? bytes : 2 * b.bytes;
             void* p = nullptr;
             if (cudaMalloc(&p, want) != cudaSuccess) {

@@ -415,11 +415,10 @@ tg_status_t launch_rows(int32_t in_dtype, const W4Params& p, const tg_epilogue_e
 
 void tg::w4_clear_counters(int dev) { g_tc.clear(dev); }
 
-extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* Bq,
-                                  const void* Bscale, const void* Bzero, void* C, int64_t M,
-                                  int64_t N, int64_t K, int32_t group, int64_t lda, int64_t ldbq,
-                                  int64_t ldbs, int64_t ldbz, int64_t ldc,
-                                  const tg_epilogue_ex_t* epi, void* stream) {
+static tg_status_t gemm_w4(int32_t in_dtype, const void* A, const void* Bq, const void* Bscale,
+                           const void* Bzero, void* C, int64_t M, int64_t N, int64_t K,
+                           int32_t group, int64_t lda, int64_t ldbq, int64_t ldbs, int64_t ldbz,
+                           int64_t ldc, const tg_epilogue_ex_t* epi, void* stream) {
     tg_epilogue_ex_t x;
     if (epi != nullptr) {
         x = *epi;
@@ -478,4 +477,15 @@ extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* B
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return in_dtype == TG_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(in_dtype, p, x, dev, s)
                                      : launch_rows<__half>(in_dtype, p, x, dev, s);
+}
+
+extern "C" tg_status_t tg_gemm_w4(int32_t in_dtype, const void* A, const void* Bq,
+                                  const void* Bscale, const void* Bzero, void* C, int64_t M,
+                                  int64_t N, int64_t K, int32_t group, int64_t lda, int64_t ldbq,
+                                  int64_t ldbs, int64_t ldbz, int64_t ldc,
+                                  const tg_epilogue_ex_t* epi, void* stream) {
+    return tg::op_entry([&] {
+        return gemm_w4(in_dtype, A, Bq, Bscale, Bzero, C, M, N, K, group, lda, ldbq, ldbs, ldbz, ldc, epi,
+                       stream);
+    });
 }
