@@ -395,6 +395,150 @@ typedef struct {
  */
 tg_status_t tg_norm_residual_backward(const tg_norm_t* n, const tg_norm_grad_t* g, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Layer norm, rows as 8-bit codes, and products of 8-bit codes.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * What the calls of the layer norm share.  Per row (mean over the row's `cols`
+ * values, everything in fp32, each output rounded once):
+ *
+ *   v = x + residual  (residual NULL: v = x)                      y = v
+ *   h = (v - mean(v)) / sqrt(mean((v - mean(v))²) + eps) · weight + bias
+ *
+ * (weight NULL: 1, bias NULL: 0; h from v before it is rounded).  x and h are of
+ * type `dtype`; residual and y of `stream_dtype`, which is the same type or
+ * TG_DTYPE_F32.  weight and bias are fp32, `cols` values each.  Matrices are
+ * row-major with any stride of at least cols elements, aligned to their element.
+ */
+typedef struct {
+    int32_t dtype;        /* tg_dtype_t of x, h and their gradients                 */
+    int32_t stream_dtype; /* tg_dtype_t of residual, y and their gradients          */
+    int64_t rows, cols;   /* rows in [0, 2^31 - 1], cols in [0, 131071]             */
+    const void* x;        /* device                                                 */
+    int64_t ldx;
+    const void* residual; /* device, or NULL                                        */
+    int64_t ldr;
+    const float* weight;  /* device, or NULL                                        */
+    const float* bias;    /* device, or NULL                                        */
+    float eps;            /* ≥ 0                                                    */
+} tg_layer_norm_t;
+
+/*
+ * tg_layer_norm — y and h above, asynchronous on `stream`.
+ * y or h may be NULL (not written; not both).  y needs a residual, and may be the
+ * residual's own buffer (same pointer and stride); any other overlap is undefined.
+ * rows == 0 or cols == 0: nothing is done.
+ * Errors: TG_ERR_INVALID_VALUE for an unknown type, a size out of range, a stride
+ * below cols, a NULL x, no output, y without a residual, a negative or NaN eps;
+ * TG_ERR_MISALIGNED; all before anything is enqueued.  TG_ERR_LAUNCH if a launch
+ * fails.
+ */
+tg_status_t tg_layer_norm(const tg_layer_norm_t* n, void* y, int64_t ldy, void* h, int64_t ldh,
+                          void* stream);
+
+/*
+ * tg_layer_norm_i8 — the same y, and h as codes and scales, as tg_quantize_rows
+ * makes them of the unrounded h: what tg_gemm_i8 takes.
+ * codes: device, rows × cols, row stride ldc ≥ cols bytes, any alignment (rows 16
+ * bytes aligned are the faster ones, here and in tg_gemm_i8).  scale: device, `rows`
+ * values.  y may be NULL.  Everything else as tg_layer_norm.
+ */
+tg_status_t tg_layer_norm_i8(const tg_layer_norm_t* n, void* y, int64_t ldy, int8_t* codes,
+                             int64_t ldc, float* scale, void* stream);
+
+/*
+ * tg_quantize_rows — each row of x as 8-bit codes with a scale, asynchronous on
+ * `stream`:
+ *
+ *   scale[i] = fp32(max_j |x[i][j]| / 127),
+ *   codes[i][j] = x[i][j] / scale[i] to the nearest whole number, ties to even
+ *
+ * (the exact quotient's; ±127 at most).  A row of zeros has scale 0 and codes 0.  A
+ * row with a NaN or an infinity has scale NaN and codes 0, so that its products are
+ * NaN.  x: device, rows × cols of `dtype`, any stride ≥ cols; codes, scale and errors
+ * as tg_layer_norm_i8.
+ */
+tg_status_t tg_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc,
+                             float* scale, int64_t rows, int64_t cols, void* stream);
+
+/* The gradients that come in and go out; any of them may be NULL: no gradient
+ * (zero) for an input, not wanted for an output. */
+typedef struct {
+    const void* dy;  /* device, rows × cols of stream_dtype: of y (of x itself, where
+                      * there is no residual and x goes on beside its norm)          */
+    int64_t lddy;
+    const void* dh;  /* device, rows × cols of dtype                                 */
+    int64_t lddh;
+    void* dx;        /* device, rows × cols of dtype                                 */
+    int64_t lddx;
+    void* dresidual; /* device, rows × cols of stream_dtype; needs residual          */
+    int64_t lddr;
+    float* dweight;  /* device, cols values; needs weight                            */
+    float* dbias;    /* device, cols values (bias itself is not read)                */
+    void* workspace; /* device, 16-byte aligned, or NULL: a buffer that belongs to the
+                      * (device, stream), grown on demand and kept until process exit;
+                      * the first call of a size on a stream then has to come before any
+                      * capture (else TG_ERR_NO_MEMORY)                              */
+    int64_t workspace_bytes; /* of it: tg_layer_norm_backward_workspace(rows, cols)  */
+} tg_layer_norm_grad_t;
+
+/* Bytes that tg_layer_norm_backward needs for the blocks' shares of the column sums;
+ * -1 for sizes out of range.  Needs no device. */
+int64_t tg_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * tg_layer_norm_backward — the gradients of the call that tg_layer_norm makes with the
+ * same `n`, asynchronous on `stream`: dx and dresidual (the same values, each in its
+ * input's type), dweight and dbias.  The statistics are made again from x and residual
+ * (not y): nothing is kept by the forward call, whose inputs have to be unchanged (no
+ * y in the residual's place).
+ * Sums over rows are taken in fp32 in a fixed order: the same call gives the same bits.
+ * Outputs are written, not added to; they overlap no input and not one another.
+ * rows == 0: dweight and dbias are zero.  The workspace holds nothing from one call to
+ * the next; calls that may overlap on the GPU need one each.
+ * Errors: as tg_layer_norm; TG_ERR_INVALID_VALUE for a gradient without what it needs
+ * or a workspace that is too small.
+ */
+tg_status_t tg_layer_norm_backward(const tg_layer_norm_t* n, const tg_layer_norm_grad_t* g,
+                                   void* stream);
+
+/* Bytes of workspace that tg_gemm_i8 needs; -1 for sizes out of range.  Needs no device. */
+int64_t tg_gemm_i8_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * tg_gemm_i8 — the product of 8-bit integers with a scale per row of A (token) and per
+ * row of B (channel), asynchronous on `stream`:
+ *
+ *   C[m][n] = out( act( Ascale[m]·Bscale[n]·Σ_k A[m][k]·B[n][k] + bias[n] ) + R[m][n] )
+ *
+ * A        device, int8, M×K, any row stride lda ≥ K and any alignment.
+ * Ascale   device, M fp32 values.
+ * B        device, int8, N×K (the [out][in] orientation of a weight), row stride ldb ≥ K;
+ *          16-byte aligned, ldb a multiple of 16 (else TG_ERR_MISALIGNED).
+ * Bscale   device, N fp32 values.
+ * C        device, M×N of epi->out_dtype (any tg_dtype_t), row stride ldc ≥ N.
+ * M, N, K  M and N in [0, 2^31 - 1], K in [0, 131071].  M == 0 or N == 0: nothing is done.
+ * epi      as tg_gemm_ex, but the residual is of C's type (may be C itself); NULL: no
+ *          bias, activation or residual, C in fp16.
+ * Sums     of whole numbers, exact up to 2^24 in size (up to 8 rows: always).  Beyond
+ *          that, each of the K / 16 additions of the tensor cores may round the running
+ *          sum in its 24th bit.
+ * workspace  device, 256-byte aligned, tg_gemm_i8_workspace(M, N, K) bytes at least; it
+ *          holds nothing from one call to the next, and calls that may overlap on the GPU
+ *          need one each.  NULL: a buffer that belongs to the (device, stream), grown on
+ *          demand and kept until process exit; the first call of a size on a stream then
+ *          has to come before any capture (else TG_ERR_NO_MEMORY).
+ * Errors   TG_ERR_INVALID_VALUE for an unknown type or activation, a size out of range, a
+ *          stride below its row, a NULL pointer where one is needed, a workspace that is
+ *          too small; TG_ERR_MISALIGNED as above; all before anything is enqueued.
+ *          TG_ERR_LAUNCH if a launch fails.
+ */
+tg_status_t tg_gemm_i8(const int8_t* A, int64_t lda, const float* Ascale, const int8_t* B,
+                       int64_t ldb, const float* Bscale, void* C, int64_t ldc, int64_t M,
+                       int64_t N, int64_t K, const tg_epilogue_ex_t* epi, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
 /*
  * tg_sync_status — wait for `stream`, then report (and clear) a device-side
  * timeout recorded by any libtgemm kernel on the current device since the

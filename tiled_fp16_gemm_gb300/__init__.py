@@ -1,8 +1,8 @@
 """Python binding for libtgemm (dense FP16 GEMM on GB300, sm_103a).
 
 Argument marshalling only: every step of C = epi(A·B), of the products with
-4-bit weights and of the norms around a block runs in the CUDA kernels of
-``libtgemm.so``, called through its C ABI (``include/tgemm.h``).
+4-bit weights and 8-bit codes and of the norms around a block runs in the CUDA
+kernels of ``libtgemm.so``, called through its C ABI (``include/tgemm.h``).
 PyTorch is used for device memory and streams.  There is no fallback: if the
 shared library is missing, the first call raises ImportError.
 
@@ -45,6 +45,8 @@ EXPORTS = (
     "tg_gemm_f16_noalloc", "tg_gemm_bf16", "tg_gemm_ex", "tg_gemm_mxfp4", "tg_gemm_sp24",
     "tg_gemm_f16_host", "tg_plan_f16_limits", "tg_device_limits", "tg_debug_last_launch",
     "tg_debug_map_cache_stats", "tg_gemm_w4", "tg_norm_residual", "tg_norm_residual_backward",
+    "tg_layer_norm", "tg_layer_norm_i8", "tg_quantize_rows", "tg_layer_norm_backward_workspace",
+    "tg_layer_norm_backward", "tg_gemm_i8_workspace", "tg_gemm_i8",
 )
 
 #: bytes of the library's fixed scratch array used by tg_gemm_f16_noalloc
@@ -97,6 +99,27 @@ class tg_norm_grad_t(ctypes.Structure):
     ]
 
 
+class tg_layer_norm_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("stream_dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("eps", ctypes.c_float),
+    ]
+
+
+class tg_layer_norm_grad_t(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+        ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+        ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+        ("dresidual", ctypes.c_void_p), ("lddr", ctypes.c_int64),
+        ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
 _lib = None
@@ -138,6 +161,22 @@ def _L():
     lib.tg_norm_residual_backward.argtypes = [ctypes.POINTER(tg_norm_t),
                                               ctypes.POINTER(tg_norm_grad_t), _vp]
     lib.tg_norm_residual_backward.restype = ctypes.c_int
+    ln = ctypes.POINTER(tg_layer_norm_t)
+    lib.tg_layer_norm.argtypes = [ln, _vp, _i64, _vp, _i64, _vp]
+    lib.tg_layer_norm.restype = ctypes.c_int
+    lib.tg_layer_norm_i8.argtypes = [ln, _vp, _i64, _vp, _i64, _vp, _vp]
+    lib.tg_layer_norm_i8.restype = ctypes.c_int
+    lib.tg_quantize_rows.argtypes = [ctypes.c_int32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp]
+    lib.tg_quantize_rows.restype = ctypes.c_int
+    lib.tg_layer_norm_backward_workspace.argtypes = [_i64, _i64]
+    lib.tg_layer_norm_backward_workspace.restype = _i64
+    lib.tg_layer_norm_backward.argtypes = [ln, ctypes.POINTER(tg_layer_norm_grad_t), _vp]
+    lib.tg_layer_norm_backward.restype = ctypes.c_int
+    lib.tg_gemm_i8_workspace.argtypes = [_i64, _i64, _i64]
+    lib.tg_gemm_i8_workspace.restype = _i64
+    lib.tg_gemm_i8.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64,
+                               ctypes.POINTER(tg_epilogue_ex_t), _vp, _i64, _vp]
+    lib.tg_gemm_i8.restype = ctypes.c_int
     lib.tg_sync_status.argtypes = [_vp]
     lib.tg_sync_status.restype = ctypes.c_int
     lib.tg_status_string.argtypes = [ctypes.c_int]
@@ -242,6 +281,49 @@ def tg_norm_residual(n: tg_norm_t, y: int | None, ldy: int, h: int | None, ldh: 
 def tg_norm_residual_backward(n: tg_norm_t, g: tg_norm_grad_t, stream: int | None) -> int:
     """Their gradient with integer device pointers; returns the status code."""
     return _L().tg_norm_residual_backward(ctypes.byref(n), ctypes.byref(g), stream or None)
+
+
+def tg_layer_norm(n: tg_layer_norm_t, y: int | None, ldy: int, h: int | None, ldh: int,
+                  stream: int | None) -> int:
+    """The layer norm and its residual sum, integer device pointers; returns the status code."""
+    return _L().tg_layer_norm(ctypes.byref(n), y or None, ldy, h or None, ldh, stream or None)
+
+
+def tg_layer_norm_i8(n: tg_layer_norm_t, y: int | None, ldy: int, codes: int, ldc: int, scale: int,
+                     stream: int | None) -> int:
+    """The same with its result as 8-bit codes and scales; returns the status code."""
+    return _L().tg_layer_norm_i8(ctypes.byref(n), y or None, ldy, codes or None, ldc, scale or None,
+                                 stream or None)
+
+
+def tg_quantize_rows(dtype: int, x: int, ldx: int, codes: int, ldc: int, scale: int, rows: int,
+                     cols: int, stream: int | None) -> int:
+    """Rows as 8-bit codes with a scale each; returns the status code."""
+    return _L().tg_quantize_rows(dtype, x or None, ldx, codes or None, ldc, scale or None, rows, cols,
+                                 stream or None)
+
+
+def tg_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    return _L().tg_layer_norm_backward_workspace(rows, cols)
+
+
+def tg_layer_norm_backward(n: tg_layer_norm_t, g: tg_layer_norm_grad_t, stream: int | None) -> int:
+    """The layer norm's gradient with integer device pointers; returns the status code."""
+    return _L().tg_layer_norm_backward(ctypes.byref(n), ctypes.byref(g), stream or None)
+
+
+def tg_gemm_i8_workspace(M: int, N: int, K: int) -> int:
+    return _L().tg_gemm_i8_workspace(M, N, K)
+
+
+def tg_gemm_i8(A: int, lda: int, Ascale: int, B: int, ldb: int, Bscale: int, C: int, ldc: int,
+               M: int, N: int, K: int, epi: tg_epilogue_ex_t | None, workspace: int | None,
+               workspace_bytes: int, stream: int | None) -> int:
+    """C = out(act(scales · A·B^T + bias) + R) of 8-bit integers, integer device
+    pointers; returns the status code."""
+    return _L().tg_gemm_i8(A, lda, Ascale or None, B, ldb, Bscale or None, C, ldc, M, N, K,
+                           ctypes.byref(epi) if epi is not None else None, workspace or None,
+                           workspace_bytes, stream or None)
 
 
 def tg_sync_status(stream: int | None) -> int:
@@ -538,6 +620,10 @@ def _bind():
         from . import _calls as calls  # built with libtgemm.so; no fallback if it is missing
         calls.bind(*(ctypes.cast(f, _vp).value for f in
                      (lib.tg_gemm_w4, lib.tg_norm_residual, lib.tg_norm_residual_backward)), NormGrads)
+        calls.bind_i8(*(ctypes.cast(f, _vp).value for f in
+                        (lib.tg_layer_norm, lib.tg_layer_norm_i8, lib.tg_quantize_rows,
+                         lib.tg_layer_norm_backward, lib.tg_layer_norm_backward_workspace,
+                         lib.tg_gemm_i8, lib.tg_gemm_i8_workspace)), LayerNormGrads)
         _plain = calls
         _DTYPES = {torch.float16: TG_DTYPE_F16, torch.bfloat16: TG_DTYPE_BF16,
                    torch.float32: TG_DTYPE_F32}
@@ -849,6 +935,292 @@ def norm_residual_backward(dy, dh, x, residual=None, *, post_weight=None, gate=N
     if stream is None and index == _get_device():
         return body(_raw_stream(index))
     return _on_stream(index, stream, (dy, dh, x, residual, post_weight, gate, pre_weight), body)
+
+def _layer_norm_args(x, residual, weight, bias, eps):
+    """Checks and packs what the layer norm's calls share."""
+    if _torch is None:
+        _bind()
+    try:
+        dtype = x.dtype
+        rows, cols = x.shape
+        index = x.get_device()
+    except AttributeError:
+        raise TypeError("x must be a torch.Tensor") from None
+    except ValueError:
+        raise ValueError("x must be 2-D") from None
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
+    if index < 0:
+        raise ValueError("x must be a CUDA tensor")
+    if cols > 131071:
+        raise ValueError(f"x must have at most 131071 columns, got {cols}")
+    px, ldx = _matrix(x, "x", dtype, rows, cols, index)
+    kind, kind_code, pr, ldr = dtype, code, None, 0
+    if residual is not None:
+        kind = getattr(residual, "dtype", None)
+        if kind is not dtype:
+            if kind is not _torch.float32:
+                raise TypeError(f"residual must be a {dtype} or float32 tensor")
+            kind_code = TG_DTYPE_F32
+        pr, ldr = _matrix(residual, "residual", kind, rows, cols, index)
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
+    n = tg_layer_norm_t(
+        code, kind_code, rows, cols, px, ldx, pr, ldr,
+        _vector(weight, "weight", cols, index) if weight is not None else None,
+        _vector(bias, "bias", cols, index) if bias is not None else None, eps)
+    return n, rows, cols, dtype, kind, index
+
+
+def layer_norm(x, residual=None, *, weight=None, bias=None, eps: float = 1e-5, out=None, normed=None,
+               stream=None):
+    """Layer norm with the residual sum before it:
+
+        y = residual + x,   h = (y - mean(y)) / sqrt(var(y) + eps) · weight + bias
+
+    over each row (var: the mean of the squared differences).  Returns (y, h); without
+    residual h is the norm of x, and y is None.
+
+    x: CUDA float16, bfloat16 or float32 tensor of rows × cols.  residual: optional
+    tensor of x's dtype or float32; y has its dtype.  weight, bias: optional float32
+    vectors of cols.  h has x's dtype, and comes from y before it is rounded.  y is
+    written to ``out`` (which may be ``residual`` itself) and h to ``normed`` where given.
+    Runs on ``stream`` (default: torch's current stream of x's device).  Like every result
+    of this library y and h carry no autograd graph: their gradient is
+    ``layer_norm_backward``.
+    """
+    if _torch is None:
+        _bind()
+    if out is None and normed is None and stream is None:
+        made = _plain.layer_norm(x, residual, weight, bias, eps)
+        if made is not None:
+            return _made(made, "tg_layer_norm")
+    n, rows, cols, dtype, kind, index = _layer_norm_args(x, residual, weight, bias, eps)
+    torch = _torch
+    py = ph = None
+    if out is not None:
+        if residual is None:
+            raise ValueError("out needs residual")
+        py, ldy = _matrix(out, "out", kind, rows, cols, index)
+    if normed is not None:
+        ph, ldh = _matrix(normed, "normed", dtype, rows, cols, index)
+
+    def body(s):
+        y, h = out, normed
+        y_at, y_ld, h_at, h_ld = py, cols, ph, cols
+        if y is not None:
+            y_ld = ldy
+        elif residual is not None:
+            y = torch.empty((rows, cols), dtype=kind, device=x.device)
+            y_at = y.data_ptr()
+        if h is not None:
+            h_ld = ldh
+        else:
+            h = torch.empty((rows, cols), dtype=dtype, device=x.device)
+            h_at = h.data_ptr()
+        st = _lib.tg_layer_norm(ctypes.byref(n), y_at, y_ld, h_at, h_ld, s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_layer_norm")
+        return y, h
+
+    return _on_stream(index, stream, (x, residual, weight, bias, out, normed), body)
+
+
+def _codes(rows: int, cols: int, device):
+    """An int8 tensor whose rows begin on 16 bytes."""
+    return _torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=_torch.int8,
+                                device=device)
+
+
+def layer_norm_i8(x, residual=None, *, weight=None, bias=None, eps: float = 1e-5, out=None,
+                  stream=None):
+    """``layer_norm`` with its result in 8-bit codes, for ``gemm_i8``: (y, codes, scale).
+
+    codes and scale are those of ``quantize_rows`` for h before it is rounded.  All
+    arguments as for ``layer_norm``.
+    """
+    if _torch is None:
+        _bind()
+    if out is None and stream is None:
+        made = _plain.layer_norm_i8(x, residual, weight, bias, eps)
+        if made is not None:
+            return _made(made, "tg_layer_norm_i8")
+    n, rows, cols, dtype, kind, index = _layer_norm_args(x, residual, weight, bias, eps)
+    torch = _torch
+    py = None
+    if out is not None:
+        if residual is None:
+            raise ValueError("out needs residual")
+        py, ldy = _matrix(out, "out", kind, rows, cols, index)
+
+    def body(s):
+        y, y_at, y_ld = out, py, cols
+        if y is not None:
+            y_ld = ldy
+        elif residual is not None:
+            y = torch.empty((rows, cols), dtype=kind, device=x.device)
+            y_at = y.data_ptr()
+        codes = _codes(rows, cols, x.device)
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if cols == 0:
+            scale.zero_()
+        st = _lib.tg_layer_norm_i8(ctypes.byref(n), y_at, y_ld, codes.data_ptr(),
+                                   (cols + 15) // 16 * 16, scale.data_ptr(), s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_layer_norm_i8")
+        return y, codes, scale
+
+    return _on_stream(index, stream, (x, residual, weight, bias, out), body)
+
+
+def quantize_rows(x, *, stream=None):
+    """Each row of x as 8-bit codes with a scale, for ``gemm_i8``: (codes, scale) with
+    scale[i] = max|x[i]| / 127 and codes[i] = x[i] / scale[i] to the nearest whole number
+    (ties to even).
+
+    x: CUDA float16, bfloat16 or float32 tensor of rows × cols (at most 131071).  codes:
+    int8, rows × cols, whose rows begin on 16 bytes; scale: float32, rows values.  A row
+    of zeros has scale 0; a row with a NaN or an infinity has scale NaN and codes 0, so
+    that its products are NaN.  Runs on ``stream`` (default: torch's current stream of
+    x's device).
+    """
+    if _torch is None:
+        _bind()
+    if stream is None:
+        made = _plain.quantize_rows(x)
+        if made is not None:
+            return _made(made, "tg_quantize_rows")
+    n, rows, cols, _, _, index = _layer_norm_args(x, None, None, None, 0.0)
+    torch = _torch
+
+    def body(s):
+        codes = _codes(rows, cols, x.device)
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if cols == 0:
+            scale.zero_()
+        st = _lib.tg_quantize_rows(n.dtype, n.x, n.ldx, codes.data_ptr(), (cols + 15) // 16 * 16,
+                                   scale.data_ptr(), rows, cols, s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_quantize_rows")
+        return codes, scale
+
+    return _on_stream(index, stream, (x,), body)
+
+
+class LayerNormGrads(NamedTuple):
+    """Gradients of ``layer_norm``; None for an input that was not given."""
+    x: object
+    residual: object
+    weight: object
+    bias: object
+
+
+def layer_norm_backward(dy, dh, x, residual=None, *, weight=None, bias=None, eps: float = 1e-5,
+                        stream=None):
+    """The gradients of ``layer_norm`` called with the same arguments, given dy and dh, the
+    gradients of its two results (either may be None: zero).  Without residual dy is what
+    else x receives (where it goes on beside its norm).
+
+    dy has residual's dtype (x's without one), dh x's.  Returns LayerNormGrads, each gradient
+    with its input's dtype and shape.  x and residual are those of the forward call: no
+    ``out`` may have been written over them.
+    """
+    if _torch is None:
+        _bind()
+    if stream is None:
+        made = _plain.layer_norm_backward(dy, dh, x, residual, weight, bias, eps)
+        if made is not None:
+            return _made(made, "tg_layer_norm_backward")
+    n, rows, cols, dtype, kind, index = _layer_norm_args(x, residual, weight, bias, eps)
+    torch = _torch
+    pdy, lddy = _matrix(dy, "dy", kind, rows, cols, index) if dy is not None else (None, 0)
+    pdh, lddh = _matrix(dh, "dh", dtype, rows, cols, index) if dh is not None else (None, 0)
+
+    def body(s):
+        empty, shape, device = torch.empty, (rows, cols), x.device
+        dx = empty(shape, dtype=dtype, device=device)
+        dr = empty(shape, dtype=kind, device=device) if residual is not None else None
+        dw = empty(cols, dtype=torch.float32, device=device) if weight is not None else None
+        db = empty(cols, dtype=torch.float32, device=device) if bias is not None else None
+        size = _lib.tg_layer_norm_backward_workspace(rows, cols)
+        # (of this call's own: graphs captured on one stream share none)
+        work = empty(size, dtype=torch.uint8, device=device)
+        at = [t.data_ptr() if t is not None else None for t in (dx, dr, dw, db)]
+        g = tg_layer_norm_grad_t(pdy, lddy, pdh, lddh, at[0], cols, at[1], cols, at[2], at[3],
+                                 work.data_ptr() or None, size)
+        st = _lib.tg_layer_norm_backward(ctypes.byref(n), ctypes.byref(g), s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_layer_norm_backward")
+        return LayerNormGrads(dx, dr, dw, db)
+
+    return _on_stream(index, stream, (dy, dh, x, residual, weight), body)
+
+
+def gemm_i8(a, b, ascale, bscale, relu: bool = False, out=None, stream=None, *, bias=None,
+            residual=None, out_dtype=None):
+    """C = out(act(ascale[m] · bscale[n] · (a @ b.T) + bias) + residual) of 8-bit integers
+    with a scale per row of a (token) and per row of b (channel).
+
+    a: CUDA int8 tensor M×K (unit column stride), for instance the codes of ``quantize_rows``
+    or ``layer_norm_i8``.  b: CUDA int8 tensor N×K, the [out][in] orientation of a weight,
+    each row on 16 bytes (row stride a multiple of 16).  K is 131071 at most.  ascale, bscale:
+    float32 vectors of M and N.  out_dtype: float16, bfloat16 or float32 (default: that of
+    ``out``, else of residual, else float16).  bias: optional float32 tensor of N elements.
+    residual: optional M×N tensor of C's dtype, added after the activation (may be ``out``
+    itself).  ``out`` (M×N) is written in place when given.  Runs on ``stream`` (default:
+    torch's current stream of a's device).
+    """
+    if _torch is None:
+        _bind()
+    if out is None and stream is None:
+        made = _plain.gemm_i8(a, b, ascale, bscale, relu, bias, residual, out_dtype)
+        if made is not None:
+            return _made(made, "tg_gemm_i8")
+    torch = _torch
+    try:
+        M, K = a.shape
+        index = a.get_device()
+    except AttributeError:
+        raise TypeError("a must be a torch.Tensor") from None
+    except ValueError:
+        raise ValueError("a must be 2-D") from None
+    if index < 0:
+        raise ValueError("a must be a CUDA tensor")
+    pa, lda = _matrix(a, "a", torch.int8, M, K, index)
+    if K > 131071:
+        raise ValueError(f"a must have at most 131071 columns, got {K}")
+    try:
+        N = b.shape[0]
+    except (AttributeError, IndexError):
+        raise TypeError("b must be a 2-D torch.int8 tensor") from None
+    pb, ldb = _matrix(b, "b", torch.int8, N, K, index)
+    psa, psb = _vector(ascale, "ascale", M, index), _vector(bscale, "bscale", N, index)
+    if out_dtype is None:
+        given = out if out is not None else residual
+        out_dtype = given.dtype if given is not None else torch.float16
+    code = _DTYPES.get(out_dtype)
+    if code is None:
+        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
+    if out is not None:
+        pc, ldc = _matrix(out, "out", out_dtype, M, N, index)
+    pbias = _vector(bias, "bias", N, index) if bias is not None else None
+    pr, ldr = _matrix(residual, "residual", out_dtype, M, N, index) if residual is not None else (None, 0)
+    epi = tg_epilogue_ex_t(1 if relu else 0, code, pbias, pr, ldr)
+
+    def body(s):
+        c = torch.empty((M, N), dtype=out_dtype, device=a.device) if out is None else out
+        size = _lib.tg_gemm_i8_workspace(M, N, K)
+        # (of this call's own: graphs captured on one stream share none)
+        work = torch.empty(size, dtype=torch.uint8, device=a.device) if size > 0 else None
+        st = _lib.tg_gemm_i8(pa, lda, psa, pb, ldb, psb, c.data_ptr(), N if out is None else ldc, M, N,
+                             K, ctypes.byref(epi), work.data_ptr() if work is not None else None, size, s)
+        if st != TG_OK:
+            raise TgemmError(st, "tg_gemm_i8")
+        return c
+
+    return _on_stream(index, stream, (a, b, ascale, bscale, bias, residual, out), body)
+
 
 
 def gemm_host(a, b, relu: bool = False, stream=None, device=None):

@@ -73,7 +73,7 @@ def nvcc_command(out: str = LIB, extra: list[str] | None = None) -> list[str]:
         _nvcc(), "-gencode", ARCH, "-O3", "-std=c++17", "-lineinfo",
         "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
         "-t", "0", "-I", INCLUDE, "-I", CSRC,
-        *(os.path.join(CSRC, f) for f in ("tgemm.cu", "w4.cu", "norm.cu")), "-o", out,
+        *(os.path.join(CSRC, f) for f in ("tgemm.cu", "w4.cu", "norm.cu", "layer_norm.cu", "i8.cu")), "-o", out,
     ] + (extra or [])
 
 

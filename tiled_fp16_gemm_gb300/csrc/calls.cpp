@@ -1,4 +1,4 @@
-// The plain calls of gemm_w4, norm_residual and norm_residual_backward from torch tensors:
+// The plain calls of gemm_w4, gemm_i8, the norms and their gradients from torch tensors:
 // checks, allocation of the results and the C entry point in one native call.  On single
 // tokens the host's work is the time of a call: read attribute by attribute from Python,
 // norm_residual on one row took 18 us, of which the kernel runs 2.6; from here it takes 4.6.
@@ -23,6 +23,14 @@ decltype(&tg_gemm_w4) g_w4 = nullptr;
 decltype(&tg_norm_residual) g_norm = nullptr;
 decltype(&tg_norm_residual_backward) g_norm_backward = nullptr;
 PyTypeObject* g_grads = nullptr;  // a named tuple of five
+decltype(&tg_layer_norm) g_layer_norm = nullptr;
+decltype(&tg_layer_norm_i8) g_layer_norm_i8 = nullptr;
+decltype(&tg_quantize_rows) g_quantize = nullptr;
+decltype(&tg_layer_norm_backward) g_layer_norm_backward = nullptr;
+decltype(&tg_layer_norm_backward_workspace) g_layer_norm_workspace = nullptr;
+decltype(&tg_gemm_i8) g_i8 = nullptr;
+decltype(&tg_gemm_i8_workspace) g_i8_workspace = nullptr;
+PyTypeObject* g_layer_norm_grads = nullptr;  // a named tuple of four
 
 // A CUDA tensor with storage of its own, or nullptr.
 const at::Tensor* plain(PyObject* o) {
@@ -82,6 +90,11 @@ bool number(PyObject* o, float* v) {
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, int index) {
     return at::Tensor(at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)),
                                              std::nullopt));
+}
+// Codes: rows that begin on 16 bytes.
+at::Tensor empty_codes(int64_t rows, int64_t cols, int index) {
+    return at::Tensor(at::detail::empty_strided_cuda({rows, cols}, {(cols + 15) / 16 * 16, 1}, at::kChar,
+                                                     c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index))));
 }
 bool here(int index) { return c10::cuda::current_device() == index; }
 void* stream_of(int index) {
@@ -286,6 +299,203 @@ PyObject* norm_residual_backward(PyObject*, PyObject* const* a, Py_ssize_t count
     });
 }
 
+// The addresses in the order of g_layer_norm to g_i8_workspace; LayerNormGrads
+PyObject* bind_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (n != 8 || !PyType_Check(a[7]) || !PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[7]), &PyTuple_Type)) {
+        PyErr_SetString(PyExc_TypeError, "bind_i8 needs seven addresses and a named tuple");
+        return nullptr;
+    }
+    g_layer_norm = reinterpret_cast<decltype(g_layer_norm)>(PyLong_AsVoidPtr(a[0]));
+    g_layer_norm_i8 = reinterpret_cast<decltype(g_layer_norm_i8)>(PyLong_AsVoidPtr(a[1]));
+    g_quantize = reinterpret_cast<decltype(g_quantize)>(PyLong_AsVoidPtr(a[2]));
+    g_layer_norm_backward = reinterpret_cast<decltype(g_layer_norm_backward)>(PyLong_AsVoidPtr(a[3]));
+    g_layer_norm_workspace = reinterpret_cast<decltype(g_layer_norm_workspace)>(PyLong_AsVoidPtr(a[4]));
+    g_i8 = reinterpret_cast<decltype(g_i8)>(PyLong_AsVoidPtr(a[5]));
+    g_i8_workspace = reinterpret_cast<decltype(g_i8_workspace)>(PyLong_AsVoidPtr(a[6]));
+    if (PyErr_Occurred()) return nullptr;
+    Py_INCREF(a[7]);
+    g_layer_norm_grads = reinterpret_cast<PyTypeObject*>(a[7]);
+    Py_RETURN_NONE;
+}
+
+// (x, residual, weight, bias, eps) to the C structure.
+bool layer_norm_args(PyObject* const* a, tg_layer_norm_t* n, at::ScalarType* type, at::ScalarType* kind, int* index) {
+    const at::Tensor* x = plain(a[0]);
+    if (x == nullptr) return false;
+    *type = *kind = x->scalar_type();
+    *index = x->get_device();
+    std::memset(n, 0, sizeof(*n));
+    Matrix m, r;
+    if (!code_of(*type, &n->dtype) || !here(*index) || !matrix(a[0], *type, -1, -1, *index, &m) ||
+        m.cols > 131071 || !number(a[4], &n->eps) || !(n->eps >= 0.0f))
+        return false;
+    n->stream_dtype = n->dtype;
+    if (a[1] != Py_None) {
+        const at::Tensor* t = plain(a[1]);
+        if (t == nullptr) return false;
+        *kind = t->scalar_type();
+        if (*kind != *type && *kind != at::kFloat) return false;
+        if (!code_of(*kind, &n->stream_dtype) || !matrix(a[1], *kind, m.rows, m.cols, *index, &r)) return false;
+    }
+    n->rows = m.rows;
+    n->cols = m.cols;
+    n->x = m.p;
+    n->ldx = m.ld;
+    n->residual = r.p;
+    n->ldr = r.ld;
+    return vector(a[2], m.cols, *index, &n->weight) && vector(a[3], m.cols, *index, &n->bias);
+}
+
+// (x, residual, weight, bias, eps)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        tg_layer_norm_t n;
+        at::ScalarType type, kind;
+        int index;
+        if (count != 5 || g_layer_norm == nullptr || !layer_norm_args(a, &n, &type, &kind, &index)) Py_RETURN_NONE;
+        at::Tensor made[2];
+        if (a[1] != Py_None) made[0] = empty({n.rows, n.cols}, kind, index);
+        made[1] = empty({n.rows, n.cols}, type, index);
+        const tg_status_t st = g_layer_norm(&n, made[0].defined() ? made[0].data_ptr() : nullptr, n.cols,
+                                            made[1].data_ptr(), n.cols, stream_of(index));
+        return st == TG_OK ? tuple_of(made, 2) : PyLong_FromLong(st);
+    });
+}
+
+// (x, residual, weight, bias, eps)
+PyObject* layer_norm_i8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        tg_layer_norm_t n;
+        at::ScalarType type, kind;
+        int index;
+        if (count != 5 || g_layer_norm_i8 == nullptr || !layer_norm_args(a, &n, &type, &kind, &index) || n.cols == 0)
+            Py_RETURN_NONE;
+        at::Tensor made[3];
+        if (a[1] != Py_None) made[0] = empty({n.rows, n.cols}, kind, index);
+        made[1] = empty_codes(n.rows, n.cols, index);
+        made[2] = empty({n.rows}, at::kFloat, index);
+        const tg_status_t st = g_layer_norm_i8(&n, made[0].defined() ? made[0].data_ptr() : nullptr, n.cols,
+                                               static_cast<int8_t*>(made[1].data_ptr()), (n.cols + 15) / 16 * 16,
+                                               static_cast<float*>(made[2].data_ptr()), stream_of(index));
+        return st == TG_OK ? tuple_of(made, 3) : PyLong_FromLong(st);
+    });
+}
+
+// (x)
+PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        const at::Tensor* x = count == 1 && g_quantize != nullptr ? plain(a[0]) : nullptr;
+        if (x == nullptr) Py_RETURN_NONE;
+        const at::ScalarType type = x->scalar_type();
+        const int index = x->get_device();
+        int32_t code;
+        Matrix m;
+        if (!code_of(type, &code) || !here(index) || !matrix(a[0], type, -1, -1, index, &m) || m.cols > 131071 ||
+            m.cols == 0)
+            Py_RETURN_NONE;
+        at::Tensor made[2];
+        made[0] = empty_codes(m.rows, m.cols, index);
+        made[1] = empty({m.rows}, at::kFloat, index);
+        const tg_status_t st = g_quantize(code, m.p, m.ld, static_cast<int8_t*>(made[0].data_ptr()),
+                                          (m.cols + 15) / 16 * 16, static_cast<float*>(made[1].data_ptr()), m.rows,
+                                          m.cols, stream_of(index));
+        return st == TG_OK ? tuple_of(made, 2) : PyLong_FromLong(st);
+    });
+}
+
+// (dy, dh, x, residual, weight, bias, eps)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        tg_layer_norm_t n;
+        tg_layer_norm_grad_t g;
+        at::ScalarType type, kind;
+        int index;
+        if (count != 7 || g_layer_norm_backward == nullptr || !layer_norm_args(a + 2, &n, &type, &kind, &index))
+            Py_RETURN_NONE;
+        std::memset(&g, 0, sizeof(g));
+        Matrix dy, dh;
+        if ((a[0] != Py_None && !matrix(a[0], kind, n.rows, n.cols, index, &dy)) ||
+            (a[1] != Py_None && !matrix(a[1], type, n.rows, n.cols, index, &dh)))
+            Py_RETURN_NONE;
+        g.dy = dy.p;
+        g.lddy = dy.ld;
+        g.dh = dh.p;
+        g.lddh = dh.ld;
+        at::Tensor made[4];
+        made[0] = empty({n.rows, n.cols}, type, index);
+        g.dx = made[0].data_ptr();
+        if (a[3] != Py_None) {
+            made[1] = empty({n.rows, n.cols}, kind, index);
+            g.dresidual = made[1].data_ptr();
+        }
+        if (a[4] != Py_None) {
+            made[2] = empty({n.cols}, at::kFloat, index);
+            g.dweight = static_cast<float*>(made[2].data_ptr());
+        }
+        if (a[5] != Py_None) {
+            made[3] = empty({n.cols}, at::kFloat, index);
+            g.dbias = static_cast<float*>(made[3].data_ptr());
+        }
+        g.lddx = g.lddr = n.cols;
+        // (of this call's own: graphs captured on one stream share none)
+        g.workspace_bytes = g_layer_norm_workspace(n.rows, n.cols);
+        const at::Tensor work = empty({g.workspace_bytes}, at::kByte, index);
+        g.workspace = work.data_ptr();
+        const tg_status_t st = g_layer_norm_backward(&n, &g, stream_of(index));
+        if (st != TG_OK) return PyLong_FromLong(st);
+        PyObject* four = tuple_of(made, 4);
+        if (four == nullptr) return nullptr;
+        PyObject* args = PyTuple_Pack(1, four);
+        Py_DECREF(four);
+        if (args == nullptr) return nullptr;
+        PyObject* grads = PyTuple_Type.tp_new(g_layer_norm_grads, args, nullptr);
+        Py_DECREF(args);
+        return grads;
+    });
+}
+
+// (a, b, ascale, bscale, relu, bias, residual, out_dtype)
+PyObject* gemm_i8(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        const at::Tensor* x = count == 8 && g_i8 != nullptr ? plain(a[0]) : nullptr;
+        const at::Tensor* w = x != nullptr ? plain(a[1]) : nullptr;
+        if (w == nullptr || w->dim() != 2 || !PyBool_Check(a[4])) Py_RETURN_NONE;
+        const int index = x->get_device();
+        const int64_t N = w->size(0);
+        at::ScalarType out_type = at::kHalf;
+        if (a[7] != Py_None) {
+            if (!THPDtype_Check(a[7])) Py_RETURN_NONE;
+            out_type = reinterpret_cast<THPDtype*>(a[7])->scalar_type;
+        } else if (a[6] != Py_None) {
+            const at::Tensor* r = plain(a[6]);
+            if (r == nullptr) Py_RETURN_NONE;
+            out_type = r->scalar_type();
+        }
+        Matrix A, B, residual;
+        const float *sa = nullptr, *sb = nullptr;
+        tg_epilogue_ex_t epi;
+        std::memset(&epi, 0, sizeof(epi));
+        if (!code_of(out_type, &epi.out_dtype) || !here(index) || !matrix(a[0], at::kChar, -1, -1, index, &A) ||
+            A.cols > 131071 || !matrix(a[1], at::kChar, N, A.cols, index, &B) || a[2] == Py_None ||
+            a[3] == Py_None || !vector(a[2], A.rows, index, &sa) || !vector(a[3], N, index, &sb) ||
+            !vector(a[5], N, index, &epi.bias) ||
+            (a[6] != Py_None && !matrix(a[6], out_type, A.rows, N, index, &residual)))
+            Py_RETURN_NONE;
+        epi.activation = a[4] == Py_True ? TG_EPI_RELU : TG_EPI_NONE;
+        epi.residual = residual.p;
+        epi.ldr = residual.ld;
+        const at::Tensor c = empty({A.rows, N}, out_type, index);
+        // (of this call's own: graphs captured on one stream share none)
+        const int64_t bytes = g_i8_workspace(A.rows, N, A.cols);
+        at::Tensor work;
+        if (bytes > 0) work = empty({bytes}, at::kByte, index);
+        const tg_status_t st =
+            g_i8(static_cast<const int8_t*>(A.p), A.ld, sa, static_cast<const int8_t*>(B.p), B.ld, sb, c.data_ptr(), N,
+                 A.rows, N, A.cols, &epi, bytes > 0 ? work.data_ptr() : nullptr, bytes, stream_of(index));
+        return st == TG_OK ? wrap(c) : PyLong_FromLong(st);
+    });
+}
+
 template <typename F>
 PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -296,6 +506,12 @@ PyMethodDef g_methods[] = {
     {"gemm_w4", fast(gemm_w4), METH_FASTCALL, nullptr},
     {"norm_residual", fast(norm_residual), METH_FASTCALL, nullptr},
     {"norm_residual_backward", fast(norm_residual_backward), METH_FASTCALL, nullptr},
+    {"bind_i8", fast(bind_i8), METH_FASTCALL, nullptr},
+    {"layer_norm", fast(layer_norm), METH_FASTCALL, nullptr},
+    {"layer_norm_i8", fast(layer_norm_i8), METH_FASTCALL, nullptr},
+    {"quantize_rows", fast(quantize_rows), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", fast(layer_norm_backward), METH_FASTCALL, nullptr},
+    {"gemm_i8", fast(gemm_i8), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,248 @@
+// tg_layer_norm, tg_layer_norm_i8, tg_quantize_rows and tg_layer_norm_backward
+// (include/tgemm.h): argument checks, workspace and launches.  The kernels and the formulas:
+// layer_norm.cuh.
+#include <cstring>
+#include <set>
+#include <type_traits>
+
+#include "layer_norm.cuh"
+#include "op_host.h"
+
+namespace {
+
+using tg::LayerNormGradParams;
+using tg::LayerNormParams;
+
+constexpr int64_t kMaxCols = 131071;   // codes of a row: whole sums of gemm_i8 fit 32 bits
+constexpr int64_t kGradBlocks = 320;   // that share the column sums, at most
+
+tg::OpWorkspace g_workspace;  // column sums of the gradient, where the caller has none
+
+int elem_bytes(int32_t dtype) { return dtype == TG_DTYPE_F32 ? 4 : 2; }
+
+bool misaligned(const void* p, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) != 0;
+}
+
+// One matrix argument: present or not, its stride, its alignment.
+tg_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int bytes) {
+    if (p == nullptr) return TG_OK;
+    if (ld < cols) return TG_ERR_INVALID_VALUE;
+    return misaligned(p, bytes) ? TG_ERR_MISALIGNED : TG_OK;
+}
+
+// The arguments that all calls share.
+tg_status_t check_norm(const tg_layer_norm_t* a, LayerNormParams* p) {
+    if (a == nullptr) return TG_ERR_INVALID_VALUE;
+    if (a->dtype != TG_DTYPE_F16 && a->dtype != TG_DTYPE_BF16 && a->dtype != TG_DTYPE_F32)
+        return TG_ERR_INVALID_VALUE;
+    if (a->stream_dtype != a->dtype && a->stream_dtype != TG_DTYPE_F32) return TG_ERR_INVALID_VALUE;
+    if (a->rows < 0 || a->rows > tg::kOpMaxDim || a->cols < 0 || a->cols > kMaxCols)
+        return TG_ERR_INVALID_VALUE;
+    if (!(a->eps >= 0.0f)) return TG_ERR_INVALID_VALUE;
+    if (a->rows > 0 && a->cols > 0 && a->x == nullptr) return TG_ERR_INVALID_VALUE;
+    tg_status_t st;
+    if ((st = check_matrix(a->x, a->ldx, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
+    if ((st = check_matrix(a->residual, a->ldr, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if (misaligned(a->weight, 4) || misaligned(a->bias, 4)) return TG_ERR_MISALIGNED;
+    std::memset(p, 0, sizeof(*p));
+    p->rows = a->rows;
+    p->cols = a->cols;
+    p->x = a->x;
+    p->ldx = a->ldx;
+    p->r = a->residual;
+    p->ldr = a->ldr;
+    p->w = a->weight;
+    p->b = a->bias;
+    p->eps = a->eps;
+    return TG_OK;
+}
+
+// f<TX, TR>() for the call's types.
+template <typename F>
+tg_status_t with_types(int32_t dtype, int32_t stream_dtype, F f) {
+    const bool wide = stream_dtype == TG_DTYPE_F32;
+    if (dtype == TG_DTYPE_F32) return f(float{}, float{});
+    if (dtype == TG_DTYPE_F16) return wide ? f(__half{}, float{}) : f(__half{}, __half{});
+    return wide ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
+}
+
+// One launch with dependent launch allowed.
+template <typename... Args, typename... Given>
+tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   Given... given) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
+        cudaGetLastError();
+        return TG_ERR_LAUNCH;
+    }
+    return TG_OK;
+}
+
+template <typename TX, typename TR, int MODE>
+tg_status_t launch_rows(const LayerNormParams& p, const tg::OpDevice& dev, cudaStream_t s) {
+    const int64_t most = 8 * int64_t{dev.num_sms};
+    return launch(tg::tg_layer_norm_simple<TX, TR, MODE>,
+                  dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)), 256, 0, s, p);
+}
+
+// y, and h or the codes of a norm.
+tg_status_t forward(const tg_layer_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh, float* scale,
+                    bool codes, void* stream) {
+    LayerNormParams p;
+    tg_status_t st = check_norm(a, &p);
+    if (st != TG_OK) return st;
+    if (y != nullptr && a->residual == nullptr) return TG_ERR_INVALID_VALUE;
+    if ((st = check_matrix(y, ldy, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if ((st = check_matrix(h, ldh, a->cols, codes ? 1 : elem_bytes(a->dtype))) != TG_OK) return st;
+    if (codes && misaligned(scale, 4)) return TG_ERR_MISALIGNED;
+    if (a->rows == 0 || a->cols == 0) return TG_OK;
+    if (codes ? h == nullptr || scale == nullptr : h == nullptr && y == nullptr) return TG_ERR_INVALID_VALUE;
+    p.y = y;
+    p.ldy = ldy;
+    p.h = h;
+    p.ldh = ldh;
+    p.scale = scale;
+    tg::OpDevice dev;
+    if ((st = tg::op_device(&dev)) != TG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_types(a->dtype, a->stream_dtype, [&](auto tx, auto tr) {
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        return codes ? launch_rows<TX, TR, tg::kLnCodes>(p, dev, s) : launch_rows<TX, TR, tg::kLnH>(p, dev, s);
+    });
+}
+
+tg_status_t quantize(int32_t dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc, float* scale,
+                     int64_t rows, int64_t cols, void* stream) {
+    tg_layer_norm_t a;
+    std::memset(&a, 0, sizeof(a));
+    a.dtype = a.stream_dtype = dtype;
+    a.rows = rows;
+    a.cols = cols;
+    a.x = x;
+    a.ldx = ldx;
+    LayerNormParams p;
+    tg_status_t st = check_norm(&a, &p);
+    if (st != TG_OK) return st;
+    if ((st = check_matrix(codes, ldc, cols, 1)) != TG_OK) return st;
+    if (misaligned(scale, 4)) return TG_ERR_MISALIGNED;
+    if (rows == 0 || cols == 0) return TG_OK;
+    if (codes == nullptr || scale == nullptr) return TG_ERR_INVALID_VALUE;
+    p.h = codes;
+    p.ldh = ldc;
+    p.scale = scale;
+    tg::OpDevice dev;
+    if ((st = tg::op_device(&dev)) != TG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return with_types(dtype, dtype, [&](auto tx, auto) {
+        using TX = decltype(tx);
+        return launch_rows<TX, TX, tg::kLnRaw>(p, dev, s);
+    });
+}
+
+int64_t grad_workspace(int64_t rows, int64_t cols) {
+    return (rows < kGradBlocks ? rows : kGradBlocks) * cols * 8;
+}
+
+tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, void* stream) {
+    LayerNormGradParams q;
+    std::memset(&q, 0, sizeof(q));
+    if (b == nullptr) return TG_ERR_INVALID_VALUE;
+    tg_status_t st = check_norm(a, &q.n);
+    if (st != TG_OK) return st;
+    const int bx = elem_bytes(a->dtype), br = elem_bytes(a->stream_dtype);
+    if (b->dresidual != nullptr && a->residual == nullptr) return TG_ERR_INVALID_VALUE;
+    if (b->dweight != nullptr && a->weight == nullptr) return TG_ERR_INVALID_VALUE;
+    if ((st = check_matrix(b->dy, b->lddy, a->cols, br)) != TG_OK) return st;
+    if ((st = check_matrix(b->dh, b->lddh, a->cols, bx)) != TG_OK) return st;
+    if ((st = check_matrix(b->dx, b->lddx, a->cols, bx)) != TG_OK) return st;
+    if ((st = check_matrix(b->dresidual, b->lddr, a->cols, br)) != TG_OK) return st;
+    if (misaligned(b->dweight, 4) || misaligned(b->dbias, 4) || misaligned(b->workspace, 16))
+        return TG_ERR_MISALIGNED;
+    if (b->workspace != nullptr && b->workspace_bytes < grad_workspace(a->rows, a->cols))
+        return TG_ERR_INVALID_VALUE;
+    if (a->cols == 0) return TG_OK;
+    tg::OpDevice dev;
+    if ((st = tg::op_device(&dev)) != TG_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    q.dy = b->dy;
+    q.lddy = b->lddy;
+    q.dh = b->dh;
+    q.lddh = b->lddh;
+    q.dx = b->dx;
+    q.lddx = b->lddx;
+    q.dr = b->dresidual;
+    q.lddr = b->lddr;
+    q.dw = b->dweight;
+    q.db = b->dbias;
+    const int64_t cols = a->cols;
+    if (a->rows == 0 || q.dh == nullptr) {  // sums of nothing
+        for (float* sum : {q.dw, q.db})
+            if (sum != nullptr && cudaMemsetAsync(sum, 0, static_cast<size_t>(cols) * 4, s) != cudaSuccess) {
+                cudaGetLastError();
+                return TG_ERR_LAUNCH;
+            }
+        q.dw = q.db = nullptr;
+    }
+    if (a->rows == 0 || (q.dx == nullptr && q.dr == nullptr && q.dw == nullptr && q.db == nullptr)) return TG_OK;
+    return with_types(a->dtype, a->stream_dtype, [&](auto tx, auto tr) {
+        using TX = decltype(tx);
+        using TR = decltype(tr);
+        const int64_t most = 2 * int64_t{dev.num_sms} < kGradBlocks ? 2 * dev.num_sms : kGradBlocks;
+        const int64_t blocks = a->rows < most ? a->rows : most;
+        tg::OpWorkspace::Hold hold;  // until the shares' sums are launched
+        if (q.dw != nullptr || q.db != nullptr) {
+            void* ws = b->workspace;
+            if (ws == nullptr) {
+                st = g_workspace.get(dev.dev, s, static_cast<size_t>(grad_workspace(a->rows, cols)), &ws, &hold);
+                if (st != TG_OK) return st;
+            }
+            float* next = static_cast<float*>(ws);
+            if (q.dw != nullptr) q.ws_w = next, next += blocks * cols;
+            if (q.db != nullptr) q.ws_b = next;
+        }
+        st = launch(tg::tg_layer_norm_grad_simple<TX, TR>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, q);
+        if (st != TG_OK || (q.dw == nullptr && q.db == nullptr)) return st;
+        return launch(tg::tg_layer_norm_grad_sum, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, s, q,
+                      blocks);
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+tg_status_t tg_layer_norm(const tg_layer_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh, void* stream) {
+    return tg::op_entry([&] { return forward(a, y, ldy, h, ldh, nullptr, false, stream); });
+}
+
+tg_status_t tg_layer_norm_i8(const tg_layer_norm_t* a, void* y, int64_t ldy, int8_t* codes, int64_t ldc,
+                             float* scale, void* stream) {
+    return tg::op_entry([&] { return forward(a, y, ldy, codes, ldc, scale, true, stream); });
+}
+
+tg_status_t tg_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc, float* scale,
+                             int64_t rows, int64_t cols, void* stream) {
+    return tg::op_entry([&] { return quantize(dtype, x, ldx, codes, ldc, scale, rows, cols, stream); });
+}
+
+int64_t tg_layer_norm_backward_workspace(int64_t rows, int64_t cols) {
+    return rows < 0 || cols < 0 || rows > tg::kOpMaxDim || cols > kMaxCols ? -1 : grad_workspace(rows, cols);
+}
+
+tg_status_t tg_layer_norm_backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, void* stream) {
+    return tg::op_entry([&] { return backward(a, b, stream); });
+}
+
+}  // extern "C"
