@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "op_device.cuh"
+#include "tc_device.cuh"
 
 namespace tg {
 
@@ -92,8 +93,6 @@ struct W4Step {
     static_assert(kScaleBytes <= 256 && kZeroAt + kZeroBytes <= kBytes, "a step's place");
 };
 
-// What copies under way get to land before a block that gave up on them ends.
-constexpr uint64_t kW4LandNs = 1000000000ull;
 
 struct W4Launch {
     W4Params p;
@@ -115,13 +114,6 @@ struct W4Launch {
 __device__ __forceinline__ uint32_t w4_lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 w4_lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(a));
     return v;
 }
 
@@ -199,9 +191,6 @@ __device__ __forceinline__ float w4_cluster_load(uint32_t a, int rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(m) : "memory");
     return v;
-}
-__device__ __forceinline__ void w4_cluster_sync() {
-    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // grid: x = clusters × cluster (the blocks of a cluster side by side), y = blocks of
@@ -324,7 +313,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
                 if (!lost && !op_bar_wait(bars + 8 * slot, parity, q.limit_ns)) {
                     // reported; nothing more is fetched once copies do not come at all
                     given_up = true;
-                    lost = !op_bar_wait(bars + 8 * slot, parity, kW4LandNs);
+                    lost = !op_bar_wait(bars + 8 * slot, parity, kTcLandNs);
                 }
                 lost = __any_sync(0xffffffffu, lost);
                 __syncwarp();  // all lanes have read the slot before, which is filled again
@@ -355,7 +344,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
                             }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 x = w4_lds128(x_lane[nt] + x_at + j * x_pitch);
+                            const uint4 x = tc_lds128(x_lane[nt] + x_at + j * x_pitch);
 #pragma unroll
                             for (int mt = 0; mt < 2; ++mt) {
                                 float(&a)[4] = acc[mt][nt];
@@ -440,7 +429,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
     }
     if (given_up && lane == 0) atomicOr(q.timeouts, kOpTimeoutW4);
     if (q.cluster > 1) {
-        w4_cluster_sync();
+        tc_cluster_sync();
         const uint32_t from = op_smem(results);
         const int outs = q.rounds * q.wn * q.tokens * kW4Rows;
         for (int i = rank * kW4Threads + threadIdx.x; i < outs; i += q.cluster * kW4Threads) {
@@ -453,7 +442,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) tg_gemm_w4(const __grid_constan
             for (int k = 0; k < q.cluster; ++k) a += w4_cluster_load(from + i * 4, k);
             w4_store<T>(p, m0 + m, n, a);
         }
-        w4_cluster_sync();  // no block leaves while another reads its shared memory
+        tc_cluster_sync();  // no block leaves while another reads its shared memory
     }
 }
 

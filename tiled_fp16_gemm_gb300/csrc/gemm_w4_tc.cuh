@@ -35,9 +35,6 @@
 
 namespace tg {
 
-constexpr int kTcRows = 128;
-constexpr int kTcK = 128;
-constexpr int kTcGroups = 3;       // of decoding warps
 // Depths of the rings, all divisors of kTcTurn: the MMA warp's loop is unrolled that far,
 // and its addresses and parities are constants.
 constexpr int kTcTurn = 8;
@@ -47,7 +44,6 @@ constexpr int kTcScaleAt = 8192;
 constexpr int kTcZeroAt = 9216;
 constexpr int kTcXStages = 4;
 constexpr int kTcABufs = 4;
-constexpr int kTcDone = 8;            // barriers of finished units
 
 template <int G, int NP>
 struct TcShape {
@@ -73,16 +69,6 @@ struct TcLaunch {
     float* slots;       // two per block: the sums of its first and last row block
     uint32_t* counters;  // eight per block
 };
-
-// First unit of block b, and the block that has unit u.
-__host__ __device__ __forceinline__ int64_t tc_first(int64_t units, int64_t blocks, int64_t b) {
-    const int64_t more = units % blocks;
-    return units / blocks * b + (b < more ? b : more);
-}
-__device__ __forceinline__ int64_t tc_block_of(int64_t units, int64_t blocks, int64_t u) {
-    const int64_t each = units / blocks, more = units % blocks;
-    return u < more * (each + 1) ? u / (each + 1) : more + (u - more * (each + 1)) / each;
-}
 
 // A in the order of the decoded pairs, in rows of `ldo` (a multiple of 128), zero past
 // column K: out[8q + (0 4 1 5 2 6 3 7)] <- a[8q + (0 .. 7)] read by place: 0 4 1 5 2 6 3 7.
@@ -111,50 +97,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// 16 columns of this warp's lanes from registers.
-__device__ __forceinline__ void tc_store16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-// 16 or 32 columns of this warp's lanes to registers.
-__device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tc_load(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tc_before_sync() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_after_sync() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // The MMAs of a unit and the commit that reports them to `bar`, issued by one lane of
 // a converged warp.  In one block, with operands that are the same in all lanes: the
 // addresses then stay in uniform registers.  (Eight blocks with an election each took
@@ -192,12 +134,6 @@ __device__ __forceinline__ void tc_unit(uint32_t d, uint32_t a, uint64_t b, uint
         "n"(kBox), "n"(G > 32 ? 1 : 0), "n"(G > 64 ? 1 : 0)
         : "memory");
 }
-// K-major rows of 64 16-bit values in 128-byte swizzle, 8-row groups 1 KB apart.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) |
-           (1ull << 46) | (2ull << 61);
-}
-
 template <typename T, int G, int NP, bool ZERO>
 __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
     tg_gemm_w4_tc(const __grid_constant__ TcLaunch q, const __grid_constant__ CUtensorMap codes,
@@ -283,7 +219,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
         }
         // copies under way have to land before the block ends
         for (int i = issued > kTcCodeStages ? issued - kTcCodeStages : 0; i < issued; ++i)
-            if (lane == 0) op_bar_wait(c_full + 8 * (i % kTcCodeStages), i / kTcCodeStages & 1, kW4LandNs);
+            if (lane == 0) op_bar_wait(c_full + 8 * (i % kTcCodeStages), i / kTcCodeStages & 1, kTcLandNs);
     } else if (warp == 2) {
         // ------------------------------------------------------------ A
         op_wait_previous();
@@ -303,7 +239,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
         // copies under way have to land before the block ends: with their units' MMAs
         bool ok = true;
         for (int i = issued > kTcXStages ? issued - kTcXStages : 0; ok && i < issued; ++i)
-            if (lane == 0) ok = op_bar_wait(done + 8 * (i % kTcDone), i / kTcDone & 1, kW4LandNs);
+            if (lane == 0) ok = op_bar_wait(done + 8 * (i % kTcDone), i / kTcDone & 1, kTcLandNs);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t fmt = std::is_same<T, __half>::value ? 0u : 1u;
@@ -325,7 +261,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
         }
         // the MMAs have to be over before the tensor memory is given back
         if (issued > 0 && lane == 0)
-            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kW4LandNs);
+            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kTcLandNs);
         __syncwarp();
     } else if (warp >= 8 && warp < 20) {
         // ------------------------------------------------------------ decoding
@@ -338,7 +274,7 @@ __global__ void __launch_bounds__((TcShape<G, NP>::kThreads), 1)
             const uint32_t at = cs + s * kTcCodeBytes;
             uint4 w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) w[c] = w4_lds128(at + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+            for (int c = 0; c < 4; ++c) w[c] = tc_lds128(at + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
             uint32_t z[S::kGroups];
 #pragma unroll
             for (int c = 0; c < S::kGroups; ++c)

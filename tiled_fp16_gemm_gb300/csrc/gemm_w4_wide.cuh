@@ -44,8 +44,6 @@
 
 namespace tg {
 
-constexpr int kWideCluster = 2;
-constexpr int kWideThreads = 768;
 constexpr int kWideStages = 6;           // of codes
 constexpr int kWideXStages = 4;
 constexpr int kWideTokens = 256;         // of a tile at most
@@ -72,82 +70,6 @@ struct WideLaunch {
     uint32_t* counters;  // eight per block
 };
 
-// Address of this block's `addr` in block `rank` of the pair.
-__device__ __forceinline__ uint32_t wide_at(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ void wide_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// A box to this block, its bytes to a barrier of either block.
-__device__ __forceinline__ void wide_tma(uint32_t dst, const void* map, uint32_t bar, uint32_t x, uint32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-// The MMAs of a unit, then (LAST) the commits, to `done` and `free` of both blocks.  As
-// tc_unit, with one accumulator; `box`: the second 64 k of b, in 16 bytes.
-template <bool LAST>
-__device__ __forceinline__ void wide_unit(uint32_t d, uint32_t a, uint64_t b, uint32_t box, uint32_t idesc,
-                                          uint32_t add, uint32_t done, uint32_t free) {
-    asm volatile(
-        "{\n\t.reg .pred e, first, one, last;\n\t.reg .b32 ak;\n\t.reg .b64 bk, bx;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 first, %5, 0;\n\tsetp.eq.b32 one, 0, 0;\n\tsetp.ne.b32 last, %9, 0;\n\t"
-        "and.pred last, last, e;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %4, first;\n\t"
-        "add.u32 ak, %1, 8;\n\tadd.u64 bk, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "add.u32 ak, %1, 16;\n\tadd.u64 bk, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "add.u32 ak, %1, 24;\n\tadd.u64 bk, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "cvt.u64.u32 bx, %3;\n\tadd.u64 bk, %2, bx;\n\tadd.u32 ak, %1, 32;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 40;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 48;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "add.u64 bk, bk, 2;\n\tadd.u32 ak, %1, 56;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [ak], bk, %4, one;\n\t"
-        "@last tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%6], %8;\n\t"
-        "@last tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%7], %8;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(box), "r"(idesc), "r"(add), "r"(done), "r"(free),
-        "h"(static_cast<uint16_t>(3)), "n"(LAST ? 1 : 0)
-        : "memory");
-}
-
-// 16 sums of a share, which lie [token / 4][row][token % 4].
-__device__ __forceinline__ void wide_load(const float* from, float (&v)[16]) {
-#pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(from + m * kTcRows));
-        v[m] = f.x, v[m + 1] = f.y, v[m + 2] = f.z, v[m + 3] = f.w;
-    }
-}
-// Reports all MMAs so far to a barrier of both blocks.
-__device__ __forceinline__ void wide_commit(uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;\n\t}" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-// p + n, not before it is needed: sixteen addresses at once do not fit the registers.
-template <typename P>
-__device__ __forceinline__ P* wide_step(P* p, int64_t n) {
-    P* r;
-    asm volatile("add.s64 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(n));
-    return r;
-}
 // EXACT: sums that came out NaN, by the definition: Σ a·((c - z)·s), each weight exact in
 // fp32, and their epilogue.  A row of A with NaN or infinities has the sum of their products,
 // whatever the others are.  `seen`: which 16 of each 32 tokens from m0 on, `nan`: which of them.
@@ -288,7 +210,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     tc_before_sync();
     __syncthreads();
-    w4_cluster_sync();  // no copy or commit reaches a block before its barriers are there
+    tc_cluster_sync();  // no copy or commit reaches a block before its barriers are there
     tc_after_sync();
     // all columns are this block's, so they begin at 0
     constexpr uint32_t tmem = 0;
@@ -335,7 +257,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // copies under way have to land before the block ends
         bool ok = true;
         for (int i = issued > kWideStages ? issued - kWideStages : 0; ok && i < issued; ++i)
-            if (lane == 0) ok = op_bar_wait(c_full + 8 * (i % kWideStages), i / kWideStages & 1, kW4LandNs);
+            if (lane == 0) ok = op_bar_wait(c_full + 8 * (i % kWideStages), i / kWideStages & 1, kTcLandNs);
     } else if (warp == 2) {
         // ------------------------------------------------------------ A
         op_wait_previous();
@@ -356,7 +278,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // the copies have to land, and the commits to arrive, before this block ends
         bool ok = true;
         for (int i = issued > kWideXStages ? issued - kWideXStages : 0; ok && i < issued; ++i)
-            if (lane == 0) ok = op_bar_wait(x_empty + 8 * (i % kWideXStages), i / kWideXStages & 1, kW4LandNs);
+            if (lane == 0) ok = op_bar_wait(x_empty + 8 * (i % kWideXStages), i / kWideXStages & 1, kTcLandNs);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
@@ -383,7 +305,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         // the MMAs have to be over before the tensor memory is given back
         if (issued > 0 && lane == 0)
-            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kW4LandNs);
+            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kTcLandNs);
         __syncwarp();
     } else if (warp >= 8 && warp < 20) {
         // ------------------------------------------------------------ decoding
@@ -396,7 +318,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint32_t at = cs + s * kWideCodeBytes;
             uint4 w[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) w[c] = w4_lds128(at + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+            for (int c = 0; c < 4; ++c) w[c] = tc_lds128(at + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
             uint32_t z[kGroups];
             T scale[kGroups];
 #pragma unroll
@@ -533,7 +455,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     __syncthreads();
     if (threadIdx.x == 0 && *dead != 0) atomicOr(q.timeouts, kOpTimeoutW4);
     __syncwarp();
-    w4_cluster_sync();  // neither block's memory or barriers are used by the other any more
+    tc_cluster_sync();  // neither block's memory or barriers are used by the other any more
     if (warp == 1) {
         __syncwarp();
         tc_after_sync();
