@@ -239,3 +239,24 @@ def test_refusals(tg):
     odd = torch.zeros(64, 40, dtype=torch.int8, device="cuda")
     with pytest.raises(tg.TgemmError):
         tg.gemm_i8(a[:, :40], odd, sa, sb)
+
+
+def test_a_wait_that_runs_out_is_reported_once(tg):
+    """Codes that never come: the kernel gives up within its limit and returns, the status
+    says so once, and the next call is right."""
+    a, b, sa, sb, _ = make(100, 1000, 900)
+    want = tg.gemm_i8(a, b, sa, sb)
+    tg.sync_status()
+    try:
+        tg.tg_debug_set_wait_timeout_ns(20_000_000)
+        tg.tg_debug_inject(1)
+        tg.gemm_i8(a, b, sa, sb)
+        with pytest.raises(tg.TgemmError) as e:
+            tg.sync_status()
+        assert e.value.status == tg.TG_ERR_TIMEOUT
+        tg.sync_status()
+    finally:
+        tg.tg_debug_inject(0)
+        tg.tg_debug_set_wait_timeout_ns(0)
+    assert torch.equal(tg.gemm_i8(a, b, sa, sb), want)
+    tg.sync_status()

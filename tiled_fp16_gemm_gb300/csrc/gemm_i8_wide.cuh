@@ -1,0 +1,375 @@
+// Products of many rows of A with 8-bit integers, on tcgen05.
+//
+// sm_103a has no integer form of tcgen05.mma, and that of mma.sync has a fifteenth of the rate of
+// tcgen05 in fp16; but whole numbers up to 2048 are exact in fp16, their products exact in the
+// fp16 MMA, and sums of them exact in its fp32 accumulator up to 2^24.  So B is decoded to
+// fp16 on the way: the structure of gemm_w4_wide.cuh, with a weight's bytes instead of nibbles,
+// no scale before the epilogue, and A as fp16 in the workspace (tg_i8_expand).
+//
+// Units of 128 rows of B by 128 k are the MMA's A operand, decoded by threads that own a row
+// into tensor memory; the pair of blocks of a cluster multiplies 256 rows of B by up to 256
+// tokens.  Roles of a block's 24 warps, as there: 0 fetches B, 2 this block's half of the
+// tokens, 1 of the even block issues the MMAs, 8-19 decode, 4-7 and 20-23 write C.  The
+// clusters have whole tiles, or share all units evenly: then each block leaves its sums of a
+// shared tile in the workspace, and the last one to come adds all of them in the order of k.
+#pragma once
+
+#include "gemm_i8.cuh"
+#include "tc_device.cuh"
+
+namespace tg {
+
+constexpr int kI8Stages = 6;  // of B
+constexpr int kI8XStages = 4;
+constexpr int kI8Tokens = 256;  // of a tile at most
+constexpr int kI8CodeBytes = kTcRows * kTcK;
+constexpr int kI8XBytes = kI8Tokens / 2 * 256;
+constexpr int kI8WideSmem = 1024 + kI8XStages * kI8XBytes + kI8Stages * kI8CodeBytes + 512;
+constexpr int kI8MaxClusters = 80;
+constexpr int64_t kI8CounterBytes = 8192;
+static_assert(kI8MaxClusters * kWideCluster * 32 <= kI8CounterBytes, "eight counters per block");
+
+struct I8Wide {
+    I8Params p;
+    uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a warp gives up on a wait
+    int32_t inject;      // 1: block 0's first codes are left out (for tests of the limit)
+    int32_t tokens;      // of a tile: a multiple of 32
+    int32_t m_tiles;
+    int32_t k_units;
+    int64_t units;       // in all: (row blocks / cluster) · m_tiles · k_units
+    int32_t grain;       // units that stay together: k_units (whole tiles) or 1
+    int32_t clusters;
+    float* slots;        // two per block: the sums of its first and last tile
+    uint32_t* counters;  // eight per block, zeroed by tg_i8_expand
+};
+
+// Four codes of a word as two pairs of fp16: with the sign turned, a byte u is code + 128, the
+// fp16 number 0x6400 | u is 1024 + u, and 1152 less is the code, exactly.
+__device__ __forceinline__ void i8_decode(uint32_t word, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = word ^ 0x80808080u;
+    const uint32_t off = 0x64806480u;  // 1152, twice
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(off));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(off));
+}
+
+// A as fp16 in rows of `ldo` (a multiple of 128), zero past column K; and the counters zeroed.
+__global__ void __launch_bounds__(256)
+    tg_i8_expand(const int8_t* __restrict__ A, int64_t lda, int64_t M, int64_t K, uint16_t* __restrict__ out,
+                 int64_t ldo, uint32_t* counters) {
+    op_wait_previous();
+    op_release_next();
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < kI8CounterBytes / 4; i += 256) counters[i] = 0;
+    const int64_t c = int64_t{blockIdx.x} * 256 + threadIdx.x;
+    if (16 * c >= ldo) return;
+    const bool wide = (reinterpret_cast<uintptr_t>(A) & 15) == 0 && lda % 16 == 0 && 16 * c + 16 <= K;
+    for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+        const int8_t* a = A + m * lda;
+        const uint4 x = wide ? *reinterpret_cast<const uint4*>(a + 16 * c) : i8_bytes(a, 16 * c, K);
+        uint4 y[2];
+        i8_decode(x.x, y[0].x, y[0].y);
+        i8_decode(x.y, y[0].z, y[0].w);
+        i8_decode(x.z, y[1].x, y[1].y);
+        i8_decode(x.w, y[1].z, y[1].w);
+        uint4* to = reinterpret_cast<uint4*>(out + m * ldo + 16 * c);
+        to[0] = y[0];
+        to[1] = y[1];
+    }
+}
+
+// Epilogue and store of 16 tokens of row n, `most` of them.
+template <typename TC>
+__device__ __forceinline__ void i8_wide_store(const I8Params& p, int64_t m, int64_t n, int most, float sb, float bias,
+                                              float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i8_value(p, v[i], i < most ? p.sa[m + i] : 0.0f, sb, bias);
+    if (p.resid != nullptr) {
+        const char* r = static_cast<const char*>(p.resid) + sizeof(TC) * (m * p.ldr + n);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i < most) v[i] += op_to_float(*reinterpret_cast<const TC*>(r));
+            r = wide_step(r, sizeof(TC) * p.ldr);
+        }
+    }
+    char* c = static_cast<char*>(p.C) + sizeof(TC) * (m * p.ldc + n);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i < most) *reinterpret_cast<TC*>(c) = op_round<TC>(v[i]);
+        c = wide_step(c, sizeof(TC) * p.ldc);
+    }
+}
+
+template <typename TC>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    tg_gemm_i8_wide(const __grid_constant__ I8Wide q, const __grid_constant__ CUtensorMap codes,
+                    const __grid_constant__ CUtensorMap order) {
+    constexpr int kABufs = 4, kACols = 64;
+    extern __shared__ __align__(1024) unsigned char wide_dynamic[];
+    const I8Params& p = q.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = blockIdx.x % kWideCluster, cluster_no = blockIdx.x / kWideCluster;
+    const uint32_t base = (op_smem(wide_dynamic) + 1023) & ~1023u;
+    unsigned char* const shared = wide_dynamic + (base - op_smem(wide_dynamic));
+    const uint32_t xs = base, cs = xs + kI8XStages * kI8XBytes;
+    const uint32_t bars = cs + kI8Stages * kI8CodeBytes;
+    const uint32_t c_full = bars, c_empty = c_full + 8 * kI8Stages;
+    const uint32_t x_full = c_empty + 8 * kI8Stages, x_empty = x_full + 8 * kI8XStages;
+    const uint32_t a_full = x_empty + 8 * kI8XStages, done = a_full + 8 * kABufs;
+    const uint32_t d_full = done + 8 * kTcDone, d_empty = d_full + 8;
+    unsigned char* after = shared + (d_empty + 8 - base);
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(after);
+    volatile int* dead = reinterpret_cast<volatile int*>(after + 4);  // a wait ran out: reported at the end
+
+    op_release_next();
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < kI8Stages; ++i) {
+            op_bar_init(c_full + 8 * i, 1);
+            op_bar_init(c_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < kI8XStages; ++i) {
+            op_bar_init(x_full + 8 * i, 1);  // of the even block: both blocks' copies
+            op_bar_init(x_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kABufs; ++i) op_bar_init(a_full + 8 * i, 8);  // of the even block
+        for (int i = 0; i < kTcDone; ++i) op_bar_init(done + 8 * i, 1);
+        op_bar_init(d_full, 1);
+        op_bar_init(d_empty, 16);  // of the even block
+        op_bar_init_done();
+        *dead = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         op_smem(tmem_at))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_before_sync();
+    __syncthreads();
+    tc_cluster_sync();  // no copy or commit reaches a block before its barriers are there
+    tc_after_sync();
+    // all columns are this block's, so they begin at 0
+    constexpr uint32_t tmem = 0;
+    constexpr uint32_t d_cols = tmem + 256;
+
+    const int64_t grains = q.units / q.grain;
+    const int64_t u0 = tc_first(grains, q.clusters, cluster_no) * q.grain;
+    const int n_units =
+        static_cast<int>(tc_first(grains, q.clusters, cluster_no + 1) * q.grain - u0);
+    int64_t tile = u0 / q.k_units;
+    int kb = static_cast<int>(u0 - tile * q.k_units);
+    // A warp waits; false once a wait has run out, here or in another warp.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, op_bar_try(bar, parity))) return true;
+        const bool ok = *dead == 0 && op_bar_wait_slow(bar, parity, q.limit_ns);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (lane == 0) *dead = 1;
+        __syncwarp();
+        return false;
+    };
+    auto next_unit = [&] {
+        if (++kb == q.k_units) kb = 0, ++tile;
+    };
+    auto first_row = [&] { return (tile / q.m_tiles * kWideCluster + rank) * kTcRows; };
+    auto first_token = [&] { return tile % q.m_tiles * q.tokens; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ B
+        // No wait for tg_i8_expand: B is not its work, and it let this kernel start only after
+        // everything before it was done.
+        int issued = 0;
+        for (int i = 0; i < n_units; ++i, next_unit()) {
+            const int s = i % kI8Stages;
+            if (i >= kI8Stages && !wait(c_empty + 8 * s, (i / kI8Stages - 1) & 1)) break;
+            if (lane == 0 && !(q.inject == 1 && blockIdx.x == 0 && i == 0)) {
+                const uint32_t bar = c_full + 8 * s;
+                op_bar_expect(bar, kI8CodeBytes);
+                op_tma_2d(cs + s * kI8CodeBytes, &codes, bar, kb * kTcK, static_cast<uint32_t>(first_row()));
+            }
+            issued = i + 1;
+        }
+        // copies under way have to land before the block ends
+        bool ok = true;
+        for (int i = issued > kI8Stages ? issued - kI8Stages : 0; ok && i < issued; ++i)
+            if (lane == 0) ok = op_bar_wait(c_full + 8 * (i % kI8Stages), i / kI8Stages & 1, kTcLandNs);
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ A
+        op_wait_previous();
+        const uint32_t part = q.tokens / 2;
+        int issued = 0;
+        for (int i = 0; i < n_units; ++i, next_unit()) {
+            const int s = i % kI8XStages;
+            if (i >= kI8XStages && !wait(x_empty + 8 * s, (i / kI8XStages - 1) & 1)) break;
+            if (lane == 0) {
+                const uint32_t to = xs + s * kI8XBytes, bar = wide_at(x_full + 8 * s, 0);
+                const uint32_t m = static_cast<uint32_t>(first_token()) + rank * part;
+                if (rank == 0) op_bar_expect(x_full + 8 * s, q.tokens * 256);
+                wide_tma(to, &order, bar, kb * kTcK, m);
+                wide_tma(to + part * 128, &order, bar, kb * kTcK + 64, m);
+            }
+            issued = i + 1;
+        }
+        // the copies have to land, and the commits to arrive, before this block ends
+        bool ok = true;
+        for (int i = issued > kI8XStages ? issued - kI8XStages : 0; ok && i < issued; ++i)
+            if (lane == 0) ok = op_bar_wait(x_empty + 8 * (i % kI8XStages), i / kI8XStages & 1, kTcLandNs);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(q.tokens >> 3) << 17) | (16u << 24);
+        int issued = 0, tiles = 0;
+        for (int i = 0; rank == 0 && i < n_units; ++i) {
+            const int s = i % kI8XStages, a = i % kABufs;
+            const bool first = i == 0 || kb == 0;
+            if (!wait(x_full + 8 * s, i / kI8XStages & 1)) break;
+            if (first && tiles++ > 0 && !wait(d_empty, tiles & 1)) break;
+            if (!wait(a_full + 8 * a, i / kABufs & 1)) break;
+            tc_after_sync();
+            wide_unit<true>(d_cols, tmem + kACols * a, tc_desc(xs + s * kI8XBytes), q.tokens / 2 * 128 / 16, idesc,
+                            first ? 0 : 1, done + 8 * (i % kTcDone), x_empty + 8 * s);
+            if (kb + 1 == q.k_units || i + 1 == n_units) wide_commit(d_full);
+            issued = i + 1;
+            next_unit();
+        }
+        // the MMAs have to be over before the tensor memory is given back
+        if (issued > 0 && lane == 0)
+            op_bar_wait(done + 8 * ((issued - 1) % kTcDone), (issued - 1) / kTcDone & 1, kTcLandNs);
+        __syncwarp();
+    } else if (warp >= 8 && warp < 20) {
+        // ------------------------------------------------------------ decoding
+        const int group = (warp - 8) >> 2;
+        const uint32_t row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        for (int i = group; i < n_units; i += kTcGroups) {
+            const int s = i % kI8Stages, a = i % kABufs;
+            if (!wait(c_full + 8 * s, i / kI8Stages & 1)) break;
+            const uint32_t at = cs + s * kI8CodeBytes + row * 128;
+            uint4 w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) w[c] = tc_lds128(at + ((c ^ (row & 7)) << 4));
+            const int old = i - kABufs;
+            if (old >= 0 && !wait(done + 8 * (old % kTcDone), old / kTcDone & 1)) break;
+            tc_after_sync();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[16];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 x = w[2 * c + j];
+                    i8_decode(x.x, r[8 * j], r[8 * j + 1]);
+                    i8_decode(x.y, r[8 * j + 2], r[8 * j + 3]);
+                    i8_decode(x.z, r[8 * j + 4], r[8 * j + 5]);
+                    i8_decode(x.w, r[8 * j + 6], r[8 * j + 7]);
+                }
+                tc_store16(tmem + lanes + kACols * a + 16 * c, r);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                wide_arrive(wide_at(a_full + 8 * a, 0));
+                // not before the codes have been used (see gemm_w4_wide.cuh)
+                tc_arrive(c_empty + 8 * s);
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ C
+        op_wait_previous();
+        const int quarter = warp & 3, set = warp < 8 ? 0 : 1;
+        const uint32_t row = 32 * quarter + lane;
+        const uint32_t at = d_cols + (static_cast<uint32_t>(32 * quarter) << 16);
+        const int64_t slot = int64_t{q.tokens} * kTcRows;
+        int i = 0;
+        uint32_t tiles = 0;
+        while (i < n_units) {
+            const int kb0 = kb;
+            const int len = q.k_units - kb < n_units - i ? q.k_units - kb : n_units - i;
+            // (a barrier of its own: a parity says nothing of a phase further off than one)
+            if (!wait(d_full, tiles++ & 1)) break;
+            tc_after_sync();
+            const int64_t n = first_row() + row, m0 = first_token();
+            const int tokens = static_cast<int>(p.M - m0 < q.tokens ? p.M - m0 : q.tokens);
+            const bool whole = len == q.k_units;
+            const float bias = p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
+            const float sb = n < p.N ? p.sb[n] : 0.0f;
+            float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
+            for (int c = 16 * set; c < tokens; c += 32) {
+                uint32_t r[16];
+                tc_load(at + c, r);
+                if (whole) {
+                    float v[16];
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) v[m] = __uint_as_float(r[m]);
+                    if (n < p.N) i8_wide_store<TC>(p, m0 + c, n, tokens - c, sb, bias, v);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 16; m += 4)
+                        __stcg(reinterpret_cast<float4*>(mine + (c + m) * kTcRows),
+                               make_float4(__uint_as_float(r[m]), __uint_as_float(r[m + 1]),
+                                           __uint_as_float(r[m + 2]), __uint_as_float(r[m + 3])));
+                }
+            }
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) wide_arrive(wide_at(d_empty, 0));
+            if (!whole) {  // a share of a tile
+                __threadfence();
+                __syncwarp();
+                const int head = static_cast<int>(tc_block_of(q.units, q.clusters, tile * q.k_units));
+                const int tail = static_cast<int>(tc_block_of(q.units, q.clusters, (tile + 1) * q.k_units - 1));
+                uint32_t before = 0;
+                if (lane == 0) {
+                    uint32_t* count = q.counters + 8 * (head * kWideCluster + rank) + 4 * set + quarter;
+                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                                 : "=r"(before)
+                                 : "l"(count)
+                                 : "memory");
+                }
+                before = __shfl_sync(0xffffffffu, before, 0);
+                __threadfence();
+                if (before == static_cast<uint32_t>(tail - head)) {
+                    // the head's share is in its second slot, the others' in their first
+                    for (int c = 16 * set; c < tokens; c += 32) {
+                        float sum[16];
+                        const float* from = q.slots + (2 * (int64_t{head} * kWideCluster + rank) + 1) * slot +
+                                            c * kTcRows + row * 4;
+                        wide_load(from, sum);
+                        // two at a time under way
+                        from = q.slots + 2 * (int64_t{head + 1} * kWideCluster + rank) * slot + c * kTcRows +
+                               row * 4;
+                        const int64_t step = 2 * kWideCluster * slot;
+                        for (int b = head + 1; b <= tail; b += 2, from += 2 * step) {
+                            float v[16], w[16];
+                            wide_load(from, v);
+                            if (b < tail) wide_load(from + step, w);
+#pragma unroll
+                            for (int m = 0; m < 16; ++m) sum[m] += v[m];
+                            if (b < tail) {
+#pragma unroll
+                                for (int m = 0; m < 16; ++m) sum[m] += w[m];
+                            }
+                        }
+                        if (n < p.N) i8_wide_store<TC>(p, m0 + c, n, tokens - c, sb, bias, sum);
+                    }
+                }
+            }
+            i += len;
+            kb = 0;
+            ++tile;
+        }
+    }
+    tc_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && *dead != 0) atomicOr(q.timeouts, kOpTimeoutI8);
+    __syncwarp();
+    tc_cluster_sync();  // neither block's memory or barriers are used by the other any more
+    if (warp == 1) {
+        __syncwarp();
+        tc_after_sync();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(*tmem_at)
+                     : "memory");
+    }
+}
+
+}  // namespace tg

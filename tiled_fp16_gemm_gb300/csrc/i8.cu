@@ -1,8 +1,9 @@
 // tg_gemm_i8 (include/tgemm.h): argument checks and launches.  The kernels and the
-// formulas: gemm_i8.cuh.
+// formulas: gemm_i8.cuh and gemm_i8_wide.cuh.
 #include <cstring>
 
 #include "gemm_i8.cuh"
+#include "gemm_i8_wide.cuh"
 #include "op_host.h"
 
 namespace {
@@ -10,26 +11,31 @@ namespace {
 using tg::I8Params;
 
 constexpr int64_t kMaxK = 131071;  // 2^17 - 1: a sum of K products of -128 · -128 fits 32 bits
+constexpr int64_t kFewRows = 8;    // of A, that take the kernel for few
 
 bool misaligned(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 
-// One launch with dependent launch allowed.
+// One launch with dependent launch allowed, in clusters of `cluster` blocks.
 template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                   Given... given) {
+tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
+                   cudaStream_t s, Given... given) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
         cudaGetLastError();
         return TG_ERR_LAUNCH;
@@ -37,14 +43,211 @@ tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
     return TG_OK;
 }
 
-template <typename TC>
-tg_status_t launch_type(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s) {
-    const int64_t blocks = (p.M * p.N + 7) / 8, most = 8 * int64_t{dev.num_sms};
-    return launch(tg::tg_gemm_i8_simple<TC>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, s,
-                  p);
+constexpr int kSmem = 226 * 1024;
+
+// Clusters of `size` blocks that the device holds at once, for a kernel opted into `smem`.
+template <typename Kernel>
+int max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
+    if (size == 1) return dev.num_sms;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(size);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
 }
 
-int64_t workspace_bytes(int64_t M, int64_t N, int64_t K) { return 0 * M * N * K; }
+// What a device holds of a kernel that uses clusters, asked once.
+struct Limits {
+    std::once_flag once;
+    int clusters[4] = {};  // of 1, 2, 4, 8 blocks; 0: the kernel cannot run
+};
+template <typename Kernel>
+const Limits& limits_of(Kernel kernel, int threads, int smem, const tg::OpDevice& dev, Limits* all) {
+    Limits& lim = all[dev.dev];
+    std::call_once(lim.once, [&] {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess)
+            for (int i = 0; i < 4; ++i) lim.clusters[i] = max_clusters(kernel, 1 << i, threads, smem, dev);
+        cudaGetLastError();
+    });
+    return lim;
+}
+
+// Few rows of A (NT: tokens / 8).  False where no shape fits: then nothing is launched.
+template <typename TC, int NT>
+bool launch_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_status_t* st) {
+    auto kernel = tg::tg_gemm_i8_few<TC, NT>;
+    static Limits limits[tg::kOpMaxDevices];
+    const Limits& lim = limits_of(kernel, tg::kI8FewThreads, kSmem, dev, limits);
+    tg::I8Few q, best;
+    std::memset(&q, 0, sizeof(q));
+    q.p = p;
+    const int64_t tiles = (p.N + 15) / 16;
+    q.tiles = static_cast<int32_t>(tiles);
+    q.chunks = static_cast<int32_t>((p.K + 63) / 64);
+    // The shape with the least time, in steps of a block's warps (16 KB of B, about 0.37 us):
+    // the steps of a block, the fetch of its part of A, and the joins of a cluster.
+    double least = 1e300;
+    size_t smem = 0;
+    int64_t grid = 0;
+    for (int i = 0; i < 4; ++i) {
+        q.cluster = 1 << i;
+        if (q.cluster > q.chunks || lim.clusters[i] < 1) break;
+        const int64_t slice = (q.chunks + q.cluster - 1) / q.cluster;
+        q.x_pitch = static_cast<int32_t>((slice * 64 + 127) / 128 * 128 + 64);
+        int64_t clusters = tiles < lim.clusters[i] ? tiles : lim.clusters[i];
+        // (a block keeps the sums of its tiles: very many rows of B take several waves)
+        const int64_t room = (kSmem - 512 - p.M * q.x_pitch) / (p.M * 64) * q.cluster;
+        if (room < 1) continue;
+        int64_t rounds = (tiles + clusters - 1) / clusters;
+        if (rounds > room) {
+            rounds = room;
+            clusters = (tiles + rounds - 1) / rounds;
+        }
+        q.rounds = static_cast<int32_t>(rounds);
+        const int64_t waves = (clusters + lim.clusters[i] - 1) / lim.clusters[i];
+        q.sums_pitch = static_cast<int32_t>((rounds + q.cluster - 1) / q.cluster * 16 + 4);
+        const int64_t bytes = p.M * (q.x_pitch + 4 * int64_t{q.sums_pitch});
+        if (bytes > kSmem) continue;
+        const double steps = static_cast<double>((rounds * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps);
+        const double time = static_cast<double>(waves) *
+                            (steps + 2e-5 * static_cast<double>(slice * 64 * p.M) + (q.cluster > 1 ? 3.0 : 0.0));
+        if (time < least) {
+            least = time;
+            best = q;
+            smem = static_cast<size_t>(bytes);
+            grid = clusters * q.cluster;
+        }
+    }
+    if (least > 1e299 || grid > tg::kOpMaxDim) return false;
+    *st = launch(kernel, dim3(static_cast<unsigned>(grid)), tg::kI8FewThreads, smem, best.cluster, s, best);
+    return true;
+}
+
+// ------------------------------------------------------------------ many rows
+
+tg::OpWorkspace g_workspace;  // where the caller has none
+
+// Rows of A at a time: fp16 rows of A take 1 GB at most.
+int64_t slab_rows(int64_t M, int64_t K) {
+    const int64_t ldo = (K + tg::kTcK - 1) / tg::kTcK * tg::kTcK;
+    const int64_t rows = (int64_t{1} << 29) / ldo / tg::kI8Tokens * tg::kI8Tokens;
+    return M < rows ? M : rows;
+}
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// Fills in the tile's width and the division of the work with the least time, as plan_wide
+// of w4.cu does.
+void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
+    q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
+    constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
+    const int64_t row_tiles = (p.N + rows - 1) / rows;
+    double least = 1e300;
+    for (int32_t tokens = 32; tokens <= tg::kI8Tokens; tokens += 32) {
+        const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
+        const double mma = 0.0024 * tokens;
+        const double unit = mma < 0.43 ? 0.43 : mma;
+        for (const int32_t grain : {q->k_units, 1}) {
+            const int64_t grains = tiles * q->k_units / grain;
+            const int64_t clusters = grains < limit ? grains : limit;
+            const int64_t most = (grains + clusters - 1) / clusters * grain;
+            double time = unit * static_cast<double>(most);
+            if (grain != q->k_units && (most % q->k_units != 0 || grains % clusters != 0))
+                time += 4.0 + 0.018 * tokens * (2.0 + static_cast<double>(q->k_units) / static_cast<double>(most));
+            if (time < least) {
+                least = time;
+                q->tokens = tokens;
+                q->m_tiles = static_cast<int32_t>(m_tiles);
+                q->grain = grain;
+                q->clusters = static_cast<int32_t>(clusters);
+                q->units = tiles * q->k_units;
+            }
+        }
+    }
+}
+
+// Counters, the blocks' shares of sums (two each), A as fp16: for any plan of these sizes.
+int64_t slot_bytes(int64_t M) {
+    const int64_t tokens = M < tg::kI8Tokens ? up(M, 32) : tg::kI8Tokens;
+    return 2 * int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tokens * tg::kTcRows * 4;
+}
+int64_t workspace_bytes(int64_t M, int64_t, int64_t K) {
+    if (M <= kFewRows || K == 0) return 0;
+    return tg::kI8CounterBytes + slot_bytes(M) + slab_rows(M, K) * up(K, tg::kTcK) * 2;
+}
+
+template <typename TC>
+tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws, cudaStream_t s) {
+    auto kernel = tg::tg_gemm_i8_wide<TC>;
+    static Limits limits[tg::kOpMaxDevices];
+    const Limits& lim = limits_of(kernel, tg::kWideThreads, tg::kI8WideSmem, dev, limits);
+    if (lim.clusters[1] < 1) return TG_ERR_LAUNCH;
+    tg::OpWorkspace::Hold hold;  // until the last product is launched
+    if (ws == nullptr) {
+        const tg_status_t st = g_workspace.get(
+            dev.dev, s, static_cast<size_t>(workspace_bytes(whole.M, whole.N, whole.K)), &ws, &hold);
+        if (st != TG_OK) return st;
+    }
+    tg::I8Wide q;
+    std::memset(&q, 0, sizeof(q));
+    q.limit_ns = tg::op_wait_limit_ns();
+    q.timeouts = dev.timeouts;
+    q.counters = static_cast<uint32_t*>(ws);
+    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + tg::kI8CounterBytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + tg::kI8CounterBytes + slot_bytes(whole.M));
+    const int64_t ldo = up(whole.K, tg::kTcK), slab = slab_rows(whole.M, whole.K);
+    CUtensorMap codes, ordered;
+    if (!tg::op_map_2d(&codes, whole.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, whole.K, whole.N, whole.ldb, tg::kTcK,
+                       tg::kTcRows, CU_TENSOR_MAP_SWIZZLE_128B))
+        return TG_ERR_LAUNCH;
+    const int elem = sizeof(TC);
+    for (int64_t m = 0; m < whole.M; m += slab) {
+        I8Params& p = q.p;
+        p = whole;
+        p.M = whole.M - m < slab ? whole.M - m : slab;
+        p.A += m * p.lda;
+        p.sa += m;
+        p.C = static_cast<char*>(p.C) + m * p.ldc * elem;
+        if (p.resid != nullptr) p.resid = static_cast<const char*>(p.resid) + m * p.ldr * elem;
+        const int64_t limit = lim.clusters[1] < tg::kI8MaxClusters ? lim.clusters[1] : tg::kI8MaxClusters;
+        plan_wide(p, limit, &q);
+        if (!tg::op_map_2d(&ordered, order, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ldo, p.M, ldo * 2, 64,
+                           static_cast<uint32_t>(q.tokens / tg::kWideCluster), CU_TENSOR_MAP_SWIZZLE_128B))
+            return TG_ERR_LAUNCH;
+        q.inject = tg::op_take_inject();
+        tg_status_t st = launch(tg::tg_i8_expand,
+                                dim3(static_cast<unsigned>((ldo / 16 + 255) / 256),
+                                     static_cast<unsigned>(p.M < 32768 ? p.M : 32768)),
+                                256, 0, 1, s, p.A, p.lda, p.M, p.K, order, ldo, q.counters);
+        if (st != TG_OK) return st;
+        st = launch(kernel, dim3(static_cast<unsigned>(q.clusters * tg::kWideCluster)), tg::kWideThreads,
+                    tg::kI8WideSmem, tg::kWideCluster, s, q, codes, ordered);
+        if (st != TG_OK) return st;
+    }
+    return TG_OK;
+}
+
+template <typename TC>
+tg_status_t launch_type(const I8Params& p, const tg::OpDevice& dev, void* ws, cudaStream_t s) {
+    tg_status_t st;
+    if (p.K > 0 && p.M <= kFewRows && launch_few<TC, 1>(p, dev, s, &st)) return st;
+    if (p.K > 0 && p.M > kFewRows) return launch_wide<TC>(p, dev, ws, s);
+    const int64_t blocks = (p.M * p.N + 7) / 8, most = 8 * int64_t{dev.num_sms};
+    return launch(tg::tg_gemm_i8_simple<TC>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, 1, s,
+                  p);
+}
 
 tg_status_t gemm_i8(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
                     const float* sb, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
@@ -92,8 +295,8 @@ tg_status_t gemm_i8(const int8_t* A, int64_t lda, const float* sa, const int8_t*
     p.K = K;
     p.relu = x.activation == TG_EPI_RELU ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (x.out_dtype == TG_DTYPE_F32) return launch_type<float>(p, dev, s);
-    return x.out_dtype == TG_DTYPE_F16 ? launch_type<__half>(p, dev, s) : launch_type<__nv_bfloat16>(p, dev, s);
+    if (x.out_dtype == TG_DTYPE_F32) return launch_type<float>(p, dev, workspace, s);
+    return x.out_dtype == TG_DTYPE_F16 ? launch_type<__half>(p, dev, workspace, s) : launch_type<__nv_bfloat16>(p, dev, workspace, s);
 }
 
 }  // namespace

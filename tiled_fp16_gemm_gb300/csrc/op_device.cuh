@@ -42,6 +42,7 @@ __device__ __forceinline__ void op_release_next() {
 // Bits of the device's word for waits that ran out (the GEMM's kernels have the low ones).
 constexpr unsigned int kOpTimeoutW4 = 1u << 16;
 constexpr unsigned int kOpTimeoutNorm = 1u << 17;
+constexpr unsigned int kOpTimeoutI8 = 1u << 18;
 
 // ------------------------------------------------------------------ mbarriers and TMA
 
