@@ -241,10 +241,11 @@ def test_refusals(tg):
         tg.gemm_i8(a[:, :40], odd, sa, sb)
 
 
-def test_a_wait_that_runs_out_is_reported_once(tg):
+@pytest.mark.parametrize("M", [3, 100])
+def test_a_wait_that_runs_out_is_reported_once(tg, M):
     """Codes that never come: the kernel gives up within its limit and returns, the status
     says so once, and the next call is right."""
-    a, b, sa, sb, _ = make(100, 1000, 900)
+    a, b, sa, sb, _ = make(M, 1000, 900)
     want = tg.gemm_i8(a, b, sa, sb)
     tg.sync_status()
     try:

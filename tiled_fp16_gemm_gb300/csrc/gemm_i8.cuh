@@ -4,6 +4,7 @@
 #pragma once
 
 #include "op_device.cuh"
+#include "tc_device.cuh"
 
 namespace tg {
 
@@ -31,29 +32,38 @@ __device__ __forceinline__ float i8_value(const I8Params& p, float sum, float sa
 
 // ------------------------------------------------------------------ few rows of A
 //
-// Up to 16 tokens: B's bytes are what counts, each read once and straight into the operands of
-// mma.sync (m16n8k32, s8 to s32), B's rows on the side of 16, the tokens on that of 8.  The sums
-// are 32-bit integers, exact in any order, so the order is free everywhere:
+// Up to 16 tokens: B's bytes are what counts, each read once.  They come by TMA (zeros past the
+// edges) and go from shared memory straight into the operands of mma.sync (m16n8k32, s8 to s32),
+// B's rows on the side of 16, the tokens on that of 8.  The sums are 32-bit integers, exact in
+// any order, so the order is free everywhere:
 //   - k: a lane takes 16 neighbouring bytes of a row for two MMAs, and the same bytes of a token;
-//   - the warps of a block share out steps of 16 rows by 64 k one by one, whatever tile they
+//   - the warps of a block share out steps of 16 rows by 128 k one by one, whatever tile they
 //     belong to, and add what they have of a tile to its sums in shared memory;
 //   - the blocks of a cluster share k too, and add to the sums in the shared memory of the
 //     tile's owner.  No scratch in global memory, one join at the end.
-// A warp has kI8Depth steps under way in registers (48 a lane), across the borders of tiles.
+// Each warp has a ring of its own, which its first lane fills some steps ahead, across the
+// borders of tiles.
 //
 // The MMA's rate here is 273 products a cycle of an SM, 34 bytes of B: for 8 tokens more than
 // memory delivers (23), for 16 half of it.
 
 constexpr int kI8FewWarps = 16;
 constexpr int kI8FewThreads = 32 * kI8FewWarps;
-constexpr int kI8Depth = 6;
+constexpr int kI8FewRows = 16;
+constexpr int kI8FewK = 128;
+constexpr int kI8FewStep = kI8FewRows * kI8FewK;
+constexpr int kI8FewStages = 6;  // at most
+constexpr int kI8FewBars = kI8FewWarps * kI8FewStages * 8;
 
 struct I8Few {
     I8Params p;
+    uint64_t limit_ns;
+    unsigned int* timeouts;  // set where a warp gives up on a wait
+    int32_t inject;    // 1: block 0's first step is not fetched (for tests of the limit)
     int32_t cluster;   // blocks that share tiles and split k
-    int32_t rounds;    // tiles of 16 rows of a cluster, at most
-    int32_t tiles;     // in all
-    int32_t chunks;    // of 64 k, in all
+    int32_t tiles;     // of 16 rows, in all
+    int32_t chunks;    // of 128 k, in all
+    int32_t stages;
     int32_t x_pitch;   // bytes of a token in shared memory
     int32_t sums_pitch;  // words of a token's sums
 };
@@ -65,14 +75,6 @@ __device__ __forceinline__ void i8_mma(int (&c)[4], uint32_t a0, uint32_t a1, ui
         "{%0, %1, %2, %3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Bytes that are read once.
-__device__ __forceinline__ uint4 i8_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 // 16 bytes of a row from byte k on, 0 past its `n`: of any alignment, and nothing outside it read.
 __device__ __forceinline__ uint4 i8_bytes(const int8_t* row, int64_t k, int64_t n) {
@@ -97,11 +99,13 @@ __device__ __forceinline__ void i8_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// NT: tokens / 8.  Grid: the clusters' blocks side by side.  Shared memory: the tokens' bytes
-// of this block's k, then the sums of the tiles that it owns (every cluster-th of the cluster's).
+// NT: tokens / 8.  Grid: the clusters' blocks side by side.  Shared memory: the rings; their
+// barriers; the tokens' bytes of this block's k; the sums of the tiles that it owns (every
+// cluster-th of the cluster's).
 template <typename TC, int NT>
-__global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_constant__ I8Few q) {
-    extern __shared__ __align__(16) unsigned char i8_shared[];
+__global__ void __launch_bounds__(kI8FewThreads, 1)
+    tg_gemm_i8_few(const __grid_constant__ I8Few q, const __grid_constant__ CUtensorMap codes) {
+    extern __shared__ __align__(1024) unsigned char i8_dynamic[];
     const I8Params& p = q.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int tokens = static_cast<int>(p.M);
@@ -112,14 +116,23 @@ __global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_
     const int tiles = q.tiles / clusters + (cluster_no < q.tiles % clusters ? 1 : 0);
     const int c0 = static_cast<int>(int64_t{q.chunks} * rank / q.cluster);
     const int chunks = static_cast<int>(int64_t{q.chunks} * (rank + 1) / q.cluster) - c0;
-    int* sums = reinterpret_cast<int*>(i8_shared + tokens * q.x_pitch);
+    const uint32_t base = (op_smem(i8_dynamic) + 1023) & ~1023u;
+    unsigned char* const shared = i8_dynamic + (base - op_smem(i8_dynamic));
+    const uint32_t ring = base + warp * q.stages * kI8FewStep;
+    unsigned char* const behind = shared + kI8FewWarps * q.stages * kI8FewStep;  // the rings
+    const uint32_t bars = op_smem(behind) + warp * kI8FewStages * 8;
+    unsigned char* const x_all = behind + kI8FewBars;
+    int* const sums = reinterpret_cast<int*>(x_all + tokens * q.x_pitch);
     op_release_next();
+    if (lane == 0) {
+        for (int s = 0; s < q.stages; ++s) op_bar_init(bars + 8 * s, 1);
+        op_bar_init_done();
+    }
     for (int i = threadIdx.x; i < tokens * q.sums_pitch; i += kI8FewThreads) sums[i] = 0;
+    __syncwarp();
     op_wait_previous();
 
-    // a lane's bytes of a step: rows g and g + 8 of the tile (the last row again past the last)
     const int dt = kI8FewWarps / chunks, dc = kI8FewWarps % chunks;
-    const bool ragged = p.K % 16 != 0;  // the last row's last bytes are read one by one
     struct Place {
         int tile, chunk;
     };
@@ -128,35 +141,29 @@ __global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_
         at.chunk += dc;
         if (at.chunk >= chunks) at.chunk -= chunks, ++at.tile;
     };
-    auto load = [&](const Place& at, uint4 (&v)[2]) {
-        const int64_t k = int64_t{c0 + at.chunk} * 64 + 16 * t;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            int64_t n = int64_t{tile0 + at.tile} * 16 + g + 8 * h;
-            if (n >= p.N) n = p.N - 1;
-            if (at.tile >= tiles || k >= p.K)
-                v[h] = make_uint4(0, 0, 0, 0);
-            else if (ragged && n == p.N - 1 && k + 16 > p.K)
-                v[h] = i8_bytes(p.B + n * p.ldb, k, p.K);
-            else
-                v[h] = i8_stream(p.B + n * p.ldb + k);
-        }
-    };
     Place next{warp / chunks, warp % chunks}, here = next;
-    uint4 v[kI8Depth][2];
-#pragma unroll
-    for (int i = 0; i < kI8Depth; ++i) {
-        load(next, v[i]);
+    int fill = 0, issued = 0;  // the stage that is filled next
+    auto fetch = [&] {
+        if (next.tile >= tiles) return;
+        if (lane == 0 && !(q.inject == 1 && blockIdx.x == 0 && issued == 0)) {
+            const uint32_t bar = bars + 8 * fill;
+            op_bar_expect(bar, kI8FewStep);
+            op_tma_2d(ring + fill * kI8FewStep, &codes, bar, (c0 + next.chunk) * kI8FewK,
+                      (tile0 + next.tile) * kI8FewRows);
+        }
         advance(next);
-    }
+        ++issued;
+        fill = fill + 1 == q.stages ? 0 : fill + 1;
+    };
+    for (int s = 0; s < q.stages; ++s) fetch();
     {  // the tokens
         const bool wide = (reinterpret_cast<uintptr_t>(p.A) & 15) == 0 && p.lda % 16 == 0;
-        const int pieces = 4 * chunks;
+        const int pieces = kI8FewK / 16 * chunks;
         for (int i = threadIdx.x; i < tokens * pieces; i += kI8FewThreads) {
             const int m = i / pieces, piece = i - m * pieces;
-            const int64_t k = int64_t{c0} * 64 + 16 * piece;
+            const int64_t k = int64_t{c0} * kI8FewK + 16 * piece;
             const int8_t* a = p.A + m * p.lda;
-            *reinterpret_cast<uint4*>(i8_shared + m * q.x_pitch + 16 * piece) =
+            *reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 16 * piece) =
                 wide && k + 16 <= p.K ? *reinterpret_cast<const uint4*>(a + k) : i8_bytes(a, k, p.K);
         }
     }
@@ -165,6 +172,9 @@ __global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_
     else
         __syncthreads();
 
+    // A lane's MMA row g is row r of the tile (g + 8: r + 8): so the eight lanes that read at a
+    // time find their 16 bytes, swizzled by r, in all banks.
+    const int r = (g >> 1) + 4 * (g & 1);
     int c[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_
     const uint32_t sums_at = op_smem(sums);
     auto flush = [&](int tile) {  // c[.][0, 1]: row g, tokens 2t and 2t + 1; [2, 3]: row g + 8
         const int slot = q.cluster > 1 ? tile / q.cluster : tile;
-        uint32_t to = sums_at + 4 * (16 * slot + g);
+        uint32_t to = sums_at + 4 * (kI8FewRows * slot + r);
         if (q.cluster > 1)
             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(to), "r"(tile - slot * q.cluster));
 #pragma unroll
@@ -189,38 +199,57 @@ __global__ void __launch_bounds__(kI8FewThreads, 1) tg_gemm_i8_few(const __grid_
                 c[i][j] = 0;
             }
     };
-    const unsigned char* x = i8_shared + g * q.x_pitch + 16 * t;
+    const unsigned char* x = x_all + g * q.x_pitch + 16 * t;
+    int slot = 0, used = 0;
+    uint32_t parity = 0;
+    bool lost = false;
     while (here.tile < tiles) {
+        const bool ok = op_bar_wait(bars + 8 * slot, parity, q.limit_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+            lost = true;
+            break;
+        }
+        const uint32_t row = ring + slot * kI8FewStep + r * kI8FewK;
 #pragma unroll
-        for (int i = 0; i < kI8Depth; ++i) {
-            if (here.tile < tiles) {
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = row + (((4 * h + t) ^ r) << 4);
+            const uint4 v = tc_lds128(at), w = tc_lds128(at + 8 * kI8FewK);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint4 a = make_uint4(0, 0, 0, 0);
-                    if (8 * j + g < tokens)
-                        a = *reinterpret_cast<const uint4*>(x + 8 * j * q.x_pitch + 64 * here.chunk);
-                    i8_mma(c[j], v[i][0].x, v[i][1].x, v[i][0].y, v[i][1].y, a.x, a.y);
-                    i8_mma(c[j], v[i][0].z, v[i][1].z, v[i][0].w, v[i][1].w, a.z, a.w);
-                }
-                load(next, v[i]);
-                advance(next);
-                const int tile = here.tile;
-                advance(here);
-                if (here.tile != tile) flush(tile);
+            for (int j = 0; j < NT; ++j) {
+                uint4 a = make_uint4(0, 0, 0, 0);
+                if (8 * j + g < tokens)
+                    a = *reinterpret_cast<const uint4*>(x + 8 * j * q.x_pitch + kI8FewK * here.chunk + 64 * h);
+                i8_mma(c[j], v.x, w.x, v.y, w.y, a.x, a.y);
+                i8_mma(c[j], v.z, w.z, v.w, w.w, a.z, a.w);
             }
         }
+        ++used;
+        __syncwarp();  // all lanes have used the stage, which is filled again
+        fetch();
+        const int tile = here.tile;
+        advance(here);
+        if (here.tile != tile) flush(tile);
+        if (++slot == q.stages) slot = 0, parity ^= 1;
+    }
+    if (lost) {
+        // copies under way have to land before the block ends
+        bool ok = true;
+        for (int i = used; ok && lane == 0 && i < issued; ++i)
+            ok = op_bar_wait(bars + 8 * (i % q.stages), i / q.stages & 1, kTcLandNs);
+        __syncwarp();
+        if (lane == 0) atomicOr(q.timeouts, kOpTimeoutI8);
     }
     if (q.cluster > 1)
         i8_cluster_sync();  // and no block leaves before its sums have come
     else
         __syncthreads();
 
-    const int owned = q.cluster > 1 ? (tiles - rank + q.cluster - 1) / q.cluster : tiles;
-    for (int i = threadIdx.x; i < owned * 16 * tokens; i += kI8FewThreads) {
-        const int m = i / (owned * 16), r = i - m * owned * 16;
-        const int64_t n = int64_t{tile0 + r / 16 * q.cluster + rank} * 16 + r % 16;
+    const int rows = (q.cluster > 1 ? (tiles - rank + q.cluster - 1) / q.cluster : tiles) * kI8FewRows;
+    for (int i = threadIdx.x; i < rows * tokens; i += kI8FewThreads) {
+        const int m = i / rows, o = i - m * rows;
+        const int64_t n = int64_t{tile0 + o / kI8FewRows * q.cluster + rank} * kI8FewRows + o % kI8FewRows;
         if (n >= p.N) continue;
-        float y = i8_value(p, static_cast<float>(sums[m * q.sums_pitch + r]), p.sa[m], p.sb[n],
+        float y = i8_value(p, static_cast<float>(sums[m * q.sums_pitch + o]), p.sa[m], p.sb[n],
                            p.bias != nullptr ? p.bias[n] : 0.0f);
         if (p.resid != nullptr) y += op_to_float((static_cast<const TC*>(p.resid) + m * p.ldr)[n]);
         (static_cast<TC*>(p.C) + m * p.ldc)[n] = op_round<TC>(y);

@@ -94,11 +94,11 @@ bool launch_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_s
     tg::I8Few q, best;
     std::memset(&q, 0, sizeof(q));
     q.p = p;
-    const int64_t tiles = (p.N + 15) / 16;
+    const int64_t tiles = (p.N + tg::kI8FewRows - 1) / tg::kI8FewRows;
     q.tiles = static_cast<int32_t>(tiles);
-    q.chunks = static_cast<int32_t>((p.K + 63) / 64);
-    // The shape with the least time, in steps of a block's warps (16 KB of B, about 0.37 us):
-    // the steps of a block, the fetch of its part of A, and the joins of a cluster.
+    q.chunks = static_cast<int32_t>((p.K + tg::kI8FewK - 1) / tg::kI8FewK);
+    // The shape with the least time, in rounds of a block's warps (32 KB of B, about 0.73 us):
+    // the steps of a block, the fetch of its part of A, the joins of a cluster, a shallow ring.
     double least = 1e300;
     size_t smem = 0;
     int64_t grid = 0;
@@ -106,33 +106,45 @@ bool launch_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_s
         q.cluster = 1 << i;
         if (q.cluster > q.chunks || lim.clusters[i] < 1) break;
         const int64_t slice = (q.chunks + q.cluster - 1) / q.cluster;
-        q.x_pitch = static_cast<int32_t>((slice * 64 + 127) / 128 * 128 + 64);
+        q.x_pitch = static_cast<int32_t>(slice * tg::kI8FewK + 64);
         int64_t clusters = tiles < lim.clusters[i] ? tiles : lim.clusters[i];
-        // (a block keeps the sums of its tiles: very many rows of B take several waves)
-        const int64_t room = (kSmem - 512 - p.M * q.x_pitch) / (p.M * 64) * q.cluster;
-        if (room < 1) continue;
-        int64_t rounds = (tiles + clusters - 1) / clusters;
-        if (rounds > room) {
-            rounds = room;
-            clusters = (tiles + rounds - 1) / rounds;
-        }
-        q.rounds = static_cast<int32_t>(rounds);
-        const int64_t waves = (clusters + lim.clusters[i] - 1) / lim.clusters[i];
-        q.sums_pitch = static_cast<int32_t>((rounds + q.cluster - 1) / q.cluster * 16 + 4);
-        const int64_t bytes = p.M * (q.x_pitch + 4 * int64_t{q.sums_pitch});
-        if (bytes > kSmem) continue;
-        const double steps = static_cast<double>((rounds * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps);
-        const double time = static_cast<double>(waves) *
-                            (steps + 2e-5 * static_cast<double>(slice * 64 * p.M) + (q.cluster > 1 ? 3.0 : 0.0));
-        if (time < least) {
-            least = time;
-            best = q;
-            smem = static_cast<size_t>(bytes);
-            grid = clusters * q.cluster;
+        for (q.stages = tg::kI8FewStages; q.stages >= 2; --q.stages) {
+            const int64_t fixed = 1024 + int64_t{tg::kI8FewWarps} * q.stages * tg::kI8FewStep + tg::kI8FewBars +
+                                  p.M * q.x_pitch;
+            // (a block keeps the sums of its tiles: very many rows of B take several waves)
+            const int64_t room = (kSmem - fixed - p.M * 16) / (p.M * tg::kI8FewRows * 4) * q.cluster;
+            int64_t rounds = (tiles + clusters - 1) / clusters;
+            if (room < 1 || (room < rounds && q.stages > 4)) continue;
+            if (rounds > room) {
+                rounds = room;
+                clusters = (tiles + rounds - 1) / rounds;
+            }
+            q.sums_pitch = static_cast<int32_t>((rounds + q.cluster - 1) / q.cluster * tg::kI8FewRows + 4);
+            const int64_t waves = (clusters + lim.clusters[i] - 1) / lim.clusters[i];
+            const double steps = static_cast<double>((rounds * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps);
+            const double time =
+                static_cast<double>(waves) * (steps + 1e-5 * static_cast<double>(slice * tg::kI8FewK * p.M) +
+                                              (q.cluster > 1 ? 1.5 : 0.0) + (q.stages < 3 ? 2.0 : 0.0));
+            if (time < least) {
+                least = time;
+                best = q;
+                smem = static_cast<size_t>(fixed + 4 * p.M * q.sums_pitch);
+                grid = clusters * q.cluster;
+            }
+            break;
         }
     }
     if (least > 1e299 || grid > tg::kOpMaxDim) return false;
-    *st = launch(kernel, dim3(static_cast<unsigned>(grid)), tg::kI8FewThreads, smem, best.cluster, s, best);
+    CUtensorMap codes;
+    if (!tg::op_map_2d(&codes, p.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.ldb, tg::kI8FewK, tg::kI8FewRows,
+                       CU_TENSOR_MAP_SWIZZLE_128B)) {
+        *st = TG_ERR_LAUNCH;
+        return true;
+    }
+    best.limit_ns = tg::op_wait_limit_ns();
+    best.timeouts = dev.timeouts;
+    best.inject = tg::op_take_inject();
+    *st = launch(kernel, dim3(static_cast<unsigned>(grid)), tg::kI8FewThreads, smem, best.cluster, s, best, codes);
     return true;
 }
 
