@@ -52,7 +52,8 @@ constexpr int kI8FewThreads = 32 * kI8FewWarps;
 constexpr int kI8FewRows = 16;
 constexpr int kI8FewK = 128;
 constexpr int kI8FewStep = kI8FewRows * kI8FewK;
-constexpr int kI8FewStages = 6;  // at most
+constexpr int kI8FewStages = 3;  // at most
+constexpr int kI8FewAhead = 3;   // steps of a warp, to L2 before the kernel may read
 constexpr int kI8FewBars = kI8FewWarps * kI8FewStages * 8;
 
 struct I8Few {
@@ -95,6 +96,13 @@ __device__ __forceinline__ uint4 i8_bytes(const int8_t* row, int64_t k, int64_t 
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// A box of a 2-D tensor map to L2.
+__device__ __forceinline__ void i8_prefetch(const void* map, uint32_t x, uint32_t y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void i8_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -130,7 +138,6 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
     }
     for (int i = threadIdx.x; i < tokens * q.sums_pitch; i += kI8FewThreads) sums[i] = 0;
     __syncwarp();
-    op_wait_previous();
 
     const int dt = kI8FewWarps / chunks, dc = kI8FewWarps % chunks;
     struct Place {
@@ -155,17 +162,31 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
         ++issued;
         fill = fill + 1 == q.stages ? 0 : fill + 1;
     };
+    if (lane == 0) {
+        // While the kernel before this one ends, the first steps come as far as L2 (no value is
+        // taken yet: that kernel may still write them).
+        Place soon = next;
+        for (int s = 0; s < kI8FewAhead && soon.tile < tiles; ++s, advance(soon))
+            i8_prefetch(&codes, (c0 + soon.chunk) * kI8FewK, (tile0 + soon.tile) * kI8FewRows);
+    }
+    op_wait_previous();
     for (int s = 0; s < q.stages; ++s) fetch();
     {  // the tokens
         const bool wide = (reinterpret_cast<uintptr_t>(p.A) & 15) == 0 && p.lda % 16 == 0;
         const int pieces = kI8FewK / 16 * chunks;
-        for (int i = threadIdx.x; i < tokens * pieces; i += kI8FewThreads) {
-            const int m = i / pieces, piece = i - m * pieces;
-            const int64_t k = int64_t{c0} * kI8FewK + 16 * piece;
+        for (int m = 0; m < tokens; ++m) {
             const int8_t* a = p.A + m * p.lda;
-            *reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 16 * piece) =
-                wide && k + 16 <= p.K ? *reinterpret_cast<const uint4*>(a + k) : i8_bytes(a, k, p.K);
+            for (int i = threadIdx.x; i < pieces; i += kI8FewThreads) {
+                const int64_t k = int64_t{c0} * kI8FewK + 16 * i;
+                unsigned char* to = x_all + m * q.x_pitch + 16 * i;
+                if (wide && k + 16 <= p.K)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
+                                 : "memory");
+                else
+                    *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (q.cluster > 1)
         i8_cluster_sync();  // (the owners' sums are zero, too)

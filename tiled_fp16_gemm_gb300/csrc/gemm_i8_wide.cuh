@@ -19,7 +19,10 @@
 
 namespace tg {
 
-constexpr int kI8Stages = 6;  // of B
+// Of B.  A decoding group meets every phase of a stage, or none: its parity says nothing of a
+// phase that the group has not waited for the one before of.
+constexpr int kI8Stages = 6;
+static_assert(kI8Stages % kTcGroups == 0, "unit i + kI8Stages is the same group's as unit i");
 constexpr int kI8XStages = 4;
 constexpr int kI8Tokens = 256;  // of a tile at most
 constexpr int kI8CodeBytes = kTcRows * kTcK;
@@ -159,6 +162,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         static_cast<int>(tc_first(grains, q.clusters, cluster_no + 1) * q.grain - u0);
     int64_t tile = u0 / q.k_units;
     int kb = static_cast<int>(u0 - tile * q.k_units);
+    // the tile's place among the row blocks and the blocks of tokens, carried along: a 64-bit
+    // division per unit costs the warps that fetch as much time as the unit's copies take
+    int row_tile = static_cast<int>(tile / q.m_tiles);
+    int m_tile = static_cast<int>(tile - int64_t{row_tile} * q.m_tiles);
     // A warp waits; false once a wait has run out, here or in another warp.
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (__all_sync(0xffffffffu, op_bar_try(bar, parity))) return true;
@@ -168,11 +175,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         __syncwarp();
         return false;
     };
-    auto next_unit = [&] {
-        if (++kb == q.k_units) kb = 0, ++tile;
+    auto next_tile = [&] {
+        kb = 0;
+        ++tile;
+        if (++m_tile == q.m_tiles) m_tile = 0, ++row_tile;
     };
-    auto first_row = [&] { return (tile / q.m_tiles * kWideCluster + rank) * kTcRows; };
-    auto first_token = [&] { return tile % q.m_tiles * q.tokens; };
+    auto next_unit = [&] {
+        if (++kb == q.k_units) next_tile();
+    };
+    auto first_row = [&] { return (int64_t{row_tile} * kWideCluster + rank) * kTcRows; };
+    auto first_token = [&] { return int64_t{m_tile} * q.tokens; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ B
@@ -355,8 +367,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
             }
             i += len;
-            kb = 0;
-            ++tile;
+            next_tile();
         }
     }
     tc_before_sync();

@@ -114,7 +114,7 @@ bool launch_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_s
             // (a block keeps the sums of its tiles: very many rows of B take several waves)
             const int64_t room = (kSmem - fixed - p.M * 16) / (p.M * tg::kI8FewRows * 4) * q.cluster;
             int64_t rounds = (tiles + clusters - 1) / clusters;
-            if (room < 1 || (room < rounds && q.stages > 4)) continue;
+            if (room < 1 || (room < rounds && q.stages > 2)) continue;
             if (rounds > room) {
                 rounds = room;
                 clusters = (tiles + rounds - 1) / rounds;
@@ -159,6 +159,8 @@ int64_t slab_rows(int64_t M, int64_t K) {
     return M < rows ? M : rows;
 }
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+// Of a tile, at most: what the shares' places are made for.
+int64_t tile_tokens(int64_t M) { return M < tg::kI8Tokens ? up(M, 32) : tg::kI8Tokens; }
 
 // Fills in the tile's width and the division of the work with the least time, as plan_wide
 // of w4.cu does.
@@ -167,7 +169,8 @@ void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
     constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
     const int64_t row_tiles = (p.N + rows - 1) / rows;
     double least = 1e300;
-    for (int32_t tokens = 32; tokens <= tg::kI8Tokens; tokens += 32) {
+    const int32_t widest = static_cast<int32_t>(tile_tokens(p.M));
+    for (int32_t tokens = 32; tokens <= widest; tokens += 32) {
         const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
         const double mma = 0.0024 * tokens;
         const double unit = mma < 0.43 ? 0.43 : mma;
@@ -192,11 +195,10 @@ void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
 
 // Counters, the blocks' shares of sums (two each), A as fp16: for any plan of these sizes.
 int64_t slot_bytes(int64_t M) {
-    const int64_t tokens = M < tg::kI8Tokens ? up(M, 32) : tg::kI8Tokens;
-    return 2 * int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tokens * tg::kTcRows * 4;
+    return 2 * int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4;
 }
 int64_t workspace_bytes(int64_t M, int64_t, int64_t K) {
-    if (M <= kFewRows || K == 0) return 0;
+    if (M <= 8 || K == 0) return 0;
     return tg::kI8CounterBytes + slot_bytes(M) + slab_rows(M, K) * up(K, tg::kTcK) * 2;
 }
 
@@ -254,8 +256,9 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
 template <typename TC>
 tg_status_t launch_type(const I8Params& p, const tg::OpDevice& dev, void* ws, cudaStream_t s) {
     tg_status_t st;
-    if (p.K > 0 && p.M <= kFewRows && launch_few<TC, 1>(p, dev, s, &st)) return st;
-    if (p.K > 0 && p.M > kFewRows) return launch_wide<TC>(p, dev, ws, s);
+    if (p.K > 0 && p.M <= 8 && launch_few<TC, 1>(p, dev, s, &st)) return st;
+    if (p.K > 0 && p.M > 8 && p.M <= kFewRows && launch_few<TC, 2>(p, dev, s, &st)) return st;
+    if (p.K > 0 && p.M > 8) return launch_wide<TC>(p, dev, ws, s);
     const int64_t blocks = (p.M * p.N + 7) / 8, most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_gemm_i8_simple<TC>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, 1, s,
                   p);
