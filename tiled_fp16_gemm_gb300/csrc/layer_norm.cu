@@ -2,34 +2,30 @@
 // (include/tgemm.h): argument checks, workspace and launches.  The kernels and the formulas:
 // layer_norm.cuh.
 #include <cstring>
-#include <set>
 #include <type_traits>
 
 #include "layer_norm.cuh"
-#include "op_host.h"
+#include "norm_host.h"
 
 namespace {
 
+using tg::allow_smem;
+using tg::check_matrix;
+using tg::elem_bytes;
+using tg::launch;
 using tg::LayerNormGradParams;
 using tg::LayerNormParams;
+using tg::max_clusters;
+using tg::misaligned;
+using tg::narrow;
+using tg::plan_rows;
+using tg::RowPlan;
+using tg::wide;
 
 constexpr int64_t kMaxCols = 131071;   // codes of a row: whole sums of gemm_i8 fit 32 bits
 constexpr int64_t kGradBlocks = 320;   // that share the column sums, at most
 
 tg::OpWorkspace g_workspace;  // column sums of the gradient, where the caller has none
-
-int elem_bytes(int32_t dtype) { return dtype == TG_DTYPE_F32 ? 4 : 2; }
-
-bool misaligned(const void* p, int bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) != 0;
-}
-
-// One matrix argument: present or not, its stride, its alignment.
-tg_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int bytes) {
-    if (p == nullptr) return TG_OK;
-    if (ld < cols) return TG_ERR_INVALID_VALUE;
-    return misaligned(p, bytes) ? TG_ERR_MISALIGNED : TG_OK;
-}
 
 // The arguments that all calls share.
 tg_status_t check_norm(const tg_layer_norm_t* a, LayerNormParams* p) {
@@ -67,33 +63,11 @@ tg_status_t with_types(int32_t dtype, int32_t stream_dtype, F f) {
     return wide ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-// One launch with dependent launch allowed.
-template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                   Given... given) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
-    return TG_OK;
-}
-
 template <typename TX, typename TR, int MODE>
 tg_status_t launch_rows(const LayerNormParams& p, const tg::OpDevice& dev, cudaStream_t s) {
     const int64_t most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_layer_norm_simple<TX, TR, MODE>,
-                  dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)), 256, 0, s, p);
+                  dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)), 256, 0, 1, s, p);
 }
 
 // y, and h or the codes of a norm.
@@ -212,9 +186,9 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             if (q.dw != nullptr) q.ws_w = next, next += blocks * cols;
             if (q.db != nullptr) q.ws_b = next;
         }
-        st = launch(tg::tg_layer_norm_grad_simple<TX, TR>, dim3(static_cast<unsigned>(blocks)), 256, 0, s, q);
+        st = launch(tg::tg_layer_norm_grad_simple<TX, TR>, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, s, q);
         if (st != TG_OK || (q.dw == nullptr && q.db == nullptr)) return st;
-        return launch(tg::tg_layer_norm_grad_sum, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, s, q,
+        return launch(tg::tg_layer_norm_grad_sum, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, 1, s, q,
                       blocks);
     });
 }

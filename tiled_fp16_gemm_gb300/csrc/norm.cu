@@ -1,16 +1,24 @@
 // tg_norm_residual and tg_norm_residual_backward (include/tgemm.h): argument
 // checks, workspace and launches.  The kernels and the formulas: norm.cuh.
 #include <cstring>
-#include <set>
 #include <type_traits>
 
-#include "norm.cuh"
-#include "op_host.h"
+#include "norm_host.h"
 
 namespace {
 
+using tg::allow_smem;
+using tg::check_matrix;
+using tg::elem_bytes;
+using tg::launch;
+using tg::max_clusters;
+using tg::misaligned;
+using tg::narrow;
 using tg::NormGradParams;
 using tg::NormParams;
+using tg::plan_rows;
+using tg::RowPlan;
+using tg::wide;
 
 template <int N>
 using Int = std::integral_constant<int, N>;
@@ -18,19 +26,6 @@ using Int = std::integral_constant<int, N>;
 constexpr int64_t kMaxCols = 32768;  // a row's fp32 values have to fit in shared memory
 
 tg::OpWorkspace g_workspace;  // column sums of the gradient
-
-int elem_bytes(int32_t dtype) { return dtype == TG_DTYPE_F32 ? 4 : 2; }
-
-bool misaligned(const void* p, int bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) != 0;
-}
-
-// One matrix argument: present or not, its stride, its alignment.
-tg_status_t check_matrix(const void* p, int64_t ld, int64_t cols, int32_t dtype) {
-    if (p == nullptr) return TG_OK;
-    if (ld < cols) return TG_ERR_INVALID_VALUE;
-    return misaligned(p, elem_bytes(dtype)) ? TG_ERR_MISALIGNED : TG_OK;
-}
 
 // The arguments that the forward and the backward call share.
 tg_status_t check_norm(const tg_norm_t* a, NormParams* p) {
@@ -46,9 +41,9 @@ tg_status_t check_norm(const tg_norm_t* a, NormParams* p) {
         return TG_ERR_INVALID_VALUE;
     if (a->rows > 0 && a->cols > 0 && a->x == nullptr) return TG_ERR_INVALID_VALUE;
     tg_status_t st;
-    if ((st = check_matrix(a->x, a->ldx, a->cols, a->dtype)) != TG_OK) return st;
-    if ((st = check_matrix(a->residual, a->ldr, a->cols, a->stream_dtype)) != TG_OK) return st;
-    if ((st = check_matrix(a->gate, a->ldg, a->cols, a->dtype)) != TG_OK) return st;
+    if ((st = check_matrix(a->x, a->ldx, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
+    if ((st = check_matrix(a->residual, a->ldr, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if ((st = check_matrix(a->gate, a->ldg, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
     if (misaligned(a->post_weight, 4) || misaligned(a->pre_weight, 4)) return TG_ERR_MISALIGNED;
     std::memset(p, 0, sizeof(*p));
     p->rows = a->rows;
@@ -76,118 +71,6 @@ tg_status_t with_types(const tg_norm_t& a, F f) {
     return wide ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
-// The row kernels count strides in 32 bits.
-bool narrow(int64_t a, int64_t b, int64_t c, int64_t d, int64_t e) {
-    return (a | b | c | d | e) < (int64_t{1} << 32);
-}
-
-// Whether every row of a matrix (or of none) lies on 8 elements: 16 or 32 bytes.
-bool wide(const void* p, int64_t ld, int bytes) {
-    return p == nullptr || (!misaligned(p, 8 * bytes) && ld % 8 == 0);
-}
-
-// One launch with dependent launch allowed, in clusters of `cluster` blocks.
-template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
-                   cudaStream_t s, Given... given) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
-    return TG_OK;
-}
-
-// Of an SM's 228 KB of shared memory, for rings (a block has 5 KB and a reserved one besides).
-constexpr int kRingBytes = 214 * 1024;
-
-// How a kernel takes rows through rings.
-struct RowPlan {
-    int threads;  // of a group
-    int groups;   // of a block
-    int stages, stage_bytes;
-    int per_sm;   // blocks
-    size_t smem;
-};
-
-// `stage`: bytes of a group's stage; `more`: of a group besides its ring; `per_sm`: the blocks that registers allow on an SM.  False if no ring fits.
-bool plan_rows(int64_t rows, int threads, int stage, int more, int per_sm, int num_sms, RowPlan* r) {
-    if (rows > tg::kOpMaxDim - 65536) return false;  // they count rows ahead in 31 bits
-    r->threads = threads;
-    r->groups = tg::kNormThreads / threads;
-    // few rows: blocks on every SM before groups in a block
-    const int64_t each = (rows + num_sms - 1) / num_sms;
-    if (r->groups > each) r->groups = static_cast<int>(each);
-    r->stage_bytes = stage;
-    for (r->per_sm = per_sm; r->per_sm >= 1; --r->per_sm)
-        for (r->stages = 4; r->stages >= (r->per_sm > 1 ? 3 : 2); --r->stages) {
-            r->smem = static_cast<size_t>(r->groups) * (r->stages * stage + more);
-            if (r->per_sm * (r->smem + 6 * 1024) <= kRingBytes + 6 * 1024) return true;
-        }
-    return false;
-}
-
-// Lets a kernel use the shared memory that a block may have, once per device.
-template <typename Kernel>
-bool allow_smem(Kernel k, int dev) {
-    static std::mutex m;
-    static std::set<std::pair<const void*, int>> done;
-    const auto key = std::make_pair(reinterpret_cast<const void*>(k), dev);
-    std::lock_guard<std::mutex> lk(m);
-    if (done.count(key) != 0) return true;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) !=
-        cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    done.insert(key);
-    return true;
-}
-
-// Clusters of `size` blocks that the device holds at once (asked once for each shape).
-template <typename Kernel>
-int64_t max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
-    static std::mutex m;
-    static std::map<std::tuple<const void*, int, int, size_t, int>, int> known;
-    const auto key = std::make_tuple(reinterpret_cast<const void*>(kernel), size, threads, smem, dev.dev);
-    std::lock_guard<std::mutex> lk(m);
-    const auto it = known.find(key);
-    if (it != known.end()) return it->second;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(size);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-    }
-    known[key] = n;
-    return n;
-}
-
 }  // namespace
 
 static tg_status_t norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void* h, int64_t ldh,
@@ -197,8 +80,8 @@ static tg_status_t norm_residual(const tg_norm_t* a, void* y, int64_t ldy, void*
     if (st != TG_OK) return st;
     if ((h != nullptr) != (a->pre_weight != nullptr) && a->rows > 0 && a->cols > 0)
         return TG_ERR_INVALID_VALUE;
-    if ((st = check_matrix(y, ldy, a->cols, a->stream_dtype)) != TG_OK) return st;
-    if ((st = check_matrix(h, ldh, a->cols, a->dtype)) != TG_OK) return st;
+    if ((st = check_matrix(y, ldy, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if ((st = check_matrix(h, ldh, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
     if (a->rows == 0 || a->cols == 0 || (y == nullptr && h == nullptr)) return TG_OK;
     p.y = y;
     p.ldy = ldy;
@@ -263,11 +146,11 @@ static tg_status_t norm_residual_backward(const tg_norm_t* a, const tg_norm_grad
         (b->dpost_weight != nullptr && a->post_weight == nullptr) ||
         (b->dpre_weight != nullptr && a->pre_weight == nullptr))
         return TG_ERR_INVALID_VALUE;
-    if ((st = check_matrix(b->dy, b->lddy, a->cols, a->stream_dtype)) != TG_OK) return st;
-    if ((st = check_matrix(b->dh, b->lddh, a->cols, a->dtype)) != TG_OK) return st;
-    if ((st = check_matrix(b->dx, b->lddx, a->cols, a->dtype)) != TG_OK) return st;
-    if ((st = check_matrix(b->dresidual, b->lddr, a->cols, a->stream_dtype)) != TG_OK) return st;
-    if ((st = check_matrix(b->dgate, b->lddg, a->cols, a->dtype)) != TG_OK) return st;
+    if ((st = check_matrix(b->dy, b->lddy, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if ((st = check_matrix(b->dh, b->lddh, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
+    if ((st = check_matrix(b->dx, b->lddx, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
+    if ((st = check_matrix(b->dresidual, b->lddr, a->cols, elem_bytes(a->stream_dtype))) != TG_OK) return st;
+    if ((st = check_matrix(b->dgate, b->lddg, a->cols, elem_bytes(a->dtype))) != TG_OK) return st;
     if (misaligned(b->dpost_weight, 4) || misaligned(b->dpre_weight, 4)) return TG_ERR_MISALIGNED;
     if (a->cols == 0) return TG_OK;
     tg::OpDevice dev;

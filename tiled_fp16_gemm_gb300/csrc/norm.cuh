@@ -602,9 +602,10 @@ struct NormPeers<true> {
     __device__ __forceinline__ static void sync() {
         asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     }
-    // The blocks' v (the same in all threads of a block), in the order of the blocks.
+    // The blocks' v (the same in all threads of a block): 8 places for each, until the next but
+    // one exchange.
     template <int N>
-    __device__ __forceinline__ void add(float (&v)[N]) {
+    __device__ __forceinline__ const float* exchange(const float (&v)[N]) {
         float* all = values + turn * kNormSplit * 8;
         const uint32_t bar = bars + 8 * turn;
         if (threadIdx.x == 0 && !lost) op_bar_expect(bar, count * N * 4);
@@ -626,13 +627,19 @@ struct NormPeers<true> {
             lost = true;
             atomicOr(timeouts, kOpTimeoutNorm);
         }
+        turn ^= 1;
+        if (turn == 0) parity ^= 1;
+        return all;
+    }
+    // Their sums, in the order of the blocks.
+    template <int N>
+    __device__ __forceinline__ void add(float (&v)[N]) {
+        const float* all = exchange(v);
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = all[k];
         for (int b = 1; b < count; ++b)
 #pragma unroll
             for (int k = 0; k < N; ++k) v[k] += all[b * 8 + k];
-        turn ^= 1;
-        if (turn == 0) parity ^= 1;
     }
     // No block leaves while another's values may be on their way to it.
     __device__ __forceinline__ void end() { sync(); }
