@@ -179,7 +179,9 @@ def test_nothing_past_the_rows_is_written(tg):
         whole = [torch.full((9, cols + 5), 7.0, dtype=k, device="cuda") for k in (F32, HALF)]
         y, h = (w[1:8, 2:2 + cols] for w in whole)
         tg.layer_norm(x, **kept, out=y, normed=h)
-        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+        assert torch.equal(y, want[0])  # one addition
+        # (h's sums may be taken in another order where rows lie otherwise: the bound of each)
+        ref.LayerNorm(x, **kept).check(y, h, f"{cols}")
         for w in whole:
             assert bool((w[0] == 7).all() and (w[8] == 7).all() and (w[:, :2] == 7).all())
             assert bool((w[:, 2 + cols:] == 7).all())

@@ -63,8 +63,45 @@ tg_status_t with_types(int32_t dtype, int32_t stream_dtype, F f) {
     return wide ? f(__nv_bfloat16{}, float{}) : f(__nv_bfloat16{}, __nv_bfloat16{});
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Rows in registers where they fit: of the widths of a thread's share (8·CH columns) the largest
+// that leaves no SM without warps.
 template <typename TX, typename TR, int MODE>
 tg_status_t launch_rows(const LayerNormParams& p, const tg::OpDevice& dev, cudaStream_t s) {
+    // whether a thread may read and write 8 neighbouring columns at a time
+    const int out = MODE == tg::kLnH ? sizeof(TX) : 1;
+    const bool vec = p.cols % 8 == 0 && wide(p.x, p.ldx, sizeof(TX)) && wide(p.r, p.ldr, sizeof(TR)) &&
+                     wide(p.w, 0, 4) && wide(p.b, 0, 4) && wide(p.y, p.ldy, sizeof(TR)) && wide(p.h, p.ldh, out);
+    const int64_t cols = p.cols;
+    auto warps = [&](int ch) { return (cols + 256 * ch - 1) / (256 * ch); };  // of a row
+    auto run = [&](auto ch, auto v, auto far) {
+        constexpr int CH = decltype(ch)::value;
+        const int threads = static_cast<int>(warps(CH)) * 32;
+        const int64_t each = (p.rows + dev.num_sms - 1) / dev.num_sms;
+        const int64_t groups = threads > 32 ? 1 : each < 4 ? each : 4;  // rows of a block
+        const int64_t blocks = (p.rows + groups - 1) / groups;
+        return launch(tg::tg_layer_norm_rows<TX, TR, CH, decltype(v)::value, MODE, decltype(far)::value>,
+                      dim3(static_cast<unsigned>(blocks)), static_cast<int>(threads * groups), 0, 1, s, p, threads);
+    };
+    auto fits = [&](int ch) { return warps(ch) <= (vec && ch == 4 ? 12 : 16); };
+    int ch = !vec || fits(4) ? 4 : 8;
+    while (ch > 1 && (cols <= 128 * ch || (p.rows * warps(ch) < 8 * dev.num_sms && fits(ch / 2)))) ch /= 2;
+    std::false_type no;
+    if (vec && fits(ch)) {
+        std::true_type v;
+        if (ch == 1) return run(Int<1>{}, v, no);
+        if (ch == 2) return run(Int<2>{}, v, no);
+        if (ch == 4) return run(Int<4>{}, v, no);
+        return run(Int<8>{}, v, no);
+    }
+    if (!vec && warps(4) <= 32) {
+        if (warps(ch) > 16) return run(Int<4>{}, no, std::true_type{});
+        if (ch == 1) return run(Int<1>{}, no, no);
+        if (ch == 2) return run(Int<2>{}, no, no);
+        return run(Int<4>{}, no, no);
+    }
     const int64_t most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_layer_norm_simple<TX, TR, MODE>,
                   dim3(static_cast<unsigned>(p.rows < most ? p.rows : most)), 256, 0, 1, s, p);

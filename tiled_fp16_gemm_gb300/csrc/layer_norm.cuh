@@ -15,6 +15,8 @@
 // from the unrounded v.
 #pragma once
 
+#include <type_traits>
+
 #include "norm.cuh"
 
 namespace tg {
@@ -58,6 +60,12 @@ enum : int { kLnH = 0, kLnCodes = 1, kLnRaw = 2 };
 
 // ------------------------------------------------------------------ codes
 
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 constexpr uint32_t kLnInf = 0x7f800000u;
 
 // The scale of a row whose largest |value| has these bits.  With a NaN or an infinity among
@@ -65,29 +73,64 @@ constexpr uint32_t kLnInf = 0x7f800000u;
 __device__ __forceinline__ float ln_scale(uint32_t largest) {
     return largest >= kLnInf ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(largest), 127.0f);
 }
-// For ln_code: what value and scale are multiplied by (a power of two; 1 but for scales whose
-// reciprocal would leave fp32), and the reciprocal.  A row of zeros (or of values so small that
-// their scale is 0), and one without a scale, has codes 0.
+// Codes of a row with this scale: value / scale to the nearest, exactly.  The product with the
+// reciprocal is off by 2^-22 of it at most, so it rounds to the right whole number or, near a
+// half, to one beside it; what is left over, value - q · scale, is exact in fp32 and tells
+// which.  Numbers are rounded by adding 1.5·2^23 (the conversions run at an eighth of the rate),
+// which leaves the code in the low byte.
 struct LnCoder {
-    float up, scale, inv;
+    float scale, inv, half;
+    bool plain;  // a scale whose reciprocal is an fp32 number, and codes within ±127 by themselves
+    static constexpr float kRound = 12582912.0f;
     __device__ __forceinline__ explicit LnCoder(float s) {
-        up = s < 1e-30f ? 1.2676506e30f : 1.0f;  // 2^100
-        scale = s * up;
-        inv = s > 0.0f ? __frcp_rn(scale) : 0.0f;
+        scale = s;
+        half = 0.5f * s;
+        plain = s >= 1e-30f;
+        inv = __frcp_rn(s);
     }
-    // value / scale to the nearest, exactly: the product with the reciprocal is off by 2^-22 of
-    // it at most, so it rounds to the right whole number or, near a half, to one beside it; what
-    // is left over, value - q · scale, is exact in fp32 and tells which.
-    __device__ __forceinline__ int code(float value) const {
-        if (!(inv > 0.0f)) return 0;
-        value *= up;
-        float q = rintf(value * inv);
-        const float rest = fmaf(-q, scale, value), twice = 2.0f * fabsf(rest);
-        const bool odd = (__float2int_rn(q) & 1) != 0;
-        if (twice > scale || (twice == scale && odd)) q += rest > 0.0f ? 1.0f : -1.0f;
-        return __float2int_rn(fminf(fmaxf(q, -127.0f), 127.0f));  // (the least scales are coarse)
+    // Any row: zeros (or values so small that their scale is 0) and one without a scale have
+    // codes 0; small scales are taken 2^100 times, and the least are so coarse that ±127 is passed.
+    __device__ __noinline__ static uint32_t any(float value, float scale) {
+        if (!(scale > 0.0f)) return 0;
+        if (scale < 1e-30f) value *= 1.2676506e30f, scale *= 1.2676506e30f;
+        float t = fmaf(value, __frcp_rn(scale), kRound);
+        const float rest = fmaf(kRound - t, scale, value), twice = 2.0f * fabsf(rest);
+        if (twice > scale || (twice == scale && (__float_as_uint(t) & 1) != 0)) t += rest > 0.0f ? 1.0f : -1.0f;
+        return __float_as_uint(fminf(fmaxf(t, kRound - 127.0f), kRound + 127.0f));
+    }
+    // Eight at once; each code in the low byte.
+    __device__ __forceinline__ void codes(const F2 (&v)[4], uint32_t (&code)[8]) const {
+        bool again = !plain;
+        if (plain) {
+            const F2 inv2 = f2(inv, inv), round2 = f2(kRound, kRound), less2 = f2(-scale, -scale);
+            const F2 back2 = f2(-kRound, -kRound);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const F2 t = f2_fma(v[i], inv2, round2);
+                const float2 rest = f2_get(f2_fma(f2_add(t, back2), less2, v[i]));
+                again = again || fabsf(rest.x) >= half || fabsf(rest.y) >= half;
+                const float2 w = f2_get(t);
+                code[2 * i] = __float_as_uint(w.x);
+                code[2 * i + 1] = __float_as_uint(w.y);
+            }
+        }
+        if (again) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 w = f2_get(v[i]);
+                code[2 * i] = any(w.x, scale);
+                code[2 * i + 1] = any(w.y, scale);
+            }
+        }
     }
 };
+
+// The larger of three sizes; NaN where one is.
+__device__ __forceinline__ float ln_most(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Largest of the block's values, for every thread.  `red`: 33 words.
 __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
@@ -103,6 +146,272 @@ __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
     v = red[32];
     __syncthreads();
     return v;
+}
+
+// ------------------------------------------------------------------ rows in registers
+//
+// A row's values stay in the registers of the threads that share it, 8·CH columns each
+// (LnCols): one warp, or for longer rows (and few of them) a block.
+//
+// One barrier for the statistics, whatever the values: a warp takes the mean m_u of its own
+// columns first, and its sums of d = v - m_u and of d².  From the warps' (m_u, Σd, Σd²) and counts
+// n_u follow, with nothing but differences of means added up,
+//   mu - m_0 = Σ_u (n_u (m_u - m_0) + Σd) / cols
+//   Σ (v - mu)² = Σ_u (Σd² + 2 g_u Σd + n_u g_u²),   g_u = m_u - mu
+// so neither a mean far from zero nor warps with different means cost digits.
+
+__device__ __forceinline__ float ln_warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Two 16-bit values of a word.
+template <typename T>
+__device__ __forceinline__ F2 ln_pair(uint32_t u) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        return f2(v.x, v.y);
+    }
+}
+// 8 values of a row that are read once.
+template <typename T>
+__device__ __forceinline__ void ln_take(const T* src, F2 (&v)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        float a, b, d, e, f, g, h, i;
+        asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(a), "=f"(b), "=f"(d), "=f"(e), "=f"(f), "=f"(g), "=f"(h), "=f"(i)
+                     : "l"(src));
+        v[0] = f2(a, b), v[1] = f2(d, e), v[2] = f2(f, g), v[3] = f2(h, i);
+    } else {
+        uint4 u;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(src));
+        v[0] = ln_pair<T>(u.x), v[1] = ln_pair<T>(u.y), v[2] = ln_pair<T>(u.z), v[3] = ln_pair<T>(u.w);
+    }
+}
+// 8·CH·32 consecutive columns of a row for each of its warps, so that a thread's lie at fixed
+// distances.  VEC: a thread has CH runs of 8 neighbours (every row on 8 elements, cols a multiple
+// of 8); else every 32nd column.
+template <int CH, bool VEC>
+struct LnCols {
+    int first, cols;  // this thread's first column
+    __device__ __forceinline__ LnCols(int cols, int warp, int lane)
+        : first(warp * 256 * CH + (VEC ? 8 : 1) * lane), cols(cols) {}
+    __device__ __forceinline__ static constexpr int at(int ch, int i) { return VEC ? 256 * ch + i : 32 * (8 * ch + i); }
+    __device__ __forceinline__ bool has(int ch, int i) const { return first < cols - at(ch, VEC ? 0 : i); }
+    // `row` is at this thread's first column, here and below
+    template <typename T>
+    __device__ __forceinline__ void load(const T* row, int ch, F2 (&v)[4]) const {
+        if constexpr (VEC) {
+            if (has(ch, 0)) {
+                ln_take<T>(row + at(ch, 0), v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = f2(has(ch, 2 * i) ? op_to_float(row[at(ch, 2 * i)]) : 0.0f,
+                          has(ch, 2 * i + 1) ? op_to_float(row[at(ch, 2 * i + 1)]) : 0.0f);
+        }
+    }
+    // of a weight, which other rows read too; `none` where there is no weight
+    __device__ __forceinline__ void weight(const float* row, int ch, F2 (&v)[4], float none) const {
+        if (row == nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = f2(none, none);
+        } else if constexpr (VEC) {
+            if (has(ch, 0)) norm_take<float>(row + at(ch, 0), v);
+        } else {
+            load(row, ch, v);
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, int ch, const F2 (&v)[4]) const {
+        if constexpr (VEC) {
+            if (!has(ch, 0)) return;
+            T* p = row + at(ch, 0);
+            if constexpr (sizeof(T) == 4) {
+                const float2 a = f2_get(v[0]), b = f2_get(v[1]), d = f2_get(v[2]), e = f2_get(v[3]);
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a.x),
+                             "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y), "f"(e.x), "f"(e.y)
+                             : "memory");
+            } else {
+                *reinterpret_cast<uint4*>(p) =
+                    make_uint4(f2_pack<T>(v[0]), f2_pack<T>(v[1]), f2_pack<T>(v[2]), f2_pack<T>(v[3]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = f2_get(v[i]);
+                if (has(ch, 2 * i)) row[at(ch, 2 * i)] = op_round<T>(f.x);
+                if (has(ch, 2 * i + 1)) row[at(ch, 2 * i + 1)] = op_round<T>(f.y);
+            }
+        }
+    }
+    // v - m, and 0 where there is no column
+    __device__ __forceinline__ void less(int ch, float m, F2 (&v)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = f2_add(v[i], f2(has(ch, 2 * i) ? -m : 0.0f, has(ch, 2 * i + 1) ? -m : 0.0f));
+    }
+};
+
+// Threads of a block at most, and how many such blocks an SM holds: what registers allow.
+// (Unaligned rows of more than 16384 columns: 1024 threads, whose registers do not hold all.)
+template <int CH, bool VEC, bool LONG>
+struct LnShape {
+    static constexpr int kThreads = LONG ? 1024 : VEC && CH == 4 ? 640 : 512;
+    static constexpr int kBlocks = CH < 4 ? 2 : 1;
+};
+
+// `threads`: of a row, 32 (a block has several rows) or all of the block.
+template <typename TX, typename TR, int CH, bool VEC, int MODE, bool LONG>
+__global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<CH, VEC, LONG>::kBlocks))
+    tg_layer_norm_rows(const LayerNormParams p, int threads) {
+    __shared__ float stat[2][3][32];  // of the warps: mean, Σd, Σd²; a row's are read while the next one's come
+    __shared__ uint32_t most[2][32];
+    const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols);
+    const bool alone = threads == 32;
+    const int warp = alone ? 0 : threadIdx.x >> 5, warps = threads >> 5;
+    const int group = alone ? threadIdx.x >> 5 : 0, groups = alone ? blockDim.x >> 5 : 1;
+    const LnCols<CH, VEC> c(cols, warp, lane);
+    const float inv = 1.0f / static_cast<float>(cols);
+    // lane u: columns of warp u
+    const float count = lane < warps ? static_cast<float>(min(cols - 256 * CH * lane, 256 * CH)) : 0.0f;
+    const float mine = __shfl_sync(0xffffffffu, count, warp);
+    const float mine_inv = mine > 0.0f ? 1.0f / mine : 0.0f;
+    op_release_next();
+    op_wait_previous();
+    int turn = 0;
+    for (int64_t row = int64_t{blockIdx.x} * groups + group; row < p.rows;
+         row += int64_t{gridDim.x} * groups, turn ^= 1) {
+        F2 v[CH][4];
+        const TX* x = static_cast<const TX*>(p.x) + row * p.ldx + c.first;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) c.load(x, ch, v[ch]);
+        if (MODE != kLnRaw && p.r != nullptr) {
+            const TR* rr = static_cast<const TR*>(p.r) + row * p.ldr + c.first;
+            F2 r[CH][4];
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) c.load(rr, ch, r[ch]);
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[ch][i]);
+        }
+        if (MODE != kLnRaw && p.y != nullptr) {
+            TR* y = static_cast<TR*>(p.y) + row * p.ldy + c.first;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) c.store(y, ch, v[ch]);
+        }
+        if (MODE != kLnRaw) {
+            if (MODE == kLnH && p.h == nullptr) continue;
+            F2 a = 0;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
+            const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
+            F2 b = 0;
+            a = 0;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                c.less(ch, m, v[ch]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a = f2_add(a, v[ch][i]);
+                    b = f2_fma(v[ch][i], v[ch][i], b);
+                }
+            }
+            // both at once: the lower lanes take Σd, the upper ones Σd²
+            const float a1 = f2_sum(a), b1 = f2_sum(b);
+            float w = (lane < 16 ? a1 : b1) + __shfl_xor_sync(0xffffffffu, lane < 16 ? b1 : a1, 16);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            float off, var;  // mu - m, Σ (v - mu)²
+            if (alone) {
+                const float s1 = __shfl_sync(0xffffffffu, w, 0);
+                off = s1 * inv;
+                var = __shfl_sync(0xffffffffu, w, 16) - off * s1;
+            } else {
+                if (lane == 0) {
+                    stat[turn][0][warp] = m;
+                    stat[turn][1][warp] = w;
+                }
+                if (lane == 16) stat[turn][2][warp] = w;
+                __syncthreads();
+                const bool has = lane < warps;
+                const float m0 = stat[turn][0][0];
+                const float mu = has ? stat[turn][0][lane] - m0 : 0.0f;
+                const float s1 = has ? stat[turn][1][lane] : 0.0f;
+                const float shift = ln_warp_sum(fmaf(count, mu, s1)) * inv;  // mu - m_0
+                const float gu = mu - shift;
+                var = ln_warp_sum(has ? fmaf(gu, fmaf(count, gu, 2.0f * s1), stat[turn][2][lane]) : 0.0f);
+                off = shift - (m - m0);
+            }
+            const float s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
+            // (fmaxf would turn a NaN into 0)
+            const float ss = var == var ? s : var;
+            const F2 s2 = f2(ss, ss), o2 = f2(-off, -off);
+            const float* w_at = p.w != nullptr ? p.w + c.first : nullptr;
+            const float* b_at = p.b != nullptr ? p.b + c.first : nullptr;
+            TX* h = static_cast<TX*>(p.h) + row * p.ldh + c.first;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                F2 w2[4], b2[4];
+                c.weight(w_at, ch, w2, 1.0f);
+                c.weight(b_at, ch, b2, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[ch][i] = f2_fma(f2_mul(f2_add(v[ch][i], o2), s2), w2[i], b2[i]);
+                if (MODE == kLnH) c.store(h, ch, v[ch]);
+            }
+        }
+        if constexpr (MODE != kLnH) {
+            float size = 0.0f;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = f2_get(v[ch][i]);
+                    size = ln_most(size, c.has(ch, 2 * i) ? f.x : 0.0f, c.has(ch, 2 * i + 1) ? f.y : 0.0f);
+                }
+            uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(size) & 0x7fffffffu);
+            if (!alone) {
+                if (lane == 0) most[turn][warp] = u;
+                __syncthreads();
+                u = __reduce_max_sync(0xffffffffu, lane < warps ? most[turn][lane] : 0u);
+            }
+            const float scale = ln_scale(u);
+            if (lane == 0 && warp == 0) p.scale[row] = scale;
+            const LnCoder coder(scale);
+            int8_t* to = static_cast<int8_t*>(p.h) + row * p.ldh + c.first;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                uint32_t code[8];
+                coder.codes(v[ch], code);
+                if constexpr (VEC) {
+                    if (c.has(ch, 0)) {
+                        uint2 w;
+                        w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040),
+                                          __byte_perm(code[2], code[3], 0x0040), 0x5410);
+                        w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040),
+                                          __byte_perm(code[6], code[7], 0x0040), 0x5410);
+                        *reinterpret_cast<uint2*>(to + c.at(ch, 0)) = w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c.has(ch, i)) to[c.at(ch, i)] = static_cast<int8_t>(code[i]);
+                }
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------------ any width and stride
@@ -149,14 +458,13 @@ __global__ void __launch_bounds__(256) tg_layer_norm_simple(const LayerNormParam
             scale = ln_scale(ln_block_max(most, reinterpret_cast<uint32_t*>(red)));
             if (threadIdx.x == 0) p.scale[row] = scale;
         }
-        const LnCoder coder(scale);
         // (the last look at r: y may take its place)
         for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
             const float v = value(c), h = normed(v, c);
             if (MODE == kLnH) {
                 if (p.h != nullptr) (static_cast<TX*>(p.h) + row * p.ldh)[c] = op_round<TX>(h);
             } else {
-                (static_cast<int8_t*>(p.h) + row * p.ldh)[c] = static_cast<int8_t>(coder.code(h));
+                (static_cast<int8_t*>(p.h) + row * p.ldh)[c] = static_cast<int8_t>(LnCoder::any(h, scale));
             }
             if (p.y != nullptr) (static_cast<TR*>(p.y) + row * p.ldy)[c] = op_round<TR>(v);
         }
