@@ -476,7 +476,7 @@ typedef struct {
     int64_t lddr;
     float* dweight;  /* device, cols values; needs weight                            */
     float* dbias;    /* device, cols values (bias itself is not read)                */
-    void* workspace; /* device, 16-byte aligned, or NULL: a buffer that belongs to the
+    void* workspace; /* device, 256-byte aligned, or NULL: a buffer that belongs to the
                       * (device, stream), grown on demand and kept until process exit;
                       * the first call of a size on a stream then has to come before any
                       * capture (else TG_ERR_NO_MEMORY)                              */

@@ -381,3 +381,40 @@ def test_codes_of_many_rows(tg, rows):
         codes, scale = tg.quantize_rows(x)
         want = ref.codes_of(x)
         assert torch.equal(scale, want[1]) and torch.equal(codes, want[0])
+
+
+def test_a_wait_for_another_block_that_runs_out_is_reported_once(tg):
+    """Sums that are not sent: the gradient's kernel gives up within its limit and returns,
+    the status says so once, and the next call is right."""
+    x, kept, dy, dh = make(3, 20000, BF16, BF16)
+    want = tg.layer_norm_backward(dy, dh, x, **kept)
+    tg.sync_status()
+    try:
+        tg.tg_debug_set_wait_timeout_ns(20_000_000)
+        tg.tg_debug_inject(1)
+        tg.layer_norm_backward(dy, dh, x, **kept)
+        with pytest.raises(tg.TgemmError) as e:
+            tg.sync_status()
+        assert e.value.status == tg.TG_ERR_TIMEOUT
+        tg.sync_status()
+    finally:
+        tg.tg_debug_inject(0)
+        tg.tg_debug_set_wait_timeout_ns(0)
+    for a, b in zip(tg.layer_norm_backward(dy, dh, x, **kept), want):
+        assert torch.equal(a, b)
+    tg.sync_status()
+
+
+@pytest.mark.parametrize("pad", [0, 1, 3])
+def test_one_row_at_the_end_of_its_memory(tg, pad):
+    """Matrices that begin and end where their allocation does (read off every boundary)."""
+    for cols in (5, 517, 1031, 9001):
+        for first in (0, 1):
+            def place(kind):
+                whole = torch.randn(3 * (cols + pad) - pad + first, device="cuda").to(kind)
+                return torch.as_strided(whole, (3, cols), (cols + pad, 1), first)
+            x, r, dy, dh = place(HALF), place(F32), place(F32), place(HALF)
+            w = 1 + torch.randn(cols, device="cuda")
+            want = ref.LayerNorm(x, r, weight=w, bias=w)
+            want.check(*tg.layer_norm(x, r, weight=w, bias=w), f"{cols}")
+            want.check_grads(tg.layer_norm_backward(dy, dh, x, r, weight=w, bias=w), dy, dh, f"{cols}")

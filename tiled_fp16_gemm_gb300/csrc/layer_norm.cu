@@ -23,6 +23,7 @@ using tg::RowPlan;
 using tg::wide;
 
 constexpr int64_t kMaxCols = 131071;   // codes of a row: whole sums of gemm_i8 fit 32 bits
+constexpr int kRingBytes = 214 * 1024;  // of shared memory, for rings
 constexpr int64_t kGradBlocks = 320;   // that share the column sums, at most
 
 tg::OpWorkspace g_workspace;  // column sums of the gradient, where the caller has none
@@ -179,7 +180,7 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
     if ((st = check_matrix(b->dh, b->lddh, a->cols, bx)) != TG_OK) return st;
     if ((st = check_matrix(b->dx, b->lddx, a->cols, bx)) != TG_OK) return st;
     if ((st = check_matrix(b->dresidual, b->lddr, a->cols, br)) != TG_OK) return st;
-    if (misaligned(b->dweight, 4) || misaligned(b->dbias, 4) || misaligned(b->workspace, 16))
+    if (misaligned(b->dweight, 4) || misaligned(b->dbias, 4) || misaligned(b->workspace, 256))
         return TG_ERR_MISALIGNED;
     if (b->workspace != nullptr && b->workspace_bytes < grad_workspace(a->rows, a->cols))
         return TG_ERR_INVALID_VALUE;
@@ -210,8 +211,41 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
     return with_types(a->dtype, a->stream_dtype, [&](auto tx, auto tr) {
         using TX = decltype(tx);
         using TR = decltype(tr);
-        const int64_t most = 2 * int64_t{dev.num_sms} < kGradBlocks ? 2 * dev.num_sms : kGradBlocks;
-        const int64_t blocks = a->rows < most ? a->rows : most;
+        const void* in[4] = {q.n.x, q.n.r, q.dy, q.dh};
+        const int64_t ld[4] = {q.n.ldx, q.n.ldr, q.lddy, q.lddh};
+        const int elem[4] = {sizeof(TX), sizeof(TR), sizeof(TR), sizeof(TX)};
+        bool vec = cols % 8 == 0 && wide(q.n.w, 0, 4) && wide(q.dx, q.lddx, sizeof(TX)) &&
+                   wide(q.dr, q.lddr, sizeof(TR));
+        for (int k = 0; k < 4; ++k) vec = vec && wide(in[k], ld[k], elem[k]);
+        // A warp has 512 columns, a block as many warps as their rings fit; longer rows lie on the
+        // blocks of a cluster.
+        const int ring = 2 * tg::kLnGradStages * (vec ? tg::LnInput<TX, true>::kBytes + tg::LnInput<TR, true>::kBytes
+                                                      : tg::LnInput<TX, false>::kBytes + tg::LnInput<TR, false>::kBytes);
+        const int fit = kRingBytes / ring < tg::kLnGradWarps ? kRingBytes / ring : tg::kLnGradWarps;
+        int split = 1;
+        while (split <= tg::kNormSplit && cols > int64_t{split} * fit * tg::kLnGradCols) split *= 2;
+        const bool rows_ring = split <= tg::kNormSplit;
+        const int part = split == 1 ? static_cast<int>(cols)
+                                    : static_cast<int>((cols + 8 * split - 1) / (8 * split)) * 8;
+        const int warps = (part + tg::kLnGradCols - 1) / tg::kLnGradCols;  // of a row
+        int groups = 1;
+        int64_t most = 2 * dev.num_sms;
+        if (rows_ring) {
+            const int64_t each = (a->rows + dev.num_sms - 1) / dev.num_sms;
+            groups = split > 1 ? 1 : fit / warps < each ? fit / warps : static_cast<int>(each);
+            most = dev.num_sms;
+        }
+        const size_t smem = static_cast<size_t>(ring) * groups * warps;
+        if (rows_ring && split > 1) {
+            const auto kernel = vec ? tg::tg_layer_norm_grad_rows<TX, TR, true, true>
+                                    : tg::tg_layer_norm_grad_rows<TX, TR, false, true>;
+            if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+            most = max_clusters(kernel, split, 32 * warps, smem, dev);
+            if (most < 1) return TG_ERR_LAUNCH;
+        }
+        if (most > kGradBlocks) most = kGradBlocks;
+        const int64_t wanted = (a->rows + groups - 1) / groups;
+        const int64_t blocks = wanted < most ? wanted : most;
         tg::OpWorkspace::Hold hold;  // until the shares' sums are launched
         if (q.dw != nullptr || q.db != nullptr) {
             void* ws = b->workspace;
@@ -223,7 +257,20 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             if (q.dw != nullptr) q.ws_w = next, next += blocks * cols;
             if (q.db != nullptr) q.ws_b = next;
         }
-        st = launch(tg::tg_layer_norm_grad_simple<TX, TR>, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, s, q);
+        auto run = [&](auto kernel) {
+            if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
+            return launch(kernel, dim3(static_cast<unsigned>(blocks * split)), 32 * warps * groups, smem, split, s, q,
+                          warps, split, part, tg::op_wait_limit_ns(), dev.timeouts,
+                          split > 1 ? tg::op_take_inject() : 0);
+        };
+        if (!rows_ring)
+            st = launch(tg::tg_layer_norm_grad_simple<TX, TR>, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, s, q);
+        else if (split > 1)
+            st = vec ? run(tg::tg_layer_norm_grad_rows<TX, TR, true, true>)
+                     : run(tg::tg_layer_norm_grad_rows<TX, TR, false, true>);
+        else
+            st = vec ? run(tg::tg_layer_norm_grad_rows<TX, TR, true, false>)
+                     : run(tg::tg_layer_norm_grad_rows<TX, TR, false, false>);
         if (st != TG_OK || (q.dw == nullptr && q.db == nullptr)) return st;
         return launch(tg::tg_layer_norm_grad_sum, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, 1, s, q,
                       blocks);

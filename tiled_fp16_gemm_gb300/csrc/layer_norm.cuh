@@ -414,6 +414,313 @@ __global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<C
     }
 }
 
+// ------------------------------------------------------------------ the gradient of rows in a ring
+//
+// A thread has 16 columns of every row that its warps take, and keeps their sums (of dw and db) in
+// registers, and their weights.  The rows come through a ring in shared memory, a part of it for
+// each warp, by cp.async: x, r and dh are read for the row's sums, dh and dy again for the results.
+// The statistics are those of tg_layer_norm_rows, with two sums more in the same exchange,
+//   Σ dn   and   Σ dn (v - mu) = Σ_u (Σ dn d + g_u Σ dn).
+// A block of 16 warps has as many groups of warps as rows fit beside one another; at the end it
+// joins their sums and writes one share.
+//
+// MULTI: the `split` blocks of a cluster share their rows, `part` columns each, and exchange
+// their means and sums: for rows of more columns than a block's threads have in registers.
+
+constexpr int kLnGradWarps = 16;
+constexpr int kLnGradCols = 512;  // of a warp
+constexpr int kLnGradStages = 2;
+
+// One input's place in the ring.  VEC: fp32 values are fetched in the order of memory (lane l the
+// l-th and the l + 32-th 16 bytes of 256 columns), so that each fetch takes whole sectors, and lie
+// turned so that the reads of both halves fall into all banks.  Else the 16-byte granules that
+// hold the warp's columns are fetched, and single values read out of them.
+template <typename T, bool VEC>
+struct LnInput {
+    using Cols = LnCols<2, VEC>;
+    static constexpr int kPieces = sizeof(T) / 2;
+    static constexpr int kBytes = kLnGradCols * static_cast<int>(sizeof(T)) + (VEC ? 0 : 16);
+    const T* base;  // at the block's first column; null: absent
+    int64_t ld;
+    unsigned char* place;  // of this warp, in stage 0
+    int first;             // column of the warp
+
+    __device__ __forceinline__ static int piece(int n) { return kPieces == 1 ? n : n ^ (n >> 3 & 1); }
+    __device__ __forceinline__ void fetch(const Cols& c, int offset, int64_t row, int lane) const {
+        if (base == nullptr) return;
+        const T* src = base + row * ld + first;
+        const uint32_t to = op_smem(place + offset);
+        if constexpr (VEC) {
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                for (int h = 0; h < kPieces; ++h) {
+                    const int n = lane + 32 * h, col = 256 * ch + n * (8 / kPieces);
+                    if (first + col < c.cols) norm_copy16(to + ch * 512 * kPieces + 16 * piece(n), src + col);
+                }
+        } else {
+            const int cols = min(c.cols - first, kLnGradCols);
+            if (cols <= 0) return;
+            const Granules g = granules(reinterpret_cast<uint64_t>(base),
+                                        static_cast<uint64_t>((row * ld + first) * static_cast<int64_t>(sizeof(T))),
+                                        cols * static_cast<int>(sizeof(T)));
+            const unsigned char* at = reinterpret_cast<const unsigned char*>(src) - g.skip;
+            for (int b = 16 * lane; b < g.end; b += 512) {
+                const int n = g.end - b < 16 ? g.end - b : 16;
+                if (b == 0 && g.outside) {
+                    for (int i = g.skip; i < n; i += static_cast<int>(sizeof(T)))
+                        *reinterpret_cast<T*>(place + offset + i) = *reinterpret_cast<const T*>(at + i);
+                } else {
+                    norm_copy16(to + b, at + b, n);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void get(const Cols& c, int offset, int64_t row, int ch, int lane, F2 (&v)[4]) const {
+        const unsigned char* s = place + offset;
+        if (base == nullptr || (VEC && !c.has(ch, 0))) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = 0;
+        } else if constexpr (!VEC) {
+            const T* t = reinterpret_cast<const T*>(
+                             s + (reinterpret_cast<uintptr_t>(base + row * ld + first) & 15)) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = f2(c.has(ch, 2 * i) ? op_to_float(t[c.at(ch, 2 * i)]) : 0.0f,
+                          c.has(ch, 2 * i + 1) ? op_to_float(t[c.at(ch, 2 * i + 1)]) : 0.0f);
+        } else if constexpr (kPieces == 2) {
+            s += ch * 1024;
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s + 16 * piece(2 * lane));
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(s + 16 * piece(2 * lane + 1));
+            v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(s + ch * 512 + 16 * lane);
+            v[0] = ln_pair<T>(u.x), v[1] = ln_pair<T>(u.y), v[2] = ln_pair<T>(u.z), v[3] = ln_pair<T>(u.w);
+        }
+    }
+};
+
+// `warps`: of a group.  Shared memory: the warps' rings, and at the end the groups' sums.
+template <typename TX, typename TR, bool VEC, bool MULTI>
+__global__ void __launch_bounds__(32 * kLnGradWarps, 1)
+    tg_layer_norm_grad_rows(const LayerNormGradParams q, int warps, int split, int part, uint64_t limit_ns,
+                            unsigned int* timeouts, int inject) {
+    constexpr int CH = 2;
+    extern __shared__ __align__(16) unsigned char ln_ring[];
+    // [turn][m, Σd, Σd², Σdn, Σdn·d][warp]: one row's are read while the next one's come
+    __shared__ float red[2][5][kLnGradWarps];
+    const LayerNormParams& p = q.n;
+    const int lane = threadIdx.x & 31, all_warps = blockDim.x >> 5;
+    const int group = (threadIdx.x >> 5) / warps, warp = (threadIdx.x >> 5) - group * warps;
+    const int groups = all_warps / warps;
+    const int rank = MULTI ? blockIdx.x % split : 0;
+    const int64_t block = MULTI ? blockIdx.x / split : blockIdx.x;
+    const int64_t blocks = MULTI ? gridDim.x / split : gridDim.x;
+    const int c0 = MULTI ? rank * part : 0;  // first column here
+    const int cols = MULTI ? min(static_cast<int>(p.cols) - c0, part) : static_cast<int>(p.cols);
+    const LnCols<CH, VEC> c(cols, warp, lane);
+    NormPeers<MULTI> peers(rank, split, limit_ns, timeouts, inject == 1 && blockIdx.x == 1);
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    // lane u (and u + 16): columns of warp u
+    const int u = lane & 15;
+    const float count = u < warps ? static_cast<float>(max(min(cols - kLnGradCols * u, kLnGradCols), 0)) : 0.0f;
+    const float mine = __shfl_sync(0xffffffffu, count, warp);
+    const float mine_inv = mine > 0.0f ? 1.0f / mine : 0.0f;
+    const float here_inv = MULTI ? 1.0f / static_cast<float>(cols) : inv;
+
+    constexpr int bx = LnInput<TX, VEC>::kBytes, br = LnInput<TR, VEC>::kBytes, kStage = 2 * (bx + br);
+    unsigned char* const place = ln_ring + (threadIdx.x >> 5) * kLnGradStages * kStage;
+    const int first = warp * kLnGradCols;
+    const LnInput<TX, VEC> in_x{static_cast<const TX*>(norm_at<TX>(p.x, c0)), p.ldx, place, first};
+    const LnInput<TX, VEC> in_dh{static_cast<const TX*>(norm_at<TX>(q.dh, c0)), q.lddh, place + bx, first};
+    const LnInput<TR, VEC> in_r{static_cast<const TR*>(norm_at<TR>(p.r, c0)), p.ldr, place + 2 * bx, first};
+    const LnInput<TR, VEC> in_dy{static_cast<const TR*>(norm_at<TR>(q.dy, c0)), q.lddy, place + 2 * bx + br, first};
+    const bool has_dh = in_dh.base != nullptr;
+    const int64_t step = blocks * groups;
+    int64_t row = block * groups + group, next = row;
+    auto fetch = [&](int offset) {
+        if (next < p.rows) {
+            if (has_dh) {
+                in_x.fetch(c, offset, next, lane);
+                in_r.fetch(c, offset, next, lane);
+                in_dh.fetch(c, offset, next, lane);
+            }
+            in_dy.fetch(c, offset, next, lane);
+        }
+        next += step;
+        norm_commit();
+    };
+    op_release_next();
+    op_wait_previous();
+    for (int i = 0; i < kLnGradStages; ++i) fetch(i * kStage);
+    F2 w[CH][4], sum_w[CH][4], sum_b[CH][4];
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+        c.weight(p.w != nullptr ? p.w + c0 + c.first : nullptr, ch, w[ch], 1.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (!c.has(ch, 2 * i)) w[ch][i] = 0;
+            sum_w[ch][i] = sum_b[ch][i] = 0;
+        }
+    }
+
+    static_assert(kLnGradStages == 2, "a row's stage is its turn");
+    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const int at = turn * kStage;
+        F2 v[CH][4];
+        float s = 0.0f, off = 0.0f, m1 = 0.0f, m2 = 0.0f;  // off: mu - m
+        if (has_dh) {
+            F2 a = 0;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                in_x.get(c, at, row, ch, lane, v[ch]);
+                if (in_r.base != nullptr) {
+                    F2 r[4];
+                    in_r.get(c, at, row, ch, lane, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
+            }
+            const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
+            F2 b[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                F2 dh[4];
+                in_dh.get(c, at, row, ch, lane, dh);
+                c.less(ch, m, v[ch]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 dn = f2_mul(dh[i], w[ch][i]);
+                    b[0] = f2_add(b[0], v[ch][i]);
+                    b[1] = f2_fma(v[ch][i], v[ch][i], b[1]);
+                    b[2] = f2_add(b[2], dn);
+                    b[3] = f2_fma(dn, v[ch][i], b[3]);
+                }
+            }
+            // Four sums at once: 8 lanes for each.
+            const bool b4 = lane & 16, b3 = lane & 8;
+            const float s0 = f2_sum(b[0]), s1 = f2_sum(b[1]), s2 = f2_sum(b[2]), s3 = f2_sum(b[3]);
+            const float e = (b4 ? s2 : s0) + __shfl_xor_sync(0xffffffffu, b4 ? s0 : s2, 16);
+            const float f = (b4 ? s3 : s1) + __shfl_xor_sync(0xffffffffu, b4 ? s1 : s3, 16);
+            float t = (b3 ? f : e) + __shfl_xor_sync(0xffffffffu, b3 ? e : f, 8);  // sum lane / 8
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            float mean, var, p1, p2;  // of the block: mean - m, Σ (v - mean)², Σ dn, Σ dn (v - mean)
+            if (warps == 1) {
+                const float d1 = __shfl_sync(0xffffffffu, t, 0), d2 = __shfl_sync(0xffffffffu, t, 8);
+                mean = d1 * here_inv;
+                var = d2 - mean * d1;
+                p1 = __shfl_sync(0xffffffffu, t, 16);
+                p2 = __shfl_sync(0xffffffffu, t, 24) - mean * p1;
+                off = mean;
+                if (MULTI) mean += m;
+            } else {
+                float* r = &red[turn][0][group * warps];
+                if ((lane & 7) == 0) r[(1 + (lane >> 3)) * kLnGradWarps + warp] = t;
+                if (lane == 0) r[warp] = m;
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
+                const bool has = u < warps;
+                const float m0 = r[0];
+                const float mu = has ? r[u] - m0 : 0.0f, d1 = has ? r[kLnGradWarps + u] : 0.0f;
+                const float dn = has ? r[3 * kLnGradWarps + u] : 0.0f;
+                // the lower lanes take one sum, the upper ones another
+                float z = b4 ? dn : fmaf(count, mu, d1);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                const float shift = __shfl_sync(0xffffffffu, z, 0) * here_inv;
+                p1 = __shfl_sync(0xffffffffu, z, 16);
+                const float gu = mu - shift;
+                z = !has ? 0.0f
+                    : b4 ? fmaf(gu, dn, r[4 * kLnGradWarps + u])
+                         : fmaf(gu, fmaf(count, gu, 2.0f * d1), r[2 * kLnGradWarps + u]);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                var = __shfl_sync(0xffffffffu, z, 0);
+                p2 = __shfl_sync(0xffffffffu, z, 16);
+                off = shift - (m - m0);
+                mean = m0 + shift;
+            }
+            if constexpr (MULTI) {
+                const float send[4] = {mean, var, p1, p2};
+                const float* got = peers.exchange(send);
+                const float from = got[0];
+                auto columns = [&](int b) {
+                    return static_cast<float>(min(static_cast<int>(p.cols) - b * part, part));
+                };
+                float shift = 0.0f;
+                for (int b = 1; b < split; ++b) shift = fmaf(columns(b), got[8 * b] - from, shift);
+                shift *= inv;
+                var = p1 = p2 = 0.0f;
+                for (int b = 0; b < split; ++b) {
+                    const float g = got[8 * b] - from - shift;
+                    var += fmaf(columns(b) * g, g, got[8 * b + 1]);
+                    p1 += got[8 * b + 2];
+                    p2 += fmaf(g, got[8 * b + 2], got[8 * b + 3]);
+                }
+                off += shift - (mean - from);
+            }
+            s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
+            if (!(var == var)) s = var;  // (fmaxf would turn a NaN into 0)
+            m1 = p1 * inv;
+            m2 = p2 * inv * s;
+        }
+        const F2 s2 = f2(s, s), o2 = f2(-off, -off), m1n = f2(-m1, -m1), m2n = f2(-m2, -m2);
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+            F2 d[4];
+            in_dy.get(c, at, row, ch, lane, d);
+            if (has_dh) {
+                F2 dh[4];
+                in_dh.get(c, at, row, ch, lane, dh);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 n = f2_mul(f2_add(v[ch][i], o2), s2);
+                    sum_b[ch][i] = f2_add(sum_b[ch][i], dh[i]);
+                    sum_w[ch][i] = f2_fma(dh[i], n, sum_w[ch][i]);
+                    d[i] = f2_fma(s2, f2_fma(n, m2n, f2_fma(dh[i], w[ch][i], m1n)), d[i]);
+                }
+            }
+            if (q.dx != nullptr) c.store(static_cast<TX*>(q.dx) + row * q.lddx + c0 + c.first, ch, d);
+            if (q.dr != nullptr) c.store(static_cast<TR*>(q.dr) + row * q.lddr + c0 + c.first, ch, d);
+        }
+        __syncwarp();  // all lanes have read the stage, which is filled again
+        fetch(at);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // The groups' sums, in their order, to the block's share.
+    auto join = [&](F2 (&v)[CH][4], float* share) {
+        if (share == nullptr) return;  // (the same for the whole grid)
+        F2* all = reinterpret_cast<F2*>(ln_ring);
+        if (groups > 1) {
+            __syncthreads();
+            if (group > 0)
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        all[((group - 1) * 8 + 4 * ch + i) * 32 * warps + 32 * warp + lane] = v[ch][i];
+            __syncthreads();
+        }
+        if (group > 0) return;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+            for (int g = 1; g < groups; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[ch][i] = f2_add(v[ch][i], all[((g - 1) * 8 + 4 * ch + i) * 32 * warps + 32 * warp + lane]);
+            c.store(share + block * p.cols + c0 + c.first, ch, v[ch]);
+        }
+    };
+    join(sum_w, q.ws_w);
+    join(sum_b, q.ws_b);
+    peers.end();
+}
+
 // ------------------------------------------------------------------ any width and stride
 //
 // A row per block and turn; values are read again for each pass, from L2.
