@@ -3,6 +3,8 @@
 //   C[m][n] = out( act( sa[m] · sb[n] · Σ_k a[m][k]·b[n][k] + bias[n] ) + R[m][n] )
 #pragma once
 
+#include <type_traits>
+
 #include "op_device.cuh"
 #include "tc_device.cuh"
 
@@ -32,20 +34,24 @@ __device__ __forceinline__ float i8_value(const I8Params& p, float sum, float sa
 
 // ------------------------------------------------------------------ few rows of A
 //
-// Up to 16 tokens: B's bytes are what counts, each read once.  They come by TMA (zeros past the
-// edges) and go from shared memory straight into the operands of mma.sync (m16n8k32, s8 to s32),
-// B's rows on the side of 16, the tokens on that of 8.  The sums are 32-bit integers, exact in
-// any order, so the order is free everywhere:
-//   - k: a lane takes 16 neighbouring bytes of a row for two MMAs, and the same bytes of a token;
-//   - the warps of a block share out steps of 16 rows by 128 k one by one, whatever tile they
-//     belong to, and add what they have of a tile to its sums in shared memory;
-//   - the blocks of a cluster share k too, and add to the sums in the shared memory of the
-//     tile's owner.  No scratch in global memory, one join at the end.
+// B's bytes are what counts, each read once.  They come by TMA (zeros past the edges) and go from
+// shared memory into the operands of mma.sync, B's rows on the side of 16, the tokens on that of
+// 8.  The order of sums of whole numbers is free everywhere:
+//   - k: a lane takes 16 neighbouring bytes of a row, and the same bytes of a token;
+//   - the warps of a block share its steps of 16 rows by 128 k evenly, whatever tiles they
+//     belong to, and add what they have of a tile to its 32-bit sums in shared memory;
+//   - the blocks of a cluster share k too, and in the end read one another's sums.  No scratch
+//     in global memory.  (Sums added straight to those of another block, by its shared memory's
+//     atomics: 512×8192 with 16 tokens 8.8 us.)
 // Each warp has a ring of its own, which its first lane fills some steps ahead, across the
 // borders of tiles.
 //
-// The MMA's rate here is 273 products a cycle of an SM, 34 bytes of B: for 8 tokens more than
-// memory delivers (23), for 16 half of it.
+// Up to 8 tokens the MMA is m16n8k32, s8 to s32.  Its rate is 273 products a cycle of an SM, 34
+// bytes of B with 8 tokens: more than memory delivers (23).  For more tokens it is m16n8k16 in
+// fp16, at 1028, on codes decoded in registers (five instructions for four) and tokens decoded
+// into shared memory: whole numbers up to 2048 are exact in fp16, and their sums in fp32 up to
+// 2^24, which eight steps do not pass; then they go to the 32-bit sums.  (16 tokens on s8:
+// 16384×8192 in 40 us.)
 
 constexpr int kI8FewWarps = 16;
 constexpr int kI8FewThreads = 32 * kI8FewWarps;
@@ -53,6 +59,7 @@ constexpr int kI8FewRows = 16;
 constexpr int kI8FewK = 128;
 constexpr int kI8FewStep = kI8FewRows * kI8FewK;
 constexpr int kI8FewStages = 3;  // at most
+constexpr int kI8FewRun = 8;     // steps whose sums are exact in fp32: 8 · 128 · 2^14 = 2^24
 constexpr int kI8FewAhead = 3;   // steps of a warp, to L2 before the kernel may read
 constexpr int kI8FewBars = kI8FewWarps * kI8FewStages * 8;
 
@@ -75,6 +82,23 @@ __device__ __forceinline__ void i8_mma(int (&c)[4], uint32_t a0, uint32_t a1, ui
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four codes of a word as two pairs of fp16: with the sign turned, a byte u is code + 128, the
+// fp16 number 0x6400 | u is 1024 + u, and 1152 less is the code, exactly.
+__device__ __forceinline__ void i8_decode(uint32_t word, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = word ^ 0x80808080u;
+    const uint32_t off = 0x64806480u;  // 1152, twice
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(off));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(off));
+}
+__device__ __forceinline__ void i8_mma_half(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // 16 bytes of a row from byte k on, 0 past its `n`: of any alignment, and nothing outside it read.
@@ -108,11 +132,11 @@ __device__ __forceinline__ void i8_cluster_sync() {
 }
 
 // NT: tokens / 8.  Grid: the clusters' blocks side by side.  Shared memory: the rings; their
-// barriers; the tokens' bytes of this block's k; the sums of the tiles that it owns (every
-// cluster-th of the cluster's).
+// barriers; the tokens' bytes of this block's k; the sums of the cluster's tiles.
 template <typename TC, int NT>
 __global__ void __launch_bounds__(kI8FewThreads, 1)
     tg_gemm_i8_few(const __grid_constant__ I8Few q, const __grid_constant__ CUtensorMap codes) {
+    constexpr bool kHalf = NT > 1, kKeep = NT == 2 || NT == 4;
     extern __shared__ __align__(1024) unsigned char i8_dynamic[];
     const I8Params& p = q.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -139,19 +163,20 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
     for (int i = threadIdx.x; i < tokens * q.sums_pitch; i += kI8FewThreads) sums[i] = 0;
     __syncwarp();
 
-    const int dt = kI8FewWarps / chunks, dc = kI8FewWarps % chunks;
+    // This warp's steps: an even share of the block's, tile by tile, k inside.
+    const int all = tiles * chunks;
+    const int u0 = static_cast<int>(int64_t{all} * warp / kI8FewWarps);
+    const int steps = static_cast<int>(int64_t{all} * (warp + 1) / kI8FewWarps) - u0;
     struct Place {
         int tile, chunk;
     };
     auto advance = [&](Place& at) {
-        at.tile += dt;
-        at.chunk += dc;
-        if (at.chunk >= chunks) at.chunk -= chunks, ++at.tile;
+        if (++at.chunk == chunks) at.chunk = 0, ++at.tile;
     };
-    Place next{warp / chunks, warp % chunks}, here = next;
+    Place next{u0 / chunks, u0 % chunks}, here = next;
     int fill = 0, issued = 0;  // the stage that is filled next
     auto fetch = [&] {
-        if (next.tile >= tiles) return;
+        if (issued == steps) return;
         if (lane == 0 && !(q.inject == 1 && blockIdx.x == 0 && issued == 0)) {
             const uint32_t bar = bars + 8 * fill;
             op_bar_expect(bar, kI8FewStep);
@@ -166,7 +191,7 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
         // While the kernel before this one ends, the first steps come as far as L2 (no value is
         // taken yet: that kernel may still write them).
         Place soon = next;
-        for (int s = 0; s < kI8FewAhead && soon.tile < tiles; ++s, advance(soon))
+        for (int s = 0; s < kI8FewAhead && s < steps; ++s, advance(soon))
             i8_prefetch(&codes, (c0 + soon.chunk) * kI8FewK, (tile0 + soon.tile) * kI8FewRows);
     }
     op_wait_previous();
@@ -174,57 +199,86 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
     {  // the tokens
         const bool wide = (reinterpret_cast<uintptr_t>(p.A) & 15) == 0 && p.lda % 16 == 0;
         const int pieces = kI8FewK / 16 * chunks;
-        for (int m = 0; m < tokens; ++m) {
-            const int8_t* a = p.A + m * p.lda;
-            for (int i = threadIdx.x; i < pieces; i += kI8FewThreads) {
-                const int64_t k = int64_t{c0} * kI8FewK + 16 * i;
-                unsigned char* to = x_all + m * q.x_pitch + 16 * i;
-                if (wide && k + 16 <= p.K)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
-                                 : "memory");
-                else
-                    *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+        if constexpr (kHalf) {
+            // four pieces of a thread under way at a time
+            for (int i0 = threadIdx.x; i0 < tokens * pieces; i0 += 4 * kI8FewThreads) {
+                uint4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * kI8FewThreads, m = i / pieces;
+                    const int64_t k = int64_t{c0} * kI8FewK + 16 * (i - m * pieces);
+                    if (m < tokens)
+                        v[j] = wide && k + 16 <= p.K ? *reinterpret_cast<const uint4*>(p.A + m * p.lda + k)
+                                                     : i8_bytes(p.A + m * p.lda, k, p.K);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j * kI8FewThreads, m = i / pieces, piece = i - m * pieces;
+                    if (m >= tokens) break;
+                    uint4 y[2];
+                    i8_decode(v[j].x, y[0].x, y[0].y);
+                    i8_decode(v[j].y, y[0].z, y[0].w);
+                    i8_decode(v[j].z, y[1].x, y[1].y);
+                    i8_decode(v[j].w, y[1].z, y[1].w);
+                    // of each 64 k the first halves of the 16s, then the others
+                    uint4* to = reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 128 * (piece >> 2) + 16 * (piece & 3));
+                    to[0] = y[0];
+                    to[4] = y[1];
+                }
+            }
+        } else {
+            for (int m = 0; m < tokens; ++m) {
+                const int8_t* a = p.A + m * p.lda;
+                for (int i = threadIdx.x; i < pieces; i += kI8FewThreads) {
+                    const int64_t k = int64_t{c0} * kI8FewK + 16 * i;
+                    unsigned char* to = x_all + m * q.x_pitch + 16 * i;
+                    if (wide && k + 16 <= p.K)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
+                                     : "memory");
+                    else
+                        *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    if (q.cluster > 1)
-        i8_cluster_sync();  // (the owners' sums are zero, too)
-    else
-        __syncthreads();
+    __syncthreads();
 
     // A lane's MMA row g is row r of the tile (g + 8: r + 8): so the eight lanes that read at a
     // time find their 16 bytes, swizzled by r, in all banks.
     const int r = (g >> 1) + 4 * (g & 1);
-    int c[NT][4];
+    typename std::conditional<kHalf, float, int>::type c[NT][4];
+    int whole[kKeep ? NT : 1][4];  // kKeep: what fp32 does not hold exactly
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[i][j] = 0;
+#pragma unroll
+    for (int i = 0; i < (kKeep ? NT : 1); ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) whole[i][j] = 0;
     const uint32_t sums_at = op_smem(sums);
     auto flush = [&](int tile) {  // c[.][0, 1]: row g, tokens 2t and 2t + 1; [2, 3]: row g + 8
-        const int slot = q.cluster > 1 ? tile / q.cluster : tile;
-        uint32_t to = sums_at + 4 * (kI8FewRows * slot + r);
-        if (q.cluster > 1)
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(to), "r"(tile - slot * q.cluster));
+        const uint32_t to = sums_at + 4 * (kI8FewRows * tile + r);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int m = 8 * i + 2 * t + (j & 1);
                 if (m < tokens)
-                    asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(
+                    asm volatile("red.relaxed.cta.shared::cta.add.s32 [%0], %1;" ::"r"(
                                      to + 4 * (m * q.sums_pitch + 8 * (j >> 1))),
-                                 "r"(c[i][j])
+                                 "r"(static_cast<int>(c[i][j]) + (kKeep ? whole[kKeep ? i : 0][j] : 0))
                                  : "memory");
                 c[i][j] = 0;
+                if (kKeep) whole[kKeep ? i : 0][j] = 0;
             }
     };
     const unsigned char* x = x_all + g * q.x_pitch + 16 * t;
-    int slot = 0, used = 0;
+    int slot = 0, used = 0, run = 0;  // run: steps in c
     uint32_t parity = 0;
     bool lost = false;
-    while (here.tile < tiles) {
+    while (used < steps) {
         const bool ok = op_bar_wait(bars + 8 * slot, parity, q.limit_ns);
         if (!__all_sync(0xffffffffu, ok)) {
             lost = true;
@@ -235,13 +289,31 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
         for (int h = 0; h < 2; ++h) {
             const uint32_t at = row + (((4 * h + t) ^ r) << 4);
             const uint4 v = tc_lds128(at), w = tc_lds128(at + 8 * kI8FewK);
+            if constexpr (kHalf) {
+                const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
+                for (int f = 0; f < 2; ++f) {  // 8 of the 16 bytes
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        i8_decode(vs[2 * f + o], a[o][0], a[o][2]);
+                        i8_decode(ws[2 * f + o], a[o][1], a[o][3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        uint4 b = make_uint4(0, 0, 0, 0);
+                        if (8 * j + g < tokens)
+                            b = *reinterpret_cast<const uint4*>(x + 8 * j * q.x_pitch + 2 * kI8FewK * here.chunk +
+                                                                128 * h + 64 * f);
+                        i8_mma_half(c[j], a[0][0], a[0][1], a[0][2], a[0][3], b.x, b.y);
+                        i8_mma_half(c[j], a[1][0], a[1][1], a[1][2], a[1][3], b.z, b.w);
+                    }
+                }
+            } else {
                 uint4 a = make_uint4(0, 0, 0, 0);
-                if (8 * j + g < tokens)
-                    a = *reinterpret_cast<const uint4*>(x + 8 * j * q.x_pitch + kI8FewK * here.chunk + 64 * h);
-                i8_mma(c[j], v.x, w.x, v.y, w.y, a.x, a.y);
-                i8_mma(c[j], v.z, w.z, v.w, w.w, a.z, a.w);
+                if (g < tokens) a = *reinterpret_cast<const uint4*>(x + kI8FewK * here.chunk + 64 * h);
+                i8_mma(c[0], v.x, w.x, v.y, w.y, a.x, a.y);
+                i8_mma(c[0], v.z, w.z, v.w, w.w, a.z, a.w);
             }
         }
         ++used;
@@ -249,7 +321,19 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
         fetch();
         const int tile = here.tile;
         advance(here);
-        if (here.tile != tile) flush(tile);
+        if (here.tile != tile || used == steps || (kHalf && !kKeep && ++run == kI8FewRun)) {
+            flush(tile);
+            run = 0;
+        } else if (kKeep && ++run == kI8FewRun) {
+#pragma unroll
+            for (int i = 0; i < (kKeep ? NT : 1); ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    whole[i][j] += static_cast<int>(c[i][j]);
+                    c[i][j] = 0;
+                }
+            run = 0;
+        }
         if (++slot == q.stages) slot = 0, parity ^= 1;
     }
     if (lost) {
@@ -261,20 +345,35 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
         if (lane == 0) atomicOr(q.timeouts, kOpTimeoutI8);
     }
     if (q.cluster > 1)
-        i8_cluster_sync();  // and no block leaves before its sums have come
+        i8_cluster_sync();  // the other blocks' sums are complete, too
     else
         __syncthreads();
 
-    const int rows = (q.cluster > 1 ? (tiles - rank + q.cluster - 1) / q.cluster : tiles) * kI8FewRows;
+    // The blocks of a cluster finish its tiles in turn, each with the sums of all.
+    const int rows = (tiles - rank + q.cluster - 1) / q.cluster * kI8FewRows;
     for (int i = threadIdx.x; i < rows * tokens; i += kI8FewThreads) {
         const int m = i / rows, o = i - m * rows;
-        const int64_t n = int64_t{tile0 + o / kI8FewRows * q.cluster + rank} * kI8FewRows + o % kI8FewRows;
+        const int place = (o / kI8FewRows * q.cluster + rank) * kI8FewRows + o % kI8FewRows;
+        const int64_t n = int64_t{tile0} * kI8FewRows + place;
         if (n >= p.N) continue;
-        float y = i8_value(p, static_cast<float>(sums[m * q.sums_pitch + o]), p.sa[m], p.sb[n],
-                           p.bias != nullptr ? p.bias[n] : 0.0f);
+        int sum = 0;
+        if (q.cluster > 1) {
+            const uint32_t at = sums_at + 4 * (m * q.sums_pitch + place);
+            for (int b = 0; b < q.cluster; ++b) {
+                uint32_t there;
+                int v;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(b));
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+                sum += v;
+            }
+        } else {
+            sum = sums[m * q.sums_pitch + place];
+        }
+        float y = i8_value(p, static_cast<float>(sum), p.sa[m], p.sb[n], p.bias != nullptr ? p.bias[n] : 0.0f);
         if (p.resid != nullptr) y += op_to_float((static_cast<const TC*>(p.resid) + m * p.ldr)[n]);
         (static_cast<TC*>(p.C) + m * p.ldc)[n] = op_round<TC>(y);
     }
+    if (q.cluster > 1) i8_cluster_sync();  // no block leaves while others read its sums
 }
 
 // ------------------------------------------------------------------ any size

@@ -47,16 +47,6 @@ struct I8Wide {
     uint32_t* counters;  // eight per block, zeroed by tg_i8_expand
 };
 
-// Four codes of a word as two pairs of fp16: with the sign turned, a byte u is code + 128, the
-// fp16 number 0x6400 | u is 1024 + u, and 1152 less is the code, exactly.
-__device__ __forceinline__ void i8_decode(uint32_t word, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = word ^ 0x80808080u;
-    const uint32_t off = 0x64806480u;  // 1152, twice
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(off));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(off));
-}
-
 // A as fp16 in rows of `ldo` (a multiple of 128), zero past column K; and the counters zeroed.
 __global__ void __launch_bounds__(256)
     tg_i8_expand(const int8_t* __restrict__ A, int64_t lda, int64_t M, int64_t K, uint16_t* __restrict__ out,

@@ -11,7 +11,6 @@ namespace {
 using tg::I8Params;
 
 constexpr int64_t kMaxK = 131071;  // 2^17 - 1: a sum of K products of -128 · -128 fits 32 bits
-constexpr int64_t kFewRows = 8;    // of A, that take the kernel for few
 
 bool misaligned(const void* p, unsigned bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
@@ -85,67 +84,78 @@ const Limits& limits_of(Kernel kernel, int threads, int smem, const tg::OpDevice
     return lim;
 }
 
-// Few rows of A (NT: tokens / 8).  False where no shape fits: then nothing is launched.
+// Few rows of A (NT: tokens / 8).
+struct FewPlan {
+    tg::I8Few q;
+    size_t smem;
+    int64_t grid;
+    double time;  // us; 1e300: no shape fits
+};
+
+// The shape with the least time.  A round of a block's warps is 16 steps, 32 KB of B: 0.73 us of
+// memory, or what the tensor pipe or shared memory takes (measured, 16384×8192: see below); then
+// the fetch of the block's part of A, the joins of a cluster, a shallow ring.
 template <typename TC, int NT>
-bool launch_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_status_t* st) {
+FewPlan plan_few(const I8Params& p, const tg::OpDevice& dev) {
     auto kernel = tg::tg_gemm_i8_few<TC, NT>;
     static Limits limits[tg::kOpMaxDevices];
     const Limits& lim = limits_of(kernel, tg::kI8FewThreads, kSmem, dev, limits);
-    tg::I8Few q, best;
+    FewPlan best;
+    best.time = 1e300;
+    tg::I8Few q;
     std::memset(&q, 0, sizeof(q));
     q.p = p;
     const int64_t tiles = (p.N + tg::kI8FewRows - 1) / tg::kI8FewRows;
     q.tiles = static_cast<int32_t>(tiles);
     q.chunks = static_cast<int32_t>((p.K + tg::kI8FewK - 1) / tg::kI8FewK);
-    // The shape with the least time, in rounds of a block's warps (32 KB of B, about 0.73 us):
-    // the steps of a block, the fetch of its part of A, the joins of a cluster, a shallow ring.
-    double least = 1e300;
-    size_t smem = 0;
-    int64_t grid = 0;
+    constexpr double round = NT <= 2 ? 0.73 : NT == 4 ? 0.8 : 1.4;
     for (int i = 0; i < 4; ++i) {
         q.cluster = 1 << i;
         if (q.cluster > q.chunks || lim.clusters[i] < 1) break;
         const int64_t slice = (q.chunks + q.cluster - 1) / q.cluster;
-        q.x_pitch = static_cast<int32_t>(slice * tg::kI8FewK + 64);
+        q.x_pitch = static_cast<int32_t>(slice * tg::kI8FewK * (NT > 1 ? 2 : 1) + 64);
         int64_t clusters = tiles < lim.clusters[i] ? tiles : lim.clusters[i];
         for (q.stages = tg::kI8FewStages; q.stages >= 2; --q.stages) {
             const int64_t fixed = 1024 + int64_t{tg::kI8FewWarps} * q.stages * tg::kI8FewStep + tg::kI8FewBars +
                                   p.M * q.x_pitch;
             // (a block keeps the sums of its tiles: very many rows of B take several waves)
-            const int64_t room = (kSmem - fixed - p.M * 16) / (p.M * tg::kI8FewRows * 4) * q.cluster;
+            const int64_t room = (kSmem - fixed - p.M * 16) / (p.M * tg::kI8FewRows * 4);
             int64_t rounds = (tiles + clusters - 1) / clusters;
             if (room < 1 || (room < rounds && q.stages > 2)) continue;
             if (rounds > room) {
                 rounds = room;
                 clusters = (tiles + rounds - 1) / rounds;
             }
-            q.sums_pitch = static_cast<int32_t>((rounds + q.cluster - 1) / q.cluster * tg::kI8FewRows + 4);
+            q.sums_pitch = static_cast<int32_t>(rounds * tg::kI8FewRows + 4);
             const int64_t waves = (clusters + lim.clusters[i] - 1) / lim.clusters[i];
             const double steps = static_cast<double>((rounds * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps);
             const double time =
-                static_cast<double>(waves) * (steps + 1e-5 * static_cast<double>(slice * tg::kI8FewK * p.M) +
-                                              (q.cluster > 1 ? 1.5 : 0.0) + (q.stages < 3 ? 2.0 : 0.0));
-            if (time < least) {
-                least = time;
-                best = q;
-                smem = static_cast<size_t>(fixed + 4 * p.M * q.sums_pitch);
-                grid = clusters * q.cluster;
+                2.0 + static_cast<double>(waves) * (round * steps + 8e-6 * static_cast<double>(slice * tg::kI8FewK * p.M) +
+                                                    (q.cluster > 1 ? 1.1 : 0.0) + (q.stages < 3 ? 1.5 : 0.0));
+            if (time < best.time && clusters * q.cluster <= tg::kOpMaxDim) {
+                best.time = time;
+                best.q = q;
+                best.smem = static_cast<size_t>(fixed + 4 * p.M * q.sums_pitch);
+                best.grid = clusters * q.cluster;
             }
             break;
         }
     }
-    if (least > 1e299 || grid > tg::kOpMaxDim) return false;
+    return best;
+}
+
+template <typename TC, int NT>
+tg_status_t launch_few(FewPlan& plan, const tg::OpDevice& dev, cudaStream_t s) {
+    const I8Params& p = plan.q.p;
     CUtensorMap codes;
     if (!tg::op_map_2d(&codes, p.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.K, p.N, p.ldb, tg::kI8FewK, tg::kI8FewRows,
-                       CU_TENSOR_MAP_SWIZZLE_128B)) {
-        *st = TG_ERR_LAUNCH;
-        return true;
-    }
-    best.limit_ns = tg::op_wait_limit_ns();
-    best.timeouts = dev.timeouts;
-    best.inject = tg::op_take_inject();
-    *st = launch(kernel, dim3(static_cast<unsigned>(grid)), tg::kI8FewThreads, smem, best.cluster, s, best, codes);
-    return true;
+                       CU_TENSOR_MAP_SWIZZLE_128B))
+        return TG_ERR_LAUNCH;
+    plan.q.limit_ns = tg::op_wait_limit_ns();
+    plan.q.timeouts = dev.timeouts;
+    plan.q.inject = tg::op_take_inject();
+    return launch(tg::tg_gemm_i8_few<TC, NT>, dim3(static_cast<unsigned>(plan.grid)), tg::kI8FewThreads, plan.smem,
+                  plan.q.cluster, s, plan.q, codes);
 }
 
 // ------------------------------------------------------------------ many rows
@@ -253,11 +263,34 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
     return TG_OK;
 }
 
+// Whether the kernel for few rows is the faster one: up to 16 rows always, more of them with small
+// weights.  Measured, us, few / wide: 16384×8192 with 16 rows 28.7 / 30.9, 32 rows 48 / 31;
+// 4096×28672 with 16 rows 29.8 / 31.2; 4096×4096 with 32 rows 11.5 / 15.5; 8192×2048 with 32 rows
+// 12.4 / 12.6, 64 rows 18.9 / 12.8; 512×8192 with 64 rows 15.4 / 16.5; 1024×1024 with 64 rows 8.4 / 9.2.
+bool prefer_few(const I8Params& p) {
+    const int64_t codes = p.N * p.K;
+    return p.M <= 16 || (p.M <= 32 && codes <= 20000000) || (p.M <= 64 && codes <= 4500000);
+}
+
+// Launches the kernel for few rows; false where no shape fits.
+template <typename TC, int NT>
+bool take_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_status_t* st) {
+    FewPlan plan = plan_few<TC, NT>(p, dev);
+    if (plan.time > 1e299) return false;
+    *st = launch_few<TC, NT>(plan, dev, s);
+    return true;
+}
+
 template <typename TC>
 tg_status_t launch_type(const I8Params& p, const tg::OpDevice& dev, void* ws, cudaStream_t s) {
-    tg_status_t st;
-    if (p.K > 0 && p.M <= 8 && launch_few<TC, 1>(p, dev, s, &st)) return st;
-    if (p.K > 0 && p.M > 8 && p.M <= kFewRows && launch_few<TC, 2>(p, dev, s, &st)) return st;
+    tg_status_t st = TG_OK;
+    if (p.K > 0 && prefer_few(p)) {
+        if (p.M <= 8 ? take_few<TC, 1>(p, dev, s, &st)
+            : p.M <= 16 ? take_few<TC, 2>(p, dev, s, &st)
+            : p.M <= 32 ? take_few<TC, 4>(p, dev, s, &st)
+                        : take_few<TC, 8>(p, dev, s, &st))
+            return st;
+    }
     if (p.K > 0 && p.M > 8) return launch_wide<TC>(p, dev, ws, s);
     const int64_t blocks = (p.M * p.N + 7) / 8, most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_gemm_i8_simple<TC>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, 1, s,
