@@ -199,7 +199,19 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
     {  // the tokens
         const bool wide = (reinterpret_cast<uintptr_t>(p.A) & 15) == 0 && p.lda % 16 == 0;
         const int pieces = kI8FewK / 16 * chunks;
-        if constexpr (kHalf) {
+        if (!kHalf && wide) {
+            for (int m = 0; m < tokens; ++m)
+                for (int i = threadIdx.x; i < pieces; i += kI8FewThreads) {
+                    const int64_t k = int64_t{c0} * kI8FewK + 16 * i;
+                    const int8_t* a = p.A + m * p.lda;
+                    unsigned char* to = x_all + m * q.x_pitch + 16 * i;
+                    if (k + 16 <= p.K)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
+                                     : "memory");
+                    else
+                        *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+                }
+        } else {
             // four pieces of a thread under way at a time
             for (int i0 = threadIdx.x; i0 < tokens * pieces; i0 += 4 * kI8FewThreads) {
                 uint4 v[4];
@@ -215,28 +227,20 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
                 for (int j = 0; j < 4; ++j) {
                     const int i = i0 + j * kI8FewThreads, m = i / pieces, piece = i - m * pieces;
                     if (m >= tokens) break;
-                    uint4 y[2];
-                    i8_decode(v[j].x, y[0].x, y[0].y);
-                    i8_decode(v[j].y, y[0].z, y[0].w);
-                    i8_decode(v[j].z, y[1].x, y[1].y);
-                    i8_decode(v[j].w, y[1].z, y[1].w);
-                    // of each 64 k the first halves of the 16s, then the others
-                    uint4* to = reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 128 * (piece >> 2) + 16 * (piece & 3));
-                    to[0] = y[0];
-                    to[4] = y[1];
-                }
-            }
-        } else {
-            for (int m = 0; m < tokens; ++m) {
-                const int8_t* a = p.A + m * p.lda;
-                for (int i = threadIdx.x; i < pieces; i += kI8FewThreads) {
-                    const int64_t k = int64_t{c0} * kI8FewK + 16 * i;
-                    unsigned char* to = x_all + m * q.x_pitch + 16 * i;
-                    if (wide && k + 16 <= p.K)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
-                                     : "memory");
-                    else
-                        *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+                    if constexpr (kHalf) {
+                        uint4 y[2];
+                        i8_decode(v[j].x, y[0].x, y[0].y);
+                        i8_decode(v[j].y, y[0].z, y[0].w);
+                        i8_decode(v[j].z, y[1].x, y[1].y);
+                        i8_decode(v[j].w, y[1].z, y[1].w);
+                        // of each 64 k the first halves of the 16s, then the others
+                        uint4* to =
+                            reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 128 * (piece >> 2) + 16 * (piece & 3));
+                        to[0] = y[0];
+                        to[4] = y[1];
+                    } else {
+                        *reinterpret_cast<uint4*>(x_all + m * q.x_pitch + 16 * piece) = v[j];
+                    }
                 }
             }
         }

@@ -28,6 +28,7 @@ constexpr int kI8Tokens = 256;  // of a tile at most
 constexpr int kI8CodeBytes = kTcRows * kTcK;
 constexpr int kI8XBytes = kI8Tokens / 2 * 256;
 constexpr int kI8WideSmem = 1024 + kI8XStages * kI8XBytes + kI8Stages * kI8CodeBytes + 512;
+static_assert(kI8WideSmem <= 227 * 1024, "shared memory of a block");
 constexpr int kI8MaxClusters = 80;
 constexpr int64_t kI8CounterBytes = 8192;
 static_assert(kI8MaxClusters * kWideCluster * 32 <= kI8CounterBytes, "eight counters per block");
@@ -72,12 +73,14 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Epilogue and store of 16 tokens of row n, `most` of them.
+// Epilogue and store of 16 tokens of row n, `most` of them, whose scales the lanes from `first` on
+// hold.
 template <typename TC>
-__device__ __forceinline__ void i8_wide_store(const I8Params& p, int64_t m, int64_t n, int most, float sb, float bias,
-                                              float (&v)[16]) {
+__device__ __forceinline__ void i8_wide_store(const I8Params& p, int64_t m, int64_t n, int most, float scales, int first,
+                                              float sb, float bias, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i8_value(p, v[i], i < most ? p.sa[m + i] : 0.0f, sb, bias);
+    for (int i = 0; i < 16; ++i) v[i] = i8_value(p, v[i], __shfl_sync(0xffffffffu, scales, first + i), sb, bias);
+    if (n >= p.N) return;
     if (p.resid != nullptr) {
         const char* r = static_cast<const char*>(p.resid) + sizeof(TC) * (m * p.ldr + n);
 #pragma unroll
@@ -282,28 +285,55 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t row = 32 * quarter + lane;
         const uint32_t at = d_cols + (static_cast<uint32_t>(32 * quarter) << 16);
         const int64_t slot = int64_t{q.tokens} * kTcRows;
+        auto release = [&] {  // the sums have been read
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) wide_arrive(wide_at(d_empty, 0));
+        };
         int i = 0;
         uint32_t tiles = 0;
         while (i < n_units) {
             const int kb0 = kb;
             const int len = q.k_units - kb < n_units - i ? q.k_units - kb : n_units - i;
-            // (a barrier of its own: a parity says nothing of a phase further off than one)
-            if (!wait(d_full, tiles++ & 1)) break;
-            tc_after_sync();
             const int64_t n = first_row() + row, m0 = first_token();
             const int tokens = static_cast<int>(p.M - m0 < q.tokens ? p.M - m0 : q.tokens);
             const bool whole = len == q.k_units;
+            // What the epilogue needs is here before the sums are: the MMAs of the next tile wait
+            // for these to be read.
             const float bias = p.bias != nullptr && n < p.N ? p.bias[n] : 0.0f;
             const float sb = n < p.N ? p.sb[n] : 0.0f;
+            float scales[kI8Tokens / 64];  // of this warp's tokens, 32 in each
+#pragma unroll
+            for (int g = 0; g < kI8Tokens / 64; ++g) {
+                const int c = 64 * g + 32 * (lane >> 4) + 16 * set + (lane & 15);
+                scales[g] = c < tokens ? p.sa[m0 + c] : 0.0f;
+            }
+            // those of the next 16 tokens, in lanes from `first` on
+            int first = 0;
+            auto next_scales = [&] {
+                if (first == 16) {
+                    const float f = scales[0];
+#pragma unroll
+                    for (int g = 0; g + 1 < kI8Tokens / 64; ++g) scales[g] = scales[g + 1];
+                    scales[kI8Tokens / 64 - 1] = f;
+                }
+                first ^= 16;
+            };
+            // (a barrier of its own: a parity says nothing of a phase further off than one)
+            if (!wait(d_full, tiles++ & 1)) break;
+            tc_after_sync();
             float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
+            if (16 * set >= tokens) release();  // (no tokens for this warp)
             for (int c = 16 * set; c < tokens; c += 32) {
                 uint32_t r[16];
                 tc_load(at + c, r);
+                if (c + 32 >= tokens) release();
                 if (whole) {
                     float v[16];
 #pragma unroll
                     for (int m = 0; m < 16; ++m) v[m] = __uint_as_float(r[m]);
-                    if (n < p.N) i8_wide_store<TC>(p, m0 + c, n, tokens - c, sb, bias, v);
+                    i8_wide_store<TC>(p, m0 + c, n, tokens - c, scales[0], first, sb, bias, v);
+                    next_scales();
                 } else {
 #pragma unroll
                     for (int m = 0; m < 16; m += 4)
@@ -312,9 +342,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                            __uint_as_float(r[m + 2]), __uint_as_float(r[m + 3])));
                 }
             }
-            tc_before_sync();
-            __syncwarp();
-            if (lane == 0) wide_arrive(wide_at(d_empty, 0));
             if (!whole) {  // a share of a tile
                 __threadfence();
                 __syncwarp();
@@ -352,7 +379,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                 for (int m = 0; m < 16; ++m) sum[m] += w[m];
                             }
                         }
-                        if (n < p.N) i8_wide_store<TC>(p, m0 + c, n, tokens - c, sb, bias, sum);
+                        i8_wide_store<TC>(p, m0 + c, n, tokens - c, scales[0], first, sb, bias, sum);
+                        next_scales();
                     }
                 }
             }

@@ -172,8 +172,11 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 // Of a tile, at most: what the shares' places are made for.
 int64_t tile_tokens(int64_t M) { return M < tg::kI8Tokens ? up(M, 32) : tg::kI8Tokens; }
 
-// Fills in the tile's width and the division of the work with the least time, as plan_wide
-// of w4.cu does.
+// Fills in the tile's width and the division of the work with the least time.  Measured, on random
+// codes: a unit takes 2.4 ns per token, and 0.4 us at least (what B takes to come and be decoded);
+// the end of a tile 8 ns per token; sharing tiles 4 us + 60 ns per token (16384×8192 with 512 rows:
+// whole tiles on 64 of the 76 pairs 84 us, all units shared evenly 92; 4096×28672 with 256 rows,
+// where 16 tiles are too few, 94 and 66).
 void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
     q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
@@ -183,14 +186,14 @@ void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
     for (int32_t tokens = 32; tokens <= widest; tokens += 32) {
         const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
         const double mma = 0.0024 * tokens;
-        const double unit = mma < 0.43 ? 0.43 : mma;
+        const double unit = mma < 0.4 ? 0.4 : mma;
         for (const int32_t grain : {q->k_units, 1}) {
             const int64_t grains = tiles * q->k_units / grain;
             const int64_t clusters = grains < limit ? grains : limit;
             const int64_t most = (grains + clusters - 1) / clusters * grain;
-            double time = unit * static_cast<double>(most);
-            if (grain != q->k_units && (most % q->k_units != 0 || grains % clusters != 0))
-                time += 4.0 + 0.018 * tokens * (2.0 + static_cast<double>(q->k_units) / static_cast<double>(most));
+            double time = unit * static_cast<double>(most) +
+                          0.008 * tokens * static_cast<double>((most + q->k_units - 1) / q->k_units);
+            if (grain != q->k_units && (most % q->k_units != 0 || grains % clusters != 0)) time += 4.0 + 0.06 * tokens;
             if (time < least) {
                 least = time;
                 q->tokens = tokens;
