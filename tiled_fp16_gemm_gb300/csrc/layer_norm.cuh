@@ -196,15 +196,31 @@ __device__ __forceinline__ void ln_take(const T* src, F2 (&v)[4]) {
 // 8·CH·32 consecutive columns of a row for each of its warps, so that a thread's lie at fixed
 // distances.  VEC: a thread has CH runs of 8 neighbours (every row on 8 elements, cols a multiple
 // of 8); else every 32nd column.
+//
+// ALL: the warp has all of its columns, and nothing is asked of single ones (unaligned rows spend
+// as much time on that as on their values).
 template <int CH, bool VEC>
 struct LnCols {
     int first, cols;  // this thread's first column
+    bool all;
     __device__ __forceinline__ LnCols(int cols, int warp, int lane)
-        : first(warp * 256 * CH + (VEC ? 8 : 1) * lane), cols(cols) {}
+        : first(warp * 256 * CH + (VEC ? 8 : 1) * lane), cols(cols), all((warp + 1) * 256 * CH <= cols) {}
+    // f(ALL): a branch around all loads of a row at once, for the results of those inside a branch
+    // are waited for at its end
+    template <typename F>
+    __device__ __forceinline__ void either(F f) const {
+        if (!VEC && all)
+            f(std::true_type{});
+        else
+            f(std::false_type{});
+    }
     __device__ __forceinline__ static constexpr int at(int ch, int i) { return VEC ? 256 * ch + i : 32 * (8 * ch + i); }
-    __device__ __forceinline__ bool has(int ch, int i) const { return first < cols - at(ch, VEC ? 0 : i); }
+    template <bool ALL = false>
+    __device__ __forceinline__ bool has(int ch, int i) const {
+        return ALL || first < cols - at(ch, VEC ? 0 : i);
+    }
     // `row` is at this thread's first column, here and below
-    template <typename T>
+    template <bool ALL, typename T>
     __device__ __forceinline__ void load(const T* row, int ch, F2 (&v)[4]) const {
         if constexpr (VEC) {
             if (has(ch, 0)) {
@@ -216,11 +232,12 @@ struct LnCols {
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = f2(has(ch, 2 * i) ? op_to_float(row[at(ch, 2 * i)]) : 0.0f,
-                          has(ch, 2 * i + 1) ? op_to_float(row[at(ch, 2 * i + 1)]) : 0.0f);
+                v[i] = f2(has<ALL>(ch, 2 * i) ? op_to_float(row[at(ch, 2 * i)]) : 0.0f,
+                          has<ALL>(ch, 2 * i + 1) ? op_to_float(row[at(ch, 2 * i + 1)]) : 0.0f);
         }
     }
     // of a weight, which other rows read too; `none` where there is no weight
+    template <bool ALL>
     __device__ __forceinline__ void weight(const float* row, int ch, F2 (&v)[4], float none) const {
         if (row == nullptr) {
 #pragma unroll
@@ -228,10 +245,10 @@ struct LnCols {
         } else if constexpr (VEC) {
             if (has(ch, 0)) norm_take<float>(row + at(ch, 0), v);
         } else {
-            load(row, ch, v);
+            load<ALL>(row, ch, v);
         }
     }
-    template <typename T>
+    template <bool ALL = false, typename T>
     __device__ __forceinline__ void store(T* row, int ch, const F2 (&v)[4]) const {
         if constexpr (VEC) {
             if (!has(ch, 0)) return;
@@ -249,16 +266,17 @@ struct LnCols {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = f2_get(v[i]);
-                if (has(ch, 2 * i)) row[at(ch, 2 * i)] = op_round<T>(f.x);
-                if (has(ch, 2 * i + 1)) row[at(ch, 2 * i + 1)] = op_round<T>(f.y);
+                if (has<ALL>(ch, 2 * i)) row[at(ch, 2 * i)] = op_round<T>(f.x);
+                if (has<ALL>(ch, 2 * i + 1)) row[at(ch, 2 * i + 1)] = op_round<T>(f.y);
             }
         }
     }
     // v - m, and 0 where there is no column
+    template <bool ALL = false>
     __device__ __forceinline__ void less(int ch, float m, F2 (&v)[4]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[i] = f2_add(v[i], f2(has(ch, 2 * i) ? -m : 0.0f, has(ch, 2 * i + 1) ? -m : 0.0f));
+            v[i] = f2_add(v[i], f2(has<ALL>(ch, 2 * i) ? -m : 0.0f, has<ALL>(ch, 2 * i + 1) ? -m : 0.0f));
     }
 };
 
@@ -292,24 +310,25 @@ __global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<C
     for (int64_t row = int64_t{blockIdx.x} * groups + group; row < p.rows;
          row += int64_t{gridDim.x} * groups, turn ^= 1) {
         F2 v[CH][4];
-        const TX* x = static_cast<const TX*>(p.x) + row * p.ldx + c.first;
+        c.either([&](auto whole) {
+            constexpr bool ALL = decltype(whole)::value;
+            const TX* x = static_cast<const TX*>(p.x) + row * p.ldx + c.first;
 #pragma unroll
-        for (int ch = 0; ch < CH; ++ch) c.load(x, ch, v[ch]);
-        if (MODE != kLnRaw && p.r != nullptr) {
+            for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(x, ch, v[ch]);
+            if (MODE == kLnRaw || p.r == nullptr) return;
             const TR* rr = static_cast<const TR*>(p.r) + row * p.ldr + c.first;
             F2 r[CH][4];
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) c.load(rr, ch, r[ch]);
+            for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(rr, ch, r[ch]);
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[ch][i]);
-        }
-        if (MODE != kLnRaw && p.y != nullptr) {
+            if (p.y == nullptr) return;
             TR* y = static_cast<TR*>(p.y) + row * p.ldy + c.first;
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) c.store(y, ch, v[ch]);
-        }
+            for (int ch = 0; ch < CH; ++ch) c.template store<ALL>(y, ch, v[ch]);
+        });
         if (MODE != kLnRaw) {
             if (MODE == kLnH && p.h == nullptr) continue;
             F2 a = 0;
@@ -320,9 +339,12 @@ __global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<C
             const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
             F2 b = 0;
             a = 0;
+            c.either([&](auto whole) {
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) c.template less<decltype(whole)::value>(ch, m, v[ch]);
+            });
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
-                c.less(ch, m, v[ch]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     a = f2_add(a, v[ch][i]);
@@ -362,15 +384,18 @@ __global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<C
             const float* w_at = p.w != nullptr ? p.w + c.first : nullptr;
             const float* b_at = p.b != nullptr ? p.b + c.first : nullptr;
             TX* h = static_cast<TX*>(p.h) + row * p.ldh + c.first;
+            c.either([&](auto whole) {
+                constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                F2 w2[4], b2[4];
-                c.weight(w_at, ch, w2, 1.0f);
-                c.weight(b_at, ch, b2, 0.0f);
+                for (int ch = 0; ch < CH; ++ch) {
+                    F2 w2[4], b2[4];
+                    c.template weight<ALL>(w_at, ch, w2, 1.0f);
+                    c.template weight<ALL>(b_at, ch, b2, 0.0f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[ch][i] = f2_fma(f2_mul(f2_add(v[ch][i], o2), s2), w2[i], b2[i]);
-                if (MODE == kLnH) c.store(h, ch, v[ch]);
-            }
+                    for (int i = 0; i < 4; ++i) v[ch][i] = f2_fma(f2_mul(f2_add(v[ch][i], o2), s2), w2[i], b2[i]);
+                    if (MODE == kLnH) c.template store<ALL>(h, ch, v[ch]);
+                }
+            });
         }
         if constexpr (MODE != kLnH) {
             float size = 0.0f;
@@ -556,7 +581,7 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
     F2 w[CH][4], sum_w[CH][4], sum_b[CH][4];
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-        c.weight(p.w != nullptr ? p.w + c0 + c.first : nullptr, ch, w[ch], 1.0f);
+        c.template weight<false>(p.w != nullptr ? p.w + c0 + c.first : nullptr, ch, w[ch], 1.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (!c.has(ch, 2 * i)) w[ch][i] = 0;
