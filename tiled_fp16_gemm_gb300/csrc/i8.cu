@@ -115,7 +115,10 @@ FewPlan plan_few(const I8Params& p, const tg::OpDevice& dev) {
         const int64_t slice = (q.chunks + q.cluster - 1) / q.cluster;
         q.x_pitch = static_cast<int32_t>(slice * tg::kI8FewK * (NT > 1 ? 2 : 1) + 64);
         int64_t clusters = tiles < lim.clusters[i] ? tiles : lim.clusters[i];
-        for (q.stages = tg::kI8FewStages; q.stages >= 2; --q.stages) {
+        // (with few steps a shallow ring: then the next call's blocks find room beside this one's, and
+        // B comes to L2 meanwhile; one row of 4096×4096 5.4 us, with three stages 6.0)
+        const int64_t each = ((tiles + clusters - 1) / clusters * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps;
+        for (q.stages = each <= 6 ? 2 : tg::kI8FewStages; q.stages >= 2; --q.stages) {
             const int64_t fixed = 1024 + int64_t{tg::kI8FewWarps} * q.stages * tg::kI8FewStep + tg::kI8FewBars +
                                   p.M * q.x_pitch;
             // (a block keeps the sums of its tiles: very many rows of B take several waves)
@@ -131,7 +134,7 @@ FewPlan plan_few(const I8Params& p, const tg::OpDevice& dev) {
             const double steps = static_cast<double>((rounds * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps);
             const double time =
                 2.0 + static_cast<double>(waves) * (round * steps + 8e-6 * static_cast<double>(slice * tg::kI8FewK * p.M) +
-                                                    (q.cluster > 1 ? 1.1 : 0.0) + (q.stages < 3 ? 1.5 : 0.0));
+                                                    (q.cluster > 1 ? 1.1 : 0.0) + (q.stages < 3 && each > 6 ? 1.5 : 0.0));
             if (time < best.time && clusters * q.cluster <= tg::kOpMaxDim) {
                 best.time = time;
                 best.q = q;
