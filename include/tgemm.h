@@ -456,8 +456,8 @@ tg_status_t tg_layer_norm_i8(const tg_layer_norm_t* n, void* y, int64_t ldy, int
  *
  * (the exact quotient's; ±127 at most).  A row of zeros has scale 0 and codes 0.  A
  * row with a NaN or an infinity has scale NaN and codes 0, so that its products are
- * NaN.  x: device, rows × cols of `dtype`, any stride ≥ cols; codes, scale and errors
- * as tg_layer_norm_i8.
+ * NaN (and 0 behind a ReLU, as of any NaN).  x: device, rows × cols of `dtype`, any
+ * stride ≥ cols; codes, scale and errors as tg_layer_norm_i8.
  */
 tg_status_t tg_quantize_rows(int32_t dtype, const void* x, int64_t ldx, int8_t* codes, int64_t ldc,
                              float* scale, int64_t rows, int64_t cols, void* stream);
@@ -523,7 +523,8 @@ int64_t tg_gemm_i8_workspace(int64_t M, int64_t N, int64_t K);
  *          bias, activation or residual, C in fp16.
  * Sums     of whole numbers, exact up to 2^24 in size (up to 8 rows: always).  Beyond
  *          that, each of the K / 16 additions of the tensor cores may round the running
- *          sum in its 24th bit.
+ *          sum in its 24th bit.  What follows is fp32: the sum times Ascale, that times
+ *          Bscale, and so on, and C is rounded once.
  * workspace  device, 256-byte aligned, tg_gemm_i8_workspace(M, N, K) bytes at least; it
  *          holds nothing from one call to the next, and calls that may overlap on the GPU
  *          need one each.  NULL: a buffer that belongs to the (device, stream), grown on
@@ -644,10 +645,11 @@ void tg_debug_set_wait_timeout_ns(uint64_t ns);
 
 /* mode 1: the next persistent/skinny launch withholds its first
  * "accumulator ready" signal, so its epilogue waits out the timeout and the
- * kernel returns early with TG_ERR_TIMEOUT recorded.  (tg_gemm_w4's kernels
- * withhold their first fetch of codes instead; tg_norm_residual_backward, where
- * blocks share rows, one block's first sums.)  mode 0: off.  The
- * setting applies to exactly one launch. */
+ * kernel returns early with TG_ERR_TIMEOUT recorded.  (The kernels of tg_gemm_w4
+ * and tg_gemm_i8 withhold their first fetch of codes instead; those of
+ * tg_norm_residual_backward and tg_layer_norm_backward, where blocks share rows,
+ * one block's first sums.)  mode 0: off.  The setting applies to exactly one
+ * launch. */
 void tg_debug_inject(int32_t mode);
 
 /* The shape of the last tg_gemm_f16 / tg_gemm_bf16 / tg_gemm_ex launch made

@@ -17,9 +17,6 @@ using tg::LayerNormGradParams;
 using tg::LayerNormParams;
 using tg::max_clusters;
 using tg::misaligned;
-using tg::narrow;
-using tg::plan_rows;
-using tg::RowPlan;
 using tg::wide;
 
 constexpr int64_t kMaxCols = 131071;   // codes of a row: whole sums of gemm_i8 fit 32 bits
