@@ -74,31 +74,45 @@ tg_status_t launch_rows(const LayerNormParams& p, const tg::OpDevice& dev, cudaS
                      wide(p.w, 0, 4) && wide(p.b, 0, 4) && wide(p.y, p.ldy, sizeof(TR)) && wide(p.h, p.ldh, out);
     const int64_t cols = p.cols;
     auto warps = [&](int ch) { return (cols + 256 * ch - 1) / (256 * ch); };  // of a row
-    auto run = [&](auto ch, auto v, auto far) {
+    auto run = [&](auto ch, auto v, auto sm) {
         constexpr int CH = decltype(ch)::value;
         const int threads = static_cast<int>(warps(CH)) * 32;
         const int64_t each = (p.rows + dev.num_sms - 1) / dev.num_sms;
         const int64_t groups = threads > 32 ? 1 : each < 4 ? each : 4;  // rows of a block
         const int64_t blocks = (p.rows + groups - 1) / groups;
-        return launch(tg::tg_layer_norm_rows<TX, TR, CH, decltype(v)::value, MODE, decltype(far)::value>,
+        return launch(tg::tg_layer_norm_rows<TX, TR, CH, decltype(v)::value, MODE, decltype(sm)::value>,
                       dim3(static_cast<unsigned>(blocks)), static_cast<int>(threads * groups), 0, 1, s, p, threads);
     };
-    auto fits = [&](int ch) { return warps(ch) <= (vec && ch == 4 ? 12 : 16); };
+    // whether the SMs hold all rows with 512 threads each
+    auto few = [&](int n) { return p.rows * warps(n) * 32 <= 512 * int64_t{dev.num_sms}; };
+    // (16 warps of four runs leave an SM one block; few rows gain: 152×16384 6.7 us, 8.1 with eight)
+    auto fits = [&](int n) { return warps(n) <= (vec && n == 4 && !few(4) ? 12 : 16); };
     int ch = !vec || fits(4) ? 4 : 8;
     while (ch > 1 && (cols <= 128 * ch || (p.rows * warps(ch) < 8 * dev.num_sms && fits(ch / 2)))) ch /= 2;
-    std::false_type no;
+    // Threads of an SM, for which a kernel's registers are: in rows of four runs 640, and 512 of an
+    // fp32 stream, whose loads under way take more (8192×4096 bf16 48 us, 52 with 512; fp32 64, 66 with
+    // 640); else 1024, and 512 where that holds all rows (16×1024 2.2 us, 2.6; 64×8192 4.1, 4.8).
+    constexpr int kFour = sizeof(TR) == 4 ? 512 : 640;
     if (vec && fits(ch)) {
+        // Warps that have all of their columns (2050×1536 8.2 us with three of 512, 8.8 with two of
+        // 1024; 1200×768 4.3 and 4.7), where an SM does not hold fewer rows for it, or holds all
+        // (700×3584 6.2 us with four of 1024, 8.3 with seven of 512 in two waves).
+        auto held = [&](int n) { return (n > 2 ? kFour : 1024) / (32 * warps(n)); };  // rows, of an SM
+        while ((ch == 4 || ch == 2) && cols % (256 * ch) != 0 && cols % (128 * ch) == 0 && fits(ch / 2) &&
+               (held(ch / 2) >= held(ch) || p.rows <= held(ch / 2) * dev.num_sms))
+            ch /= 2;
         std::true_type v;
-        if (ch == 1) return run(Int<1>{}, v, no);
-        if (ch == 2) return run(Int<2>{}, v, no);
-        if (ch == 4) return run(Int<4>{}, v, no);
-        return run(Int<8>{}, v, no);
+        if (ch == 1) return few(1) ? run(Int<1>{}, v, Int<512>{}) : run(Int<1>{}, v, Int<1024>{});
+        if (ch == 2) return few(2) ? run(Int<2>{}, v, Int<512>{}) : run(Int<2>{}, v, Int<1024>{});
+        if (ch == 4) return few(4) ? run(Int<4>{}, v, Int<512>{}) : run(Int<4>{}, v, Int<kFour>{});
+        return run(Int<8>{}, v, Int<512>{});
     }
     if (!vec && warps(4) <= 32) {
-        if (warps(ch) > 16) return run(Int<4>{}, no, std::true_type{});
-        if (ch == 1) return run(Int<1>{}, no, no);
-        if (ch == 2) return run(Int<2>{}, no, no);
-        return run(Int<4>{}, no, no);
+        std::false_type v;
+        if (warps(ch) > 16) return run(Int<4>{}, v, Int<1024>{});  // (registers do not hold all)
+        if (ch == 1) return few(1) ? run(Int<1>{}, v, Int<512>{}) : run(Int<1>{}, v, Int<1024>{});
+        if (ch == 2) return few(2) ? run(Int<2>{}, v, Int<512>{}) : run(Int<2>{}, v, Int<1024>{});
+        return run(Int<4>{}, v, Int<512>{});
     }
     const int64_t most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_layer_norm_simple<TX, TR, MODE>,

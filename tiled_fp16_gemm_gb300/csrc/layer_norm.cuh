@@ -205,8 +205,9 @@ __device__ __forceinline__ void ln_take(const T* src, F2 (&v)[4]) {
 // distances.  VEC: a thread has CH runs of 8 neighbours (every row on 8 elements, cols a multiple
 // of 8); else every 32nd column.
 //
-// ALL: the warp has all of its columns, and nothing is asked of single ones (unaligned rows spend
-// as much time on that as on their values).
+// ALL: the warp has all of its columns, and nothing is asked of single ones.  Then the loads of
+// a row leave one after another (8192×4096 bf16 48 us, 52 with each asked for; 600×16384 17.7 and
+// 20.6), and unaligned rows do not spend as much time on the questions as on their values.
 template <int CH, bool VEC>
 struct LnCols {
     int first, cols;  // this thread's first column
@@ -217,7 +218,7 @@ struct LnCols {
     // are waited for at its end
     template <typename F>
     __device__ __forceinline__ void either(F f) const {
-        if (!VEC && all)
+        if (all)
             f(std::true_type{});
         else
             f(std::false_type{});
@@ -231,7 +232,7 @@ struct LnCols {
     template <bool ALL, typename T>
     __device__ __forceinline__ void load(const T* row, int ch, F2 (&v)[4]) const {
         if constexpr (VEC) {
-            if (has(ch, 0)) {
+            if (has<ALL>(ch, 0)) {
                 ln_take<T>(row + at(ch, 0), v);
             } else {
 #pragma unroll
@@ -251,7 +252,7 @@ struct LnCols {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = f2(none, none);
         } else if constexpr (VEC) {
-            if (has(ch, 0)) norm_take<float>(row + at(ch, 0), v);
+            if (has<ALL>(ch, 0)) norm_take<float>(row + at(ch, 0), v);
         } else {
             load<ALL>(row, ch, v);
         }
@@ -259,7 +260,7 @@ struct LnCols {
     template <bool ALL = false, typename T>
     __device__ __forceinline__ void store(T* row, int ch, const F2 (&v)[4]) const {
         if constexpr (VEC) {
-            if (!has(ch, 0)) return;
+            if (!has<ALL>(ch, 0)) return;
             T* p = row + at(ch, 0);
             if constexpr (sizeof(T) == 4) {
                 const float2 a = f2_get(v[0]), b = f2_get(v[1]), d = f2_get(v[2]), e = f2_get(v[3]);
@@ -288,17 +289,10 @@ struct LnCols {
     }
 };
 
-// Threads of a block at most, and how many such blocks an SM holds: what registers allow.
-// (Unaligned rows of more than 16384 columns: 1024 threads, whose registers do not hold all.)
-template <int CH, bool VEC, bool LONG>
-struct LnShape {
-    static constexpr int kThreads = LONG ? 1024 : VEC && CH == 4 ? 640 : 512;
-    static constexpr int kBlocks = CH < 4 ? 2 : 1;
-};
-
-// `threads`: of a row, 32 (a block has several rows) or all of the block.
-template <typename TX, typename TR, int CH, bool VEC, int MODE, bool LONG>
-__global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<CH, VEC, LONG>::kBlocks))
+// `threads`: of a row, 32 (a block has several rows) or all of the block.  SM: of an SM, what
+// registers are for.
+template <typename TX, typename TR, int CH, bool VEC, int MODE, int SM>
+__global__ void __launch_bounds__(SM, 1)
     tg_layer_norm_rows(const LayerNormParams p, int threads) {
     __shared__ float stat[2][3][32];  // of the warps: mean, Σd, Σd²; a row's are read while the next one's come
     __shared__ uint32_t most[2][32];
@@ -407,13 +401,17 @@ __global__ void __launch_bounds__((LnShape<CH, VEC, LONG>::kThreads), (LnShape<C
         }
         if constexpr (MODE != kLnH) {
             float size = 0.0f;
+            c.either([&](auto whole) {
+                constexpr bool ALL = decltype(whole)::value;
 #pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
+                for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = f2_get(v[ch][i]);
-                    size = ln_most(size, c.has(ch, 2 * i) ? f.x : 0.0f, c.has(ch, 2 * i + 1) ? f.y : 0.0f);
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = f2_get(v[ch][i]);
+                        size = ln_most(size, c.template has<ALL>(ch, 2 * i) ? f.x : 0.0f,
+                                       c.template has<ALL>(ch, 2 * i + 1) ? f.y : 0.0f);
+                    }
+            });
             uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(size) & 0x7fffffffu);
             if (!alone) {
                 if (lane == 0) most[turn][warp] = u;
