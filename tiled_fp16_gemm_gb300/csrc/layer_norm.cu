@@ -245,6 +245,10 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             const int64_t each = (a->rows + dev.num_sms - 1) / dev.num_sms;
             groups = split > 1 ? 1 : fit / warps < each ? fit / warps : static_cast<int>(each);
             most = dev.num_sms;
+            // two rows of an SM in two blocks, where that is not too many shares (160×1024 5.7 us, 6.7 with
+            // two groups in a block; 256×1024 5.9 and 7.4; 256×4096 10.0 and 9.3)
+            if (groups == 2 && each == 2 && (a->rows <= 160 || (a->rows <= 256 && cols <= 1024)))
+                groups = 1, most = 2 * dev.num_sms;
         }
         const size_t smem = static_cast<size_t>(ring) * groups * warps;
         if (rows_ring && split > 1) {
@@ -283,8 +287,14 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             st = vec ? run(tg::tg_layer_norm_grad_rows<TX, TR, true, false>)
                      : run(tg::tg_layer_norm_grad_rows<TX, TR, false, false>);
         if (st != TG_OK || (q.dw == nullptr && q.db == nullptr)) return st;
-        return launch(tg::tg_layer_norm_grad_sum, dim3(static_cast<unsigned>((cols + 31) / 32), 2), 512, 0, 1, s, q,
-                      blocks);
+        // long rows: fewer and wider blocks (50×16384 11.0 us, 13.8 with 32 columns; 500×12001 37.6, 39.4;
+        // up to 9000 columns there is no difference)
+        auto sum = [&](auto kernel, int columns) {
+            return launch(kernel, dim3(static_cast<unsigned>((cols + columns - 1) / columns), 2), 1024, 0, 1, s, q,
+                          blocks);
+        };
+        return cols <= 64 * dev.num_sms ? sum(tg::tg_layer_norm_grad_sum<1>, 32)
+                                        : sum(tg::tg_layer_norm_grad_sum<4>, 128);
     });
 }
 

@@ -458,10 +458,11 @@ __global__ void __launch_bounds__(SM, 1)
 // MULTI: the `split` blocks of a cluster share their rows, `part` columns each, and exchange
 // their means and sums: for rows of more columns than a block's threads have in registers.
 //
-// Measured: 8192×4096 bf16 70 us (5.7 TB/s), on an fp32 stream 109 us; 8192×1024 27 us, 2048×8192 43
-// us, 2048×16384 100 us; unaligned, 2050×1537 on an fp32 stream 25 us, 1021×5119 30 us; 256×1024 8 us,
-// of which the sum of the shares is some 3.  Aligned rows are bound by memory, unaligned ones by the
-// issue of single-value accesses, rows that blocks share by their exchanges.
+// Measured: 8192×4096 bf16 67 us (6.0 TB/s), on an fp32 stream 107 us; 8192×1024 24 us, 2048×8192 40
+// us, 600×16384 34 us; unaligned, 2050×1537 on an fp32 stream 22 us, 1021×5119 27 us; 256×1024 5.9 us.
+// The column sums (a block's share, the second launch) are 2 to 5 us of each.  Aligned rows are bound
+// by memory, unaligned ones by the issue of single-value accesses, rows that blocks share by their
+// exchanges.  (The groups' sums joined by the first group alone, one sum after the other: 2 us more.)
 
 constexpr int kLnGradWarps = 16;
 constexpr int kLnGradCols = 512;  // of a warp
@@ -512,9 +513,10 @@ struct LnInput {
             }
         }
     }
+    template <bool ALL>
     __device__ __forceinline__ void get(const Cols& c, int offset, int64_t row, int ch, int lane, F2 (&v)[4]) const {
         const unsigned char* s = place + offset;
-        if (base == nullptr || (VEC && !c.has(ch, 0))) {
+        if (base == nullptr || (VEC && !c.template has<ALL>(ch, 0))) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = 0;
         } else if constexpr (!VEC) {
@@ -522,8 +524,8 @@ struct LnInput {
                              s + (reinterpret_cast<uintptr_t>(base + row * ld + first) & 15)) + lane;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = f2(c.has(ch, 2 * i) ? op_to_float(t[c.at(ch, 2 * i)]) : 0.0f,
-                          c.has(ch, 2 * i + 1) ? op_to_float(t[c.at(ch, 2 * i + 1)]) : 0.0f);
+                v[i] = f2(c.template has<ALL>(ch, 2 * i) ? op_to_float(t[c.at(ch, 2 * i)]) : 0.0f,
+                          c.template has<ALL>(ch, 2 * i + 1) ? op_to_float(t[c.at(ch, 2 * i + 1)]) : 0.0f);
         } else if constexpr (kPieces == 2) {
             s += ch * 1024;
             const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(s + 16 * piece(2 * lane));
@@ -601,159 +603,186 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
     }
 
     static_assert(kLnGradStages == 2, "a row's stage is its turn");
-    for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();
-        const int at = turn * kStage;
-        F2 v[CH][4];
-        float s = 0.0f, off = 0.0f, m1 = 0.0f, m2 = 0.0f;  // off: mu - m
-        if (has_dh) {
-            F2 a = 0;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                in_x.get(c, at, row, ch, lane, v[ch]);
-                if (in_r.base != nullptr) {
-                    F2 r[4];
-                    in_r.get(c, at, row, ch, lane, r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
-            }
-            const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
-            F2 b[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                F2 dh[4];
-                in_dh.get(c, at, row, ch, lane, dh);
-                c.less(ch, m, v[ch]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 dn = f2_mul(dh[i], w[ch][i]);
-                    b[0] = f2_add(b[0], v[ch][i]);
-                    b[1] = f2_fma(v[ch][i], v[ch][i], b[1]);
-                    b[2] = f2_add(b[2], dn);
-                    b[3] = f2_fma(dn, v[ch][i], b[3]);
-                }
-            }
-            // Four sums at once: 8 lanes for each.
-            const bool b4 = lane & 16, b3 = lane & 8;
-            const float s0 = f2_sum(b[0]), s1 = f2_sum(b[1]), s2 = f2_sum(b[2]), s3 = f2_sum(b[3]);
-            const float e = (b4 ? s2 : s0) + __shfl_xor_sync(0xffffffffu, b4 ? s0 : s2, 16);
-            const float f = (b4 ? s3 : s1) + __shfl_xor_sync(0xffffffffu, b4 ? s1 : s3, 16);
-            float t = (b3 ? f : e) + __shfl_xor_sync(0xffffffffu, b3 ? e : f, 8);  // sum lane / 8
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            float mean, var, p1, p2;  // of the block: mean - m, Σ (v - mean)², Σ dn, Σ dn (v - mean)
-            if (warps == 1) {
-                const float d1 = __shfl_sync(0xffffffffu, t, 0), d2 = __shfl_sync(0xffffffffu, t, 8);
-                mean = d1 * here_inv;
-                var = d2 - mean * d1;
-                p1 = __shfl_sync(0xffffffffu, t, 16);
-                p2 = __shfl_sync(0xffffffffu, t, 24) - mean * p1;
-                off = mean;
-                if (MULTI) mean += m;
-            } else {
-                float* r = &red[turn][0][group * warps];
-                if ((lane & 7) == 0) r[(1 + (lane >> 3)) * kLnGradWarps + warp] = t;
-                if (lane == 0) r[warp] = m;
-                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
-                const bool has = u < warps;
-                const float m0 = r[0];
-                const float mu = has ? r[u] - m0 : 0.0f, d1 = has ? r[kLnGradWarps + u] : 0.0f;
-                const float dn = has ? r[3 * kLnGradWarps + u] : 0.0f;
-                // the lower lanes take one sum, the upper ones another
-                float z = b4 ? dn : fmaf(count, mu, d1);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                const float shift = __shfl_sync(0xffffffffu, z, 0) * here_inv;
-                p1 = __shfl_sync(0xffffffffu, z, 16);
-                const float gu = mu - shift;
-                z = !has ? 0.0f
-                    : b4 ? fmaf(gu, dn, r[4 * kLnGradWarps + u])
-                         : fmaf(gu, fmaf(count, gu, 2.0f * d1), r[2 * kLnGradWarps + u]);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-                var = __shfl_sync(0xffffffffu, z, 0);
-                p2 = __shfl_sync(0xffffffffu, z, 16);
-                off = shift - (m - m0);
-                mean = m0 + shift;
-            }
-            if constexpr (MULTI) {
-                const float send[4] = {mean, var, p1, p2};
-                const float* got = peers.exchange(send);
-                const float from = got[0];
-                auto columns = [&](int b) {
-                    return static_cast<float>(min(static_cast<int>(p.cols) - b * part, part));
-                };
-                float shift = 0.0f;
-                for (int b = 1; b < split; ++b) shift = fmaf(columns(b), got[8 * b] - from, shift);
-                shift *= inv;
-                var = p1 = p2 = 0.0f;
-                for (int b = 0; b < split; ++b) {
-                    const float g = got[8 * b] - from - shift;
-                    var += fmaf(columns(b) * g, g, got[8 * b + 1]);
-                    p1 += got[8 * b + 2];
-                    p2 += fmaf(g, got[8 * b + 2], got[8 * b + 3]);
-                }
-                off += shift - (mean - from);
-            }
-            s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
-            if (!(var == var)) s = var;  // (fmaxf would turn a NaN into 0)
-            m1 = p1 * inv;
-            m2 = p2 * inv * s;
-        }
-        const F2 s2 = f2(s, s), o2 = f2(-off, -off), m1n = f2(-m1, -m1), m2n = f2(-m2, -m2);
-#pragma unroll
-        for (int ch = 0; ch < CH; ++ch) {
-            F2 d[4];
-            in_dy.get(c, at, row, ch, lane, d);
+    c.either([&](auto whole) {  // (the barrier inside counts warps, wherever they are in the code)
+        constexpr bool ALL = decltype(whole)::value;
+        for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+            const int at = turn * kStage;
+            F2 v[CH][4];
+            float s = 0.0f, off = 0.0f, m1 = 0.0f, m2 = 0.0f;  // off: mu - m
             if (has_dh) {
-                F2 dh[4];
-                in_dh.get(c, at, row, ch, lane, dh);
+                F2 a = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 n = f2_mul(f2_add(v[ch][i], o2), s2);
-                    sum_b[ch][i] = f2_add(sum_b[ch][i], dh[i]);
-                    sum_w[ch][i] = f2_fma(dh[i], n, sum_w[ch][i]);
-                    d[i] = f2_fma(s2, f2_fma(n, m2n, f2_fma(dh[i], w[ch][i], m1n)), d[i]);
+                for (int ch = 0; ch < CH; ++ch) {
+                    in_x.template get<ALL>(c, at, row, ch, lane, v[ch]);
+                    if (in_r.base != nullptr) {
+                        F2 r[4];
+                        in_r.template get<ALL>(c, at, row, ch, lane, r);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
                 }
+                const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
+                F2 b[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    F2 dh[4];
+                    in_dh.template get<ALL>(c, at, row, ch, lane, dh);
+                    c.template less<ALL>(ch, m, v[ch]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 dn = f2_mul(dh[i], w[ch][i]);
+                        b[0] = f2_add(b[0], v[ch][i]);
+                        b[1] = f2_fma(v[ch][i], v[ch][i], b[1]);
+                        b[2] = f2_add(b[2], dn);
+                        b[3] = f2_fma(dn, v[ch][i], b[3]);
+                    }
+                }
+                // Four sums at once: 8 lanes for each.
+                const bool b4 = lane & 16, b3 = lane & 8;
+                const float s0 = f2_sum(b[0]), s1 = f2_sum(b[1]), s2 = f2_sum(b[2]), s3 = f2_sum(b[3]);
+                const float e = (b4 ? s2 : s0) + __shfl_xor_sync(0xffffffffu, b4 ? s0 : s2, 16);
+                const float f = (b4 ? s3 : s1) + __shfl_xor_sync(0xffffffffu, b4 ? s1 : s3, 16);
+                float t = (b3 ? f : e) + __shfl_xor_sync(0xffffffffu, b3 ? e : f, 8);  // sum lane / 8
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                float mean, var, p1, p2;  // of the block: mean - m, Σ (v - mean)², Σ dn, Σ dn (v - mean)
+                if (warps == 1) {
+                    const float d1 = __shfl_sync(0xffffffffu, t, 0), d2 = __shfl_sync(0xffffffffu, t, 8);
+                    mean = d1 * here_inv;
+                    var = d2 - mean * d1;
+                    p1 = __shfl_sync(0xffffffffu, t, 16);
+                    p2 = __shfl_sync(0xffffffffu, t, 24) - mean * p1;
+                    off = mean;
+                    if (MULTI) mean += m;
+                } else {
+                    float* r = &red[turn][0][group * warps];
+                    if ((lane & 7) == 0) r[(1 + (lane >> 3)) * kLnGradWarps + warp] = t;
+                    if (lane == 0) r[warp] = m;
+                    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(32 * warps) : "memory");
+                    const bool has = u < warps;
+                    const float m0 = r[0];
+                    const float mu = has ? r[u] - m0 : 0.0f, d1 = has ? r[kLnGradWarps + u] : 0.0f;
+                    const float dn = has ? r[3 * kLnGradWarps + u] : 0.0f;
+                    // the lower lanes take one sum, the upper ones another
+                    float z = b4 ? dn : fmaf(count, mu, d1);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                    const float shift = __shfl_sync(0xffffffffu, z, 0) * here_inv;
+                    p1 = __shfl_sync(0xffffffffu, z, 16);
+                    const float gu = mu - shift;
+                    z = !has ? 0.0f
+                        : b4 ? fmaf(gu, dn, r[4 * kLnGradWarps + u])
+                             : fmaf(gu, fmaf(count, gu, 2.0f * d1), r[2 * kLnGradWarps + u]);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                    var = __shfl_sync(0xffffffffu, z, 0);
+                    p2 = __shfl_sync(0xffffffffu, z, 16);
+                    off = shift - (m - m0);
+                    mean = m0 + shift;
+                }
+                if constexpr (MULTI) {
+                    const float send[4] = {mean, var, p1, p2};
+                    const float* got = peers.exchange(send);
+                    const float from = got[0];
+                    auto columns = [&](int b) {
+                        return static_cast<float>(min(static_cast<int>(p.cols) - b * part, part));
+                    };
+                    float shift = 0.0f;
+                    for (int b = 1; b < split; ++b) shift = fmaf(columns(b), got[8 * b] - from, shift);
+                    shift *= inv;
+                    var = p1 = p2 = 0.0f;
+                    for (int b = 0; b < split; ++b) {
+                        const float g = got[8 * b] - from - shift;
+                        var += fmaf(columns(b) * g, g, got[8 * b + 1]);
+                        p1 += got[8 * b + 2];
+                        p2 += fmaf(g, got[8 * b + 2], got[8 * b + 3]);
+                    }
+                    off += shift - (mean - from);
+                }
+                s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
+                if (!(var == var)) s = var;  // (fmaxf would turn a NaN into 0)
+                m1 = p1 * inv;
+                m2 = p2 * inv * s;
             }
-            if (q.dx != nullptr) c.store(static_cast<TX*>(q.dx) + row * q.lddx + c0 + c.first, ch, d);
-            if (q.dr != nullptr) c.store(static_cast<TR*>(q.dr) + row * q.lddr + c0 + c.first, ch, d);
+            const F2 s2 = f2(s, s), o2 = f2(-off, -off), m1n = f2(-m1, -m1), m2n = f2(-m2, -m2);
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                F2 d[4];
+                in_dy.template get<ALL>(c, at, row, ch, lane, d);
+                if (has_dh) {
+                    F2 dh[4];
+                    in_dh.template get<ALL>(c, at, row, ch, lane, dh);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const F2 n = f2_mul(f2_add(v[ch][i], o2), s2);
+                        sum_b[ch][i] = f2_add(sum_b[ch][i], dh[i]);
+                        sum_w[ch][i] = f2_fma(dh[i], n, sum_w[ch][i]);
+                        d[i] = f2_fma(s2, f2_fma(n, m2n, f2_fma(dh[i], w[ch][i], m1n)), d[i]);
+                    }
+                }
+                if (q.dx != nullptr) c.template store<ALL>(static_cast<TX*>(q.dx) + row * q.lddx + c0 + c.first, ch, d);
+                if (q.dr != nullptr) c.template store<ALL>(static_cast<TR*>(q.dr) + row * q.lddr + c0 + c.first, ch, d);
+            }
+            __syncwarp();  // all lanes have read the stage, which is filled again
+            fetch(at);
         }
-        __syncwarp();  // all lanes have read the stage, which is filled again
-        fetch(at);
-    }
+    });
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
     // The groups' sums, in their order, to the block's share.
-    auto join = [&](F2 (&v)[CH][4], float* share) {
-        if (share == nullptr) return;  // (the same for the whole grid)
-        F2* all = reinterpret_cast<F2*>(ln_ring);
-        if (groups > 1) {
-            __syncthreads();
-            if (group > 0)
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        all[((group - 1) * 8 + 4 * ch + i) * 32 * warps + 32 * warp + lane] = v[ch][i];
-            __syncthreads();
-        }
-        if (group > 0) return;
+    float* const share_w = q.ws_w != nullptr ? q.ws_w + block * p.cols + c0 : nullptr;
+    float* const share_b = q.ws_b != nullptr ? q.ws_b + block * p.cols + c0 : nullptr;
+    if (groups == 1) {
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
-            for (int g = 1; g < groups; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[ch][i] = f2_add(v[ch][i], all[((g - 1) * 8 + 4 * ch + i) * 32 * warps + 32 * warp + lane]);
-            c.store(share + block * p.cols + c0 + c.first, ch, v[ch]);
+            if (share_w != nullptr) c.store(share_w + c.first, ch, sum_w[ch]);
+            if (share_b != nullptr) c.store(share_b + c.first, ch, sum_b[ch]);
         }
-    };
-    join(sum_w, q.ws_w);
-    join(sum_b, q.ws_b);
+    } else if (share_w != nullptr || share_b != nullptr) {
+        // (4 KB of each warp, whose ring had 8)
+        float* const all = reinterpret_cast<float*>(ln_ring);
+        const int width = kLnGradCols * warps;
+        __syncthreads();  // all have read their rings
+        auto keep = [&](float* to, int ch, const F2 (&v)[4]) {
+            if constexpr (VEC) {
+                ulonglong2* at = reinterpret_cast<ulonglong2*>(to + c.at(ch, 0));
+                at[0] = make_ulonglong2(v[0], v[1]);
+                at[1] = make_ulonglong2(v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = f2_get(v[i]);
+                    to[c.at(ch, 2 * i)] = f.x;
+                    to[c.at(ch, 2 * i + 1)] = f.y;
+                }
+            }
+        };
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+            keep(all + 2 * group * width + c.first, ch, sum_w[ch]);
+            keep(all + (2 * group + 1) * width + c.first, ch, sum_b[ch]);
+        }
+        __syncthreads();
+        const int threads = blockDim.x;
+        for (int which = share_w != nullptr ? 0 : 1; which < (share_b != nullptr ? 2 : 1); ++which) {
+            float* const share = which == 0 ? share_w : share_b;
+            for (int col = threadIdx.x; col < cols; col += 4 * threads) {  // four under way at a time
+                const float* at = all + which * width + col;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int g = 0; g < groups; ++g, at += 2 * width)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (col + k * threads < cols) sum[k] += at[k * threads];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (col + k * threads < cols) share[col + k * threads] = sum[k];
+            }
+        }
+    }
     peers.end();
 }
 
@@ -870,32 +899,47 @@ __global__ void __launch_bounds__(256) tg_layer_norm_grad_simple(const LayerNorm
     }
 }
 
-// The column sums of the blocks' shares, in the order of the blocks: blockIdx.y 0: dw, 1: db.
-// 32 columns per block, 16 warps with every 16th share each, 8 of them under way at a time.
-__global__ void __launch_bounds__(512) tg_layer_norm_grad_sum(const LayerNormGradParams q, int64_t blocks) {
-    __shared__ float part[16][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+// The column sums of the blocks' shares, in a fixed order: blockIdx.y 0: dw, 1: db.  32·G columns
+// per block, 32 warps with every 32nd share each, 8 values of a thread under way at a time: with G
+// = 1 those of 256 shares.  (16 warps with every 16th share, and 64-bit addresses: 2 us more.)
+template <int G>
+__global__ void __launch_bounds__(1024) tg_layer_norm_grad_sum(const LayerNormGradParams q, int blocks) {
+    constexpr int kAhead = 8 / G;
+    __shared__ float part[32][32 * G + 1];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, cols = static_cast<int>(q.n.cols);
+    const int c0 = blockIdx.x * 32 * G, here = cols - c0 - lane;  // columns from this thread's first on
+    const float* src = blockIdx.y == 0 ? q.ws_w : q.ws_b;
     op_release_next();
     op_wait_previous();
-    const int64_t c = int64_t{blockIdx.x} * 32 + lane;
-    const float* src = blockIdx.y == 0 ? q.ws_w : q.ws_b;
     if (src == nullptr) return;
-    float s = 0.0f;
-    if (c < q.n.cols) {
-        for (int64_t k = w; k < blocks; k += 128) {
-            float v[8];
+    float s[G];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k + 16 * i < blocks ? src[(k + 16 * i) * q.n.cols + c] : 0.0f;
+    for (int g = 0; g < G; ++g) s[g] = 0.0f;
+    const float* at = src + (w * cols + c0 + lane);  // (42 million elements at most)
+    const int step = 32 * cols;
+    for (int k = w; k < blocks; k += 32 * kAhead, at += kAhead * step) {
+        float v[kAhead][G];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += v[i];
-        }
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                v[i][g] = 0.0f;
+                if (k + 32 * i < blocks && 32 * g < here) v[i][g] = at[i * step + 32 * g];
+            }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g) s[g] += v[i][g];
     }
-    part[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && c < q.n.cols) {
 #pragma unroll
-        for (int k = 1; k < 16; ++k) s += part[k][lane];
-        (blockIdx.y == 0 ? q.dw : q.db)[c] = s;
+    for (int g = 0; g < G; ++g) part[w][32 * g + lane] = s[g];
+    __syncthreads();
+    // warp w: columns w, w + 32, ... of them
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float sum = ln_warp_sum(part[lane][32 * g + w]);
+        const int c = c0 + 32 * g + w;
+        if (lane == 0 && c < cols) (blockIdx.y == 0 ? q.dw : q.db)[c] = sum;
     }
 }
 
