@@ -215,8 +215,12 @@ __global__ void __launch_bounds__(kI8FewThreads, 1)
                     if (k + 16 <= p.K)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(op_smem(to)), "l"(a + k)
                                      : "memory");
+                    else if (k < p.K)  // zeros past the end (single bytes: 7 tokens of K = 4099 1.4 us more)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(op_smem(to)), "l"(a + k),
+                                     "r"(static_cast<int>(p.K - k))
+                                     : "memory");
                     else
-                        *reinterpret_cast<uint4*>(to) = i8_bytes(a, k, p.K);
+                        *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
                 }
         } else {
             // four pieces of a thread under way at a time
