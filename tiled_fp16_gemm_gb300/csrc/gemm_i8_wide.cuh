@@ -10,17 +10,20 @@
 // into tensor memory; the pair of blocks of a cluster multiplies 256 rows of B by up to 256
 // tokens.  Roles of a block's 24 warps, as there: 0 fetches B, 2 this block's half of the
 // tokens, 1 of the even block issues the MMAs, 8-19 decode, 4-7 and 20-23 write C.  The
-// clusters have whole tiles, or share all units evenly: then each block leaves its sums of a
-// shared tile in the workspace, and the last one to come adds all of them in the order of k.
+// clusters have whole tiles, equal parts of a tile, or even runs of all units.  Of a shared tile
+// each adds its sums to 32-bit ones in the workspace, and the last one to come writes C.  These are
+// whole numbers (and stay so where the accumulator rounds in its 24th bit), so their order is
+// free, and none passes 2^31: an addition that rounds up, by 128 at most, has a product in it that is
+// no multiple of 128, so 255 below the largest.  (Each cluster's sums left in a place of their own,
+// for the last one to read: 1024×8192 with 128 rows 22 us, now 14; 4096×28672 43, now 37.)
 //
 // Measured, bf16 results, random codes (they draw more power than zeros: 512 rows 84 to 88 us where a
 // constant weight takes 80): 16384×8192 with 64 / 128 / 256 / 512 / 1024 rows 32 / 35 / 48 / 86 / 166 us,
-// 28672×4096 33 / 37 / 51 / 75 / 139, 1024×1024 with 128 to 512 rows 9.  A unit takes 0.62 us with 256
+// 28672×4096 33 / 37 / 51 / 75 / 139, 4096×4096 14 / 16 / 21, 1024×1024 with 128 to 512 rows 9.  A unit takes 0.62 us with 256
 // tokens (0.54 at full clocks), bound by the MMAs; with few tokens the blocks fetch B at 5.5 TB/s,
 // and 8 us go to two launches, the start and the end.  The C warps have what the epilogue needs
 // before the sums are there, and give the accumulator back when they have read it, before they
-// have stored: 512 rows of 28672×4096 73 us instead of 84.  Registers are full (80): a variant with
-// the last share taken straight from the accumulator spilled and was slower.
+// have stored: 512 rows of 28672×4096 73 us instead of 84.  Registers are full (80).
 #pragma once
 
 #include "gemm_i8.cuh"
@@ -51,21 +54,34 @@ struct I8Wide {
     int32_t m_tiles;
     int32_t k_units;
     int64_t units;       // in all: (row blocks / cluster) · m_tiles · k_units
-    int32_t grain;       // units that stay together: k_units (whole tiles) or 1
+    int32_t parts;       // clusters of a tile, each with a run of its units (clusters = tiles · parts); 0:
+    int32_t grain;       // the clusters have even runs of all units, of k_units (whole tiles) or 1 at least
     int32_t clusters;
-    float* slots;        // two per block: the sums of its first and last tile
+    int32_t* sums;       // of the shared tiles, zeroed by tg_i8_expand: 128 rows for each token and block
+    int32_t by_tile;     // the tiles' places: their own numbers, else those of their first clusters
     uint32_t* counters;  // eight per block, zeroed by tg_i8_expand
 };
 
-// A as fp16 in rows of `ldo` (a multiple of 128), zero past column K; and the counters zeroed.
+// A cluster's first unit.
+__device__ __forceinline__ int64_t i8_first(const I8Wide& q, int cluster) {
+    if (q.parts == 0) return tc_first(q.units / q.grain, q.clusters, cluster) * q.grain;
+    const int tile = cluster / q.parts;
+    return int64_t{tile} * q.k_units + tc_first(q.k_units, q.parts, cluster - tile * q.parts);
+}
+
+// A as fp16 in rows of `ldo` (a multiple of 128), zero past column K; and the counters and `zeros` 16
+// bytes of the shared tiles' sums zeroed.
 __global__ void __launch_bounds__(256)
     tg_i8_expand(const int8_t* __restrict__ A, int64_t lda, int64_t M, int64_t K, uint16_t* __restrict__ out,
-                 int64_t ldo, uint32_t* counters) {
+                 int64_t ldo, uint32_t* counters, uint4* sums, int64_t zeros) {
     op_wait_previous();
     op_release_next();
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int i = threadIdx.x; i < kI8CounterBytes / 4; i += 256) counters[i] = 0;
     const int64_t c = int64_t{blockIdx.x} * 256 + threadIdx.x;
+    const int64_t threads = int64_t{gridDim.x} * gridDim.y * 256;
+    for (int64_t i = int64_t{blockIdx.y} * gridDim.x * 256 + c; i < zeros; i += threads)
+        sums[i] = make_uint4(0, 0, 0, 0);
     if (16 * c >= ldo) return;
     const bool wide = (reinterpret_cast<uintptr_t>(A) & 15) == 0 && lda % 16 == 0 && 16 * c + 16 <= K;
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
@@ -158,10 +174,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     constexpr uint32_t tmem = 0;
     constexpr uint32_t d_cols = tmem + 256;
 
-    const int64_t grains = q.units / q.grain;
-    const int64_t u0 = tc_first(grains, q.clusters, cluster_no) * q.grain;
-    const int n_units =
-        static_cast<int>(tc_first(grains, q.clusters, cluster_no + 1) * q.grain - u0);
+    const int64_t u0 = i8_first(q, cluster_no);
+    const int n_units = static_cast<int>(i8_first(q, cluster_no + 1) - u0);
     int64_t tile = u0 / q.k_units;
     int kb = static_cast<int>(u0 - tile * q.k_units);
     // the tile's place among the row blocks and the blocks of tokens, carried along: a 64-bit
@@ -293,7 +307,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int quarter = warp & 3, set = warp < 8 ? 0 : 1;
         const uint32_t row = 32 * quarter + lane;
         const uint32_t at = d_cols + (static_cast<uint32_t>(32 * quarter) << 16);
-        const int64_t slot = int64_t{q.tokens} * kTcRows;
         auto release = [&] {  // the sums have been read
             tc_before_sync();
             __syncwarp();
@@ -331,7 +344,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             // (a barrier of its own: a parity says nothing of a phase further off than one)
             if (!wait(d_full, tiles++ & 1)) break;
             tc_after_sync();
-            float* mine = q.slots + (2 * int64_t{blockIdx.x} + (kb0 > 0 ? 0 : 1)) * slot + row * 4;
+            int head = 0, tail = 0;  // of the clusters that share the tile
+            int32_t* sums = nullptr;
+            if (!whole) {
+                if (q.parts > 0) {
+                    head = static_cast<int>(tile) * q.parts;
+                    tail = head + q.parts - 1;
+                } else {
+                    head = static_cast<int>(tc_block_of(q.units, q.clusters, tile * q.k_units));
+                    tail = static_cast<int>(tc_block_of(q.units, q.clusters, (tile + 1) * q.k_units - 1));
+                }
+                const int place = q.by_tile ? static_cast<int>(tile) : head;
+                sums = q.sums + int64_t{place * kWideCluster + rank} * q.tokens * kTcRows + row;
+            }
             if (16 * set >= tokens) release();  // (no tokens for this warp)
             for (int c = 16 * set; c < tokens; c += 32) {
                 uint32_t r[16];
@@ -345,19 +370,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     next_scales();
                 } else {
 #pragma unroll
-                    for (int m = 0; m < 16; m += 4)
-                        __stcg(reinterpret_cast<float4*>(mine + (c + m) * kTcRows),
-                               make_float4(__uint_as_float(r[m]), __uint_as_float(r[m + 1]),
-                                           __uint_as_float(r[m + 2]), __uint_as_float(r[m + 3])));
+                    for (int m = 0; m < 16; ++m)
+                        asm volatile("red.relaxed.gpu.global.add.s32 [%0], %1;" ::"l"(sums + (c + m) * kTcRows),
+                                     "r"(__float2int_rn(__uint_as_float(r[m])))
+                                     : "memory");
                 }
             }
             if (!whole) {  // a share of a tile
-                __threadfence();
                 __syncwarp();
-                const int head = static_cast<int>(tc_block_of(q.units, q.clusters, tile * q.k_units));
-                const int tail = static_cast<int>(tc_block_of(q.units, q.clusters, (tile + 1) * q.k_units - 1));
                 uint32_t before = 0;
-                if (lane == 0) {
+                if (lane == 0) {  // (its release and acquire are those of the warp, by the barriers around)
                     uint32_t* count = q.counters + 8 * (head * kWideCluster + rank) + 4 * set + quarter;
                     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
                                  : "=r"(before)
@@ -365,30 +387,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                  : "memory");
                 }
                 before = __shfl_sync(0xffffffffu, before, 0);
-                __threadfence();
+                __syncwarp();
                 if (before == static_cast<uint32_t>(tail - head)) {
-                    // the head's share is in its second slot, the others' in their first
                     for (int c = 16 * set; c < tokens; c += 32) {
-                        float sum[16];
-                        const float* from = q.slots + (2 * (int64_t{head} * kWideCluster + rank) + 1) * slot +
-                                            c * kTcRows + row * 4;
-                        wide_load(from, sum);
-                        // two at a time under way
-                        from = q.slots + 2 * (int64_t{head + 1} * kWideCluster + rank) * slot + c * kTcRows +
-                               row * 4;
-                        const int64_t step = 2 * kWideCluster * slot;
-                        for (int b = head + 1; b <= tail; b += 2, from += 2 * step) {
-                            float v[16], w[16];
-                            wide_load(from, v);
-                            if (b < tail) wide_load(from + step, w);
+                        int32_t sum[16];
 #pragma unroll
-                            for (int m = 0; m < 16; ++m) sum[m] += v[m];
-                            if (b < tail) {
+                        for (int m = 0; m < 16; ++m) sum[m] = __ldcg(sums + (c + m) * kTcRows);
+                        float v[16];
 #pragma unroll
-                                for (int m = 0; m < 16; ++m) sum[m] += w[m];
-                            }
-                        }
-                        i8_wide_store<TC>(p, m0 + c, n, tokens - c, scales[0], first, sb, bias, sum);
+                        for (int m = 0; m < 16; ++m) v[m] = static_cast<float>(sum[m]);
+                        i8_wide_store<TC>(p, m0 + c, n, tokens - c, scales[0], first, sb, bias, v);
                         next_scales();
                     }
                 }

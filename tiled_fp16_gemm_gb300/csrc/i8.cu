@@ -176,42 +176,47 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tile_tokens(int64_t M) { return M < tg::kI8Tokens ? up(M, 32) : tg::kI8Tokens; }
 
 // Fills in the tile's width and the division of the work with the least time.  Measured, on random
-// codes: a unit takes 2.4 ns per token, and 0.4 us at least (what B takes to come and be decoded);
-// the end of a tile 8 ns per token; sharing tiles 4 us + 60 ns per token (16384×8192 with 512 rows:
-// whole tiles on 64 of the 76 pairs 84 us, all units shared evenly 92; 4096×28672 with 256 rows,
-// where 16 tiles are too few, 94 and 66).
+// codes: a unit takes 2.4 ns per token, and 0.4 us at least (what B takes to be decoded; to come, 6 ns
+// per cluster); the end of a tile 8 ns per token; the sums of a shared tile 2.5 us + 25 ns per token,
+// twice as much per token where a cluster has two of them.  Whole tiles / even runs / equal parts,
+// us: 2048×8192 with 64 rows 28.6 / 14.9 / 13.8, 4096×8192 with 128 30.3 / 21.4 / 20.3, 4096×28672
+// with 128 86 / 36.0 / 37.0, 5120×2048 with 64 12.3 / 13.8 / -, 16384×8192 with 64 32.0 / 36.0 / -.
 void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
-    q->k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
+    const int32_t k_units = static_cast<int32_t>((p.K + tg::kTcK - 1) / tg::kTcK);
     constexpr int64_t rows = int64_t{tg::kTcRows} * tg::kWideCluster;
     const int64_t row_tiles = (p.N + rows - 1) / rows;
+    q->k_units = k_units;
     double least = 1e300;
     const int32_t widest = static_cast<int32_t>(tile_tokens(p.M));
     for (int32_t tokens = 32; tokens <= widest; tokens += 32) {
         const int64_t m_tiles = (p.M + tokens - 1) / tokens, tiles = row_tiles * m_tiles;
-        const double mma = 0.0024 * tokens;
-        const double unit = mma < 0.4 ? 0.4 : mma;
-        for (const int32_t grain : {q->k_units, 1}) {
-            const int64_t grains = tiles * q->k_units / grain;
-            const int64_t clusters = grains < limit ? grains : limit;
-            const int64_t most = (grains + clusters - 1) / clusters * grain;
-            double time = unit * static_cast<double>(most) +
-                          0.008 * tokens * static_cast<double>((most + q->k_units - 1) / q->k_units);
-            if (grain != q->k_units && (most % q->k_units != 0 || grains % clusters != 0)) time += 4.0 + 0.06 * tokens;
-            if (time < least) {
-                least = time;
-                q->tokens = tokens;
-                q->m_tiles = static_cast<int32_t>(m_tiles);
-                q->grain = grain;
-                q->clusters = static_cast<int32_t>(clusters);
-                q->units = tiles * q->k_units;
-            }
-        }
+        const double mma = 0.0024 * tokens, decoded = mma < 0.4 ? 0.4 : mma;
+        auto offer = [&](int32_t parts, int32_t grain, int64_t clusters, int64_t most, double sums) {
+            const double memory = 0.006 * static_cast<double>(clusters);
+            const double time = (memory < decoded ? decoded : memory) * static_cast<double>(most) +
+                                0.008 * tokens * static_cast<double>((most + k_units - 1) / k_units) + sums;
+            if (time >= least) return;
+            least = time;
+            q->tokens = tokens;
+            q->m_tiles = static_cast<int32_t>(m_tiles);
+            q->parts = parts;
+            q->grain = grain;
+            q->clusters = static_cast<int32_t>(clusters);
+            q->units = tiles * k_units;
+        };
+        const int64_t whole = tiles < limit ? tiles : limit;
+        offer(0, k_units, whole, (tiles + whole - 1) / whole * k_units, 0.0);
+        const int64_t units = tiles * k_units, even = units < limit ? units : limit;
+        offer(0, 1, even, (units + even - 1) / even, 2.5 + 0.05 * tokens);
+        const int64_t each = limit / tiles, parts = each < k_units ? each : k_units;
+        if (parts > 1)
+            offer(static_cast<int32_t>(parts), 1, tiles * parts, (k_units + parts - 1) / parts, 2.5 + 0.025 * tokens);
     }
 }
 
-// Counters, the blocks' shares of sums (two each), A as fp16: for any plan of these sizes.
+// Counters, the shared tiles' sums, A as fp16: for any plan of these sizes.
 int64_t slot_bytes(int64_t M) {
-    return 2 * int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4;
+    return int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4;
 }
 int64_t workspace_bytes(int64_t M, int64_t, int64_t K) {
     if (M <= 8 || K == 0) return 0;
@@ -235,7 +240,7 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
     q.limit_ns = tg::op_wait_limit_ns();
     q.timeouts = dev.timeouts;
     q.counters = static_cast<uint32_t*>(ws);
-    q.slots = reinterpret_cast<float*>(static_cast<char*>(ws) + tg::kI8CounterBytes);
+    q.sums = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + tg::kI8CounterBytes);
     uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + tg::kI8CounterBytes + slot_bytes(whole.M));
     const int64_t ldo = up(whole.K, tg::kTcK), slab = slab_rows(whole.M, whole.K);
     CUtensorMap codes, ordered;
@@ -257,10 +262,18 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
                            static_cast<uint32_t>(q.tokens / tg::kWideCluster), CU_TENSOR_MAP_SWIZZLE_128B))
             return TG_ERR_LAUNCH;
         q.inject = tg::op_take_inject();
+        // a cluster is the first of one shared tile at most
+        const int64_t tiles = q.units / q.k_units, places = tiles < q.clusters ? tiles : q.clusters;
+        const bool shares = q.grain != q.k_units;
+        q.by_tile = tiles < q.clusters ? 1 : 0;
+        // (with sums to zero, blocks on all SMs)
+        const int64_t across = (ldo / 16 + 255) / 256, down = p.M < 32768 ? p.M : 32768;
+        const int64_t least = shares ? (dev.num_sms + across - 1) / across : 1;
         tg_status_t st = launch(tg::tg_i8_expand,
-                                dim3(static_cast<unsigned>((ldo / 16 + 255) / 256),
-                                     static_cast<unsigned>(p.M < 32768 ? p.M : 32768)),
-                                256, 0, 1, s, p.A, p.lda, p.M, p.K, order, ldo, q.counters);
+                                dim3(static_cast<unsigned>(across), static_cast<unsigned>(down > least ? down : least)),
+                                256, 0, 1, s, p.A, p.lda, p.M, p.K, order, ldo, q.counters,
+                                reinterpret_cast<uint4*>(q.sums),
+                                shares ? places * tg::kWideCluster * q.tokens * tg::kTcRows / 4 : int64_t{0});
         if (st != TG_OK) return st;
         st = launch(kernel, dim3(static_cast<unsigned>(q.clusters * tg::kWideCluster)), tg::kWideThreads,
                     tg::kI8WideSmem, tg::kWideCluster, s, q, codes, ordered);
@@ -271,11 +284,13 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
 
 // Whether the kernel for few rows is the faster one: up to 16 rows always, more of them with small
 // weights.  Measured, us, few / wide: 16384×8192 with 16 rows 28.7 / 30.9, 32 rows 48 / 31;
-// 4096×28672 with 16 rows 29.8 / 31.2; 4096×4096 with 32 rows 11.5 / 15.5; 8192×2048 with 32 rows
-// 12.4 / 12.6, 64 rows 18.9 / 12.8; 512×8192 with 64 rows 15.4 / 16.5; 1024×1024 with 64 rows 8.4 / 9.2.
+// 4096×28672 with 16 rows 29.8 / 31.2; 9728×2560 with 32 rows 13.6 / 13.8, 9728×4096 18.0 / 17.4;
+// 4096×1024 with 48 rows 8.6 / 9.1, 64 rows 11.6 / 9.2; 2560×2560 with 48 rows 10.8 / 10.8;
+// 1024×1024 with 64 rows 9.0 / 9.0.
 bool prefer_few(const I8Params& p) {
     const int64_t codes = p.N * p.K;
-    return p.M <= 16 || (p.M <= 32 && codes <= 20000000) || (p.M <= 64 && codes <= 4500000);
+    return p.M <= 16 || (p.M <= 32 && codes <= 30000000) || (p.M <= 48 && codes <= 5000000) ||
+           (p.M <= 64 && codes <= 1000000);
 }
 
 // Launches the kernel for few rows; false where no shape fits.
