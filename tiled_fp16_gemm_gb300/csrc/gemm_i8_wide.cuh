@@ -19,11 +19,12 @@
 //
 // Measured, bf16 results, random codes (they draw more power than zeros: 512 rows 84 to 88 us where a
 // constant weight takes 80): 16384×8192 with 64 / 128 / 256 / 512 / 1024 rows 32 / 35 / 48 / 86 / 166 us,
-// 28672×4096 33 / 37 / 51 / 75 / 139, 4096×4096 14 / 16 / 21, 1024×1024 with 128 to 512 rows 9.  A unit takes 0.62 us with 256
-// tokens (0.54 at full clocks), bound by the MMAs; with few tokens the blocks fetch B at 5.5 TB/s,
-// and 8 us go to two launches, the start and the end.  The C warps have what the epilogue needs
-// before the sums are there, and give the accumulator back when they have read it, before they
-// have stored: 512 rows of 28672×4096 73 us instead of 84.  Registers are full (80).
+// 28672×4096 33 / 37 / 51 / 75 / 139, 4096×4096 with 64 / 128 / 256 rows 14 / 16 / 21, 1024×1024 with
+// 128 to 512 rows 9.  A unit takes 0.62 us with 256 tokens (0.54 at full clocks), bound by the MMAs;
+// with few tokens the blocks fetch B at 5.5 TB/s, and 6 to 8 us go to two launches, the start and the
+// end.  The C warps have what the epilogue needs before the sums are there, and give the accumulator
+// back when they have read it, before they have stored: 512 rows of 28672×4096 73 us instead of 84.
+// Registers are full (80).
 #pragma once
 
 #include "gemm_i8.cuh"
