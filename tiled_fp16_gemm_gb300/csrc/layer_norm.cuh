@@ -160,13 +160,14 @@ __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
 //   Σ (v - mu)² = Σ_u (Σd² + 2 g_u Σd + n_u g_u²),   g_u = m_u - mu
 // so neither a mean far from zero nor warps with different means cost digits.
 //
-// Measured: 8192×4096 bf16 on an fp32 stream 70 us (5.7 TB/s), bf16 52 us, its codes 71 us; rows of
-// x as codes 21 us; 2048×16384 bf16 58 us; unaligned, 1021×5119 13 us, 4096×767 10 us; one row of
-// 4096 2.7 us.  Bound by memory on the fp32 stream; else by the way of a row from its loads to its
+// Measured: 8192×4096 bf16 on an fp32 stream 64 us (6.3 TB/s), bf16 48 us, its codes 54 us; rows of
+// x as codes 21 us; 600×16384 bf16 17.6 us; unaligned, 1021×5119 13 us, 4096×767 10 us; one row of
+// 4096 2.5 us.  Bound by memory on the fp32 stream; else by the way of a row from its loads to its
 // stores, with five rows of 4096 on an SM (96 registers).  The weights' reads, from L1, are 4 us of
-// 70.  Tried: the next rows fetched ahead by cp.async (2048×8192 29 us instead of 33, 2048×16384 88
+// 64.  Tried: the next rows fetched ahead by cp.async (2048×8192 29 us instead of 33, 2048×16384 88
 // instead of 57) or to L2 (slower everywhere), a warp per row of 4096 (spills, 83 us), a thread's
-// columns a block apart (addresses in registers, 80 us).
+// columns a block apart (addresses in registers, 80 us), runs of 4 or 2 neighbours instead of 8 (bf16
+// 57 and 63 us).
 
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
