@@ -168,3 +168,24 @@ def test_captured_products_that_share_tiles(tg):
                 graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for w, g in zip(want, got) for x, y in zip(w, g))
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 1024, 8192), (40, 9700, 2048)])
+def test_a_wait_that_runs_out_in_a_shared_tile(tg, M, N, K):
+    """One cluster of a tile gives up: reported once, the others end, and the next call is right."""
+    a, b, sa, sb, _ = codes_case(M, N, K)
+    want = tg.gemm_i8(a, b, sa, sb)
+    tg.sync_status()
+    try:
+        tg.tg_debug_set_wait_timeout_ns(20_000_000)
+        tg.tg_debug_inject(1)
+        tg.gemm_i8(a, b, sa, sb)
+        with pytest.raises(tg.TgemmError) as e:
+            tg.sync_status()
+        assert e.value.status == tg.TG_ERR_TIMEOUT
+        tg.sync_status()
+    finally:
+        tg.tg_debug_inject(0)
+        tg.tg_debug_set_wait_timeout_ns(0)
+    assert torch.equal(tg.gemm_i8(a, b, sa, sb), want)
+    tg.sync_status()
