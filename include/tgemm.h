@@ -521,10 +521,8 @@ int64_t tg_gemm_i8_workspace(int64_t M, int64_t N, int64_t K);
  * M, N, K  M and N in [0, 2^31 - 1], K in [0, 131071].  M == 0 or N == 0: nothing is done.
  * epi      as tg_gemm_ex, but the residual is of C's type (may be C itself); NULL: no
  *          bias, activation or residual, C in fp16.
- * Sums     of whole numbers, exact up to 2^24 in size (up to 8 rows: always).  Beyond
- *          that, each of the K / 16 additions of the tensor cores may round the running
- *          sum in its 24th bit.  What follows is fp32: the sum times Ascale, that times
- *          Bscale, and so on, and C is rounded once.
+ * Sums     of whole numbers, exact at every size.  What follows is fp32: the sum, rounded,
+ *          times Ascale, that times Bscale, and so on, and C is rounded once.
  * workspace  device, 256-byte aligned, tg_gemm_i8_workspace(M, N, K) bytes at least; it
  *          holds nothing from one call to the next, and calls that may overlap on the GPU
  *          need one each.  NULL: a buffer that belongs to the (device, stream), grown on

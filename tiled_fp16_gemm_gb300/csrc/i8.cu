@@ -214,13 +214,16 @@ void plan_wide(const I8Params& p, int64_t limit, tg::I8Wide* q) {
     }
 }
 
-// Counters, the shared tiles' sums, A as fp16: for any plan of these sizes.
-int64_t slot_bytes(int64_t M) {
-    return int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4;
+// Counters and peaks, the tiles' sums (those of shared ones, and where the accumulator may not take all of K
+// also of each cluster's own), A as fp16: for any plan of these sizes.
+bool more_runs(int64_t K) { return K > int64_t{tg::kI8WideRun} * tg::kTcK; }
+int64_t slot_bytes(int64_t M, int64_t K) {
+    return int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4 * (more_runs(K) ? 2 : 1);
 }
+constexpr int64_t kHeadBytes = tg::kI8CounterBytes + tg::kI8PeakBytes;
 int64_t workspace_bytes(int64_t M, int64_t, int64_t K) {
     if (M <= 8 || K == 0) return 0;
-    return tg::kI8CounterBytes + slot_bytes(M) + slab_rows(M, K) * up(K, tg::kTcK) * 2;
+    return kHeadBytes + slot_bytes(M, K) + slab_rows(M, K) * up(K, tg::kTcK) * 2;
 }
 
 template <typename TC>
@@ -240,8 +243,11 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
     q.limit_ns = tg::op_wait_limit_ns();
     q.timeouts = dev.timeouts;
     q.counters = static_cast<uint32_t*>(ws);
-    q.sums = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + tg::kI8CounterBytes);
-    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + tg::kI8CounterBytes + slot_bytes(whole.M));
+    tg::I8Peak* peaks = nullptr;
+    if (more_runs(whole.K)) peaks = reinterpret_cast<tg::I8Peak*>(static_cast<char*>(ws) + tg::kI8CounterBytes);
+    q.peaks = peaks;
+    q.sums = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kHeadBytes);
+    uint16_t* order = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + kHeadBytes + slot_bytes(whole.M, whole.K));
     const int64_t ldo = up(whole.K, tg::kTcK), slab = slab_rows(whole.M, whole.K);
     CUtensorMap codes, ordered;
     if (!tg::op_map_2d(&codes, whole.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, whole.K, whole.N, whole.ldb, tg::kTcK,
@@ -266,14 +272,18 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
         const int64_t tiles = q.units / q.k_units, places = tiles < q.clusters ? tiles : q.clusters;
         const bool shares = q.grain != q.k_units;
         q.by_tile = tiles < q.clusters ? 1 : 0;
-        // (with sums to zero, blocks on all SMs)
-        const int64_t across = (ldo / 16 + 255) / 256, down = p.M < 32768 ? p.M : 32768;
-        const int64_t least = shares ? (dev.num_sms + across - 1) / across : 1;
-        tg_status_t st = launch(tg::tg_i8_expand,
-                                dim3(static_cast<unsigned>(across), static_cast<unsigned>(down > least ? down : least)),
-                                256, 0, 1, s, p.A, p.lda, p.M, p.K, order, ldo, q.counters,
+        q.places = shares ? static_cast<int32_t>(places) : 0;
+        // (what the SMs hold at once, so that the peaks are few; with sums to zero, blocks on all SMs)
+        const int64_t across = (ldo + tg::kI8PeakColumns - 1) / tg::kI8PeakColumns;
+        const int64_t held = 8 * int64_t{dev.num_sms} < tg::kI8Peaks ? 8 * int64_t{dev.num_sms} : tg::kI8Peaks;
+        const int64_t least = shares ? (dev.num_sms + across - 1) / across : 1, most = held / across;
+        const int64_t down = p.M < least ? least : p.M < most ? p.M : most;
+        q.across = static_cast<int32_t>(across);
+        q.down = static_cast<int32_t>(down);
+        tg_status_t st = launch(tg::tg_i8_expand, dim3(static_cast<unsigned>(across), static_cast<unsigned>(down)), 256,
+                                0, 1, s, p.A, p.lda, p.M, p.K, order, ldo, q.counters,
                                 reinterpret_cast<uint4*>(q.sums),
-                                shares ? places * tg::kWideCluster * q.tokens * tg::kTcRows / 4 : int64_t{0});
+                                shares ? places * tg::kWideCluster * q.tokens * tg::kTcRows / 4 : int64_t{0}, peaks);
         if (st != TG_OK) return st;
         st = launch(kernel, dim3(static_cast<unsigned>(q.clusters * tg::kWideCluster)), tg::kWideThreads,
                     tg::kI8WideSmem, tg::kWideCluster, s, q, codes, ordered);
