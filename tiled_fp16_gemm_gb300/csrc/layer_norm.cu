@@ -247,10 +247,11 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             const int64_t each = (a->rows + dev.num_sms - 1) / dev.num_sms;
             groups = split > 1 ? 1 : fit / warps < each ? fit / warps : static_cast<int>(each);
             most = dev.num_sms;
-            // two rows of an SM in two blocks, where that is not too many shares (160×1024 5.7 us, 6.7 with
-            // two groups in a block; 256×1024 5.9 and 7.4; 256×4096 10.0 and 9.3)
-            if (groups == 2 && each == 2 && (a->rows <= 160 || (a->rows <= 256 && cols <= 1024)))
-                groups = 1, most = 2 * dev.num_sms;
+            // Two rows of an SM in two blocks, not in two groups of a block, while the second launch has
+            // all shares under way at once.  us, groups / blocks, in bf16: 160×1024 5.9 / 4.8, 224×512 4.9 /
+            // 4.5, 256×1024 6.3 / 5.2, 256×1536 6.4 / 5.9, 224×2560 6.7 / 6.6, 256×4096 8.2 / 7.9; past
+            // that number 257×1024 6.3 / 6.6, 304×1024 6.2 / 7.3, 257×4096 8.2 / 9.3.
+            if (groups == 2 && each == 2 && a->rows <= tg::kLnSumShares) groups = 1, most = 2 * dev.num_sms;
         }
         const size_t smem = static_cast<size_t>(ring) * groups * warps;
         if (rows_ring && split > 1) {

@@ -901,11 +901,13 @@ __global__ void __launch_bounds__(256) tg_layer_norm_grad_simple(const LayerNorm
 }
 
 // The column sums of the blocks' shares, in a fixed order: blockIdx.y 0: dw, 1: db.  32·G columns
-// per block, 32 warps with every 32nd share each, 8 values of a thread under way at a time: with G
-// = 1 those of 256 shares.  (16 warps with every 16th share, and 64-bit addresses: 2 us more.)
+// per block, 32 warps with every 32nd share each, 8 values of a thread under way at a time.  (16
+// warps with every 16th share, and 64-bit addresses: 2 us more.)
+constexpr int kLnSumAhead = 8;
+constexpr int kLnSumShares = 32 * kLnSumAhead;  // under way at once, with G = 1
 template <int G>
 __global__ void __launch_bounds__(1024) tg_layer_norm_grad_sum(const LayerNormGradParams q, int blocks) {
-    constexpr int kAhead = 8 / G;
+    constexpr int kAhead = kLnSumAhead / G;
     __shared__ float part[32][32 * G + 1];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, cols = static_cast<int>(q.n.cols);
     const int c0 = blockIdx.x * 32 * G, here = cols - c0 - lane;  // columns from this thread's first on
