@@ -89,32 +89,29 @@ tg_status_t launch_rows(const LayerNormParams& p, const tg::OpDevice& dev, cudaS
     auto fits = [&](int n) { return warps(n) <= (vec && n == 4 && !few(4) ? 12 : 16); };
     int ch = !vec || fits(4) ? 4 : 8;
     while (ch > 1 && (cols <= 128 * ch || (p.rows * warps(ch) < 8 * dev.num_sms && fits(ch / 2)))) ch /= 2;
-    // Threads of an SM, for which a kernel's registers are: in rows of four runs 640, and 512 of an
-    // fp32 stream, whose loads under way take more (8192×4096 bf16 48 us, 52 with 512; fp32 64, 66 with
-    // 640); else 1024, and 512 where that holds all rows (16×1024 2.2 us, 2.6; 64×8192 4.1, 4.8).
-    constexpr int kFour = sizeof(TR) == 4 ? 512 : 640;
+    // Threads of an SM, for which a kernel's registers are: in rows of four runs 640, of eight 512; else
+    // 1024, and 512 where that holds all rows, whose weights come with them (16×1024 1.9 us, 2.1 without;
+    // 64×8192 2.95, 3.25).
     if (vec && fits(ch)) {
         // Warps that have all of their columns (2050×1536 8.2 us with three of 512, 8.8 with two of
         // 1024; 1200×768 4.3 and 4.7), where an SM does not hold fewer rows for it, or holds all
         // (700×3584 6.2 us with four of 1024, 8.3 with seven of 512 in two waves).
-        auto held = [&](int n) { return (n > 2 ? kFour : 1024) / (32 * warps(n)); };  // rows, of an SM
+        auto held = [&](int n) { return (n > 2 ? 640 : 1024) / (32 * warps(n)); };  // rows, of an SM
         while ((ch == 4 || ch == 2) && cols % (256 * ch) != 0 && cols % (128 * ch) == 0 && fits(ch / 2) &&
                (held(ch / 2) >= held(ch) || p.rows <= held(ch / 2) * dev.num_sms))
             ch /= 2;
         std::true_type v;
         if (ch == 1) return few(1) ? run(Int<1>{}, v, Int<512>{}) : run(Int<1>{}, v, Int<1024>{});
         if (ch == 2) return few(2) ? run(Int<2>{}, v, Int<512>{}) : run(Int<2>{}, v, Int<1024>{});
-        if (ch == 4) return few(4) ? run(Int<4>{}, v, Int<512>{}) : run(Int<4>{}, v, Int<kFour>{});
-        return run(Int<8>{}, v, Int<512>{});
+        return ch == 4 ? run(Int<4>{}, v, Int<640>{}) : run(Int<8>{}, v, Int<512>{});
     }
     if (!vec && warps(4) <= 32) {
         std::false_type v;
         if (warps(ch) > 16) return run(Int<4>{}, v, Int<1024>{});  // (registers do not hold all)
         if (ch == 1) return few(1) ? run(Int<1>{}, v, Int<512>{}) : run(Int<1>{}, v, Int<1024>{});
         if (ch == 2) return few(2) ? run(Int<2>{}, v, Int<512>{}) : run(Int<2>{}, v, Int<1024>{});
-        // (codes with 640, where an SM then has a block more: 1021×5119 14.5 us, 17.0; without codes 13.6, 13.3)
-        return MODE != tg::kLnH && !few(4) && warps(4) <= 10 ? run(Int<4>{}, v, Int<640>{})
-                                                             : run(Int<4>{}, v, Int<512>{});
+        // (640 where an SM then has a block more: 1021×5119 12.9 us, 14.7 with 512; 700×9999 17.3, 22.6)
+        return warps(4) <= 10 ? run(Int<4>{}, v, Int<640>{}) : run(Int<4>{}, v, Int<512>{});
     }
     const int64_t most = 8 * int64_t{dev.num_sms};
     return launch(tg::tg_layer_norm_simple<TX, TR, MODE>,

@@ -160,11 +160,14 @@ __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
 //   Σ (v - mu)² = Σ_u (Σd² + 2 g_u Σd + n_u g_u²),   g_u = m_u - mu
 // so neither a mean far from zero nor warps with different means cost digits.
 //
-// Measured: 8192×4096 bf16 on an fp32 stream 64 us (6.3 TB/s), bf16 48 us, its codes 54 us; rows of
-// x as codes 21 us; 600×16384 bf16 17.6 us; unaligned, 1021×5119 13 us, 4096×767 10 us; one row of
-// 4096 2.5 us.  Bound by memory on the fp32 stream; else by the way of a row from its loads to its
-// stores, with five rows of 4096 on an SM (96 registers).  The weights' reads, from L1, are 4 us of
-// 64.  Tried: the next rows fetched ahead by cp.async (2048×8192 29 us instead of 33, 2048×16384 88
+// Measured: 8192×4096 bf16 on an fp32 stream 60 us (6.7 TB/s), bf16 47 us, its codes 59 and 49 us; rows of
+// x as codes 17 us; 600×16384 bf16 16.1 us; 8192×1536 19 us; unaligned, 1021×5119 13 us, 4096×767 10 us;
+// one row of 4096 2.1 us.  Bound by memory on the fp32 stream; else by the way of a row from its loads to
+// its stores, with five rows of 4096 on an SM (96 registers).  The weights' reads, from L1, are some 4 us
+// of 60.  A warp or block has one row and is done: a loop over rows kept weights and addresses in
+// registers that the row needs (8192×1536 22.6 us, rows of x as codes 21).  Registers hold a row in all
+// classes but runs of eight and unaligned runs of four with 640 or 1024 threads, which spill 12 to 20 bytes.
+// Tried: the next rows fetched ahead by cp.async (2048×8192 29 us instead of 33, 2048×16384 88
 // instead of 57) or to L2 (slower everywhere), a warp per row of 4096 (spills, 83 us), a thread's
 // columns a block apart (addresses in registers, 80 us), runs of 4 or 2 neighbours instead of 8 (bf16
 // 57 and 63 us).
@@ -290,13 +293,13 @@ struct LnCols {
     }
 };
 
-// `threads`: of a row, 32 (a block has several rows) or all of the block.  SM: of an SM, what
+// `threads`: of a row, 32 (a block has a row for each warp) or all of the block.  SM: of an SM, what
 // registers are for.
 template <typename TX, typename TR, int CH, bool VEC, int MODE, int SM>
 __global__ void __launch_bounds__(SM, 1)
     tg_layer_norm_rows(const LayerNormParams p, int threads) {
-    __shared__ float stat[2][3][32];  // of the warps: mean, Σd, Σd²; a row's are read while the next one's come
-    __shared__ uint32_t most[2][32];
+    __shared__ float stat[3][32];  // of the warps: mean, Σd, Σd²
+    __shared__ uint32_t most[32];
     const int lane = threadIdx.x & 31, cols = static_cast<int>(p.cols);
     const bool alone = threads == 32;
     const int warp = alone ? 0 : threadIdx.x >> 5, warps = threads >> 5;
@@ -309,138 +312,148 @@ __global__ void __launch_bounds__(SM, 1)
     const float mine_inv = mine > 0.0f ? 1.0f / mine : 0.0f;
     op_release_next();
     op_wait_previous();
-    int turn = 0;
-    for (int64_t row = int64_t{blockIdx.x} * groups + group; row < p.rows;
-         row += int64_t{gridDim.x} * groups, turn ^= 1) {
-        F2 v[CH][4];
+    const int64_t row = int64_t{blockIdx.x} * groups + group;
+    if (row >= p.rows) return;
+    // The weights come with the row where the SMs hold all rows at once (64×8192 3.0 us, 3.25 without;
+    // 2048×512 3.0, 3.3); else rows on an SM take turns, and registers count for more.
+    constexpr bool kEarly = MODE != kLnRaw && SM == 512 && CH <= 2;
+    auto here = [&](const float* all) { return all != nullptr ? all + c.first : nullptr; };
+    F2 v[CH][4], w_row[kEarly ? CH : 1][4], b_row[kEarly ? CH : 1][4];
+    c.either([&](auto whole) {
+        constexpr bool ALL = decltype(whole)::value;
+        const TX* x = static_cast<const TX*>(p.x) + row * p.ldx + c.first;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(x, ch, v[ch]);
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                c.template weight<ALL>(here(p.w), ch, w_row[ch], 1.0f);
+                c.template weight<ALL>(here(p.b), ch, b_row[ch], 0.0f);
+            }
+        }
+        if (MODE == kLnRaw || p.r == nullptr) return;
+        const TR* rr = static_cast<const TR*>(p.r) + row * p.ldr + c.first;
+        F2 r[CH][4];
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(rr, ch, r[ch]);
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[ch][i]);
+        if (p.y == nullptr) return;
+        TR* y = static_cast<TR*>(p.y) + row * p.ldy + c.first;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) c.template store<ALL>(y, ch, v[ch]);
+    });
+    if (MODE != kLnRaw) {
+        if (MODE == kLnH && p.h == nullptr) return;
+        F2 a = 0;
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
+        const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
+        F2 b = 0;
+        a = 0;
+        c.either([&](auto whole) {
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) c.template less<decltype(whole)::value>(ch, m, v[ch]);
+        });
+#pragma unroll
+        for (int ch = 0; ch < CH; ++ch) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a = f2_add(a, v[ch][i]);
+                b = f2_fma(v[ch][i], v[ch][i], b);
+            }
+        }
+        // both at once: the lower lanes take Σd, the upper ones Σd²
+        const float a1 = f2_sum(a), b1 = f2_sum(b);
+        float w = (lane < 16 ? a1 : b1) + __shfl_xor_sync(0xffffffffu, lane < 16 ? b1 : a1, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        float off, var;  // mu - m, Σ (v - mu)²
+        if (alone) {
+            const float s1 = __shfl_sync(0xffffffffu, w, 0);
+            off = s1 * inv;
+            var = __shfl_sync(0xffffffffu, w, 16) - off * s1;
+        } else {
+            if (lane == 0) {
+                stat[0][warp] = m;
+                stat[1][warp] = w;
+            }
+            if (lane == 16) stat[2][warp] = w;
+            __syncthreads();
+            const bool has = lane < warps;
+            const float m0 = stat[0][0];
+            const float mu = has ? stat[0][lane] - m0 : 0.0f;
+            const float s1 = has ? stat[1][lane] : 0.0f;
+            const float shift = ln_warp_sum(fmaf(count, mu, s1)) * inv;  // mu - m_0
+            const float gu = mu - shift;
+            var = ln_warp_sum(has ? fmaf(gu, fmaf(count, gu, 2.0f * s1), stat[2][lane]) : 0.0f);
+            off = shift - (m - m0);
+        }
+        const float s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
+        // (fmaxf would turn a NaN into 0)
+        const float ss = var == var ? s : var;
+        const F2 s2 = f2(ss, ss), o2 = f2(-off, -off);
+        TX* h = static_cast<TX*>(p.h) + row * p.ldh + c.first;
         c.either([&](auto whole) {
             constexpr bool ALL = decltype(whole)::value;
-            const TX* x = static_cast<const TX*>(p.x) + row * p.ldx + c.first;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(x, ch, v[ch]);
-            if (MODE == kLnRaw || p.r == nullptr) return;
-            const TR* rr = static_cast<const TR*>(p.r) + row * p.ldr + c.first;
-            F2 r[CH][4];
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) c.template load<ALL>(rr, ch, r[ch]);
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[ch][i] = f2_add(v[ch][i], r[ch][i]);
-            if (p.y == nullptr) return;
-            TR* y = static_cast<TR*>(p.y) + row * p.ldy + c.first;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) c.template store<ALL>(y, ch, v[ch]);
-        });
-        if (MODE != kLnRaw) {
-            if (MODE == kLnH && p.h == nullptr) continue;
-            F2 a = 0;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a = f2_add(a, v[ch][i]);
-            const float m = ln_warp_sum(f2_sum(a)) * mine_inv;
-            F2 b = 0;
-            a = 0;
-            c.either([&](auto whole) {
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch) c.template less<decltype(whole)::value>(ch, m, v[ch]);
-            });
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
+                const int at = kEarly ? ch : 0;
+                if constexpr (!kEarly) {
+                    c.template weight<ALL>(here(p.w), ch, w_row[0], 1.0f);
+                    c.template weight<ALL>(here(p.b), ch, b_row[0], 0.0f);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[ch][i] = f2_fma(f2_mul(f2_add(v[ch][i], o2), s2), w_row[at][i], b_row[at][i]);
+                if (MODE == kLnH) c.template store<ALL>(h, ch, v[ch]);
+            }
+        });
+    }
+    if constexpr (MODE != kLnH) {
+        float size = 0.0f;
+        c.either([&](auto whole) {
+            constexpr bool ALL = decltype(whole)::value;
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    a = f2_add(a, v[ch][i]);
-                    b = f2_fma(v[ch][i], v[ch][i], b);
+                    const float2 f = f2_get(v[ch][i]);
+                    size = ln_most(size, c.template has<ALL>(ch, 2 * i) ? f.x : 0.0f,
+                                   c.template has<ALL>(ch, 2 * i + 1) ? f.y : 0.0f);
                 }
-            }
-            // both at once: the lower lanes take Σd, the upper ones Σd²
-            const float a1 = f2_sum(a), b1 = f2_sum(b);
-            float w = (lane < 16 ? a1 : b1) + __shfl_xor_sync(0xffffffffu, lane < 16 ? b1 : a1, 16);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            float off, var;  // mu - m, Σ (v - mu)²
-            if (alone) {
-                const float s1 = __shfl_sync(0xffffffffu, w, 0);
-                off = s1 * inv;
-                var = __shfl_sync(0xffffffffu, w, 16) - off * s1;
-            } else {
-                if (lane == 0) {
-                    stat[turn][0][warp] = m;
-                    stat[turn][1][warp] = w;
-                }
-                if (lane == 16) stat[turn][2][warp] = w;
-                __syncthreads();
-                const bool has = lane < warps;
-                const float m0 = stat[turn][0][0];
-                const float mu = has ? stat[turn][0][lane] - m0 : 0.0f;
-                const float s1 = has ? stat[turn][1][lane] : 0.0f;
-                const float shift = ln_warp_sum(fmaf(count, mu, s1)) * inv;  // mu - m_0
-                const float gu = mu - shift;
-                var = ln_warp_sum(has ? fmaf(gu, fmaf(count, gu, 2.0f * s1), stat[turn][2][lane]) : 0.0f);
-                off = shift - (m - m0);
-            }
-            const float s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
-            // (fmaxf would turn a NaN into 0)
-            const float ss = var == var ? s : var;
-            const F2 s2 = f2(ss, ss), o2 = f2(-off, -off);
-            const float* w_at = p.w != nullptr ? p.w + c.first : nullptr;
-            const float* b_at = p.b != nullptr ? p.b + c.first : nullptr;
-            TX* h = static_cast<TX*>(p.h) + row * p.ldh + c.first;
-            c.either([&](auto whole) {
-                constexpr bool ALL = decltype(whole)::value;
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch) {
-                    F2 w2[4], b2[4];
-                    c.template weight<ALL>(w_at, ch, w2, 1.0f);
-                    c.template weight<ALL>(b_at, ch, b2, 0.0f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[ch][i] = f2_fma(f2_mul(f2_add(v[ch][i], o2), s2), w2[i], b2[i]);
-                    if (MODE == kLnH) c.template store<ALL>(h, ch, v[ch]);
-                }
-            });
+        });
+        uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(size) & 0x7fffffffu);
+        if (!alone) {
+            if (lane == 0) most[warp] = u;
+            __syncthreads();
+            u = __reduce_max_sync(0xffffffffu, lane < warps ? most[lane] : 0u);
         }
-        if constexpr (MODE != kLnH) {
-            float size = 0.0f;
-            c.either([&](auto whole) {
-                constexpr bool ALL = decltype(whole)::value;
+        const float scale = ln_scale(u);
+        if (lane == 0 && warp == 0) p.scale[row] = scale;
+        const LnCoder coder(scale);
+        int8_t* to = static_cast<int8_t*>(p.h) + row * p.ldh + c.first;
 #pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = f2_get(v[ch][i]);
-                        size = ln_most(size, c.template has<ALL>(ch, 2 * i) ? f.x : 0.0f,
-                                       c.template has<ALL>(ch, 2 * i + 1) ? f.y : 0.0f);
-                    }
-            });
-            uint32_t u = __reduce_max_sync(0xffffffffu, __float_as_uint(size) & 0x7fffffffu);
-            if (!alone) {
-                if (lane == 0) most[turn][warp] = u;
-                __syncthreads();
-                u = __reduce_max_sync(0xffffffffu, lane < warps ? most[turn][lane] : 0u);
-            }
-            const float scale = ln_scale(u);
-            if (lane == 0 && warp == 0) p.scale[row] = scale;
-            const LnCoder coder(scale);
-            int8_t* to = static_cast<int8_t*>(p.h) + row * p.ldh + c.first;
-#pragma unroll
-            for (int ch = 0; ch < CH; ++ch) {
-                uint32_t code[8];
-                coder.codes(v[ch], code);
-                if constexpr (VEC) {
-                    if (c.has(ch, 0)) {
-                        uint2 w;
-                        w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040),
-                                          __byte_perm(code[2], code[3], 0x0040), 0x5410);
-                        w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040),
-                                          __byte_perm(code[6], code[7], 0x0040), 0x5410);
-                        *reinterpret_cast<uint2*>(to + c.at(ch, 0)) = w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c.has(ch, i)) to[c.at(ch, i)] = static_cast<int8_t>(code[i]);
+        for (int ch = 0; ch < CH; ++ch) {
+            uint32_t code[8];
+            coder.codes(v[ch], code);
+            if constexpr (VEC) {
+                if (c.has(ch, 0)) {
+                    uint2 w;
+                    w.x = __byte_perm(__byte_perm(code[0], code[1], 0x0040),
+                                      __byte_perm(code[2], code[3], 0x0040), 0x5410);
+                    w.y = __byte_perm(__byte_perm(code[4], code[5], 0x0040),
+                                      __byte_perm(code[6], code[7], 0x0040), 0x5410);
+                    *reinterpret_cast<uint2*>(to + c.at(ch, 0)) = w;
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c.has(ch, i)) to[c.at(ch, i)] = static_cast<int8_t>(code[i]);
             }
         }
     }
