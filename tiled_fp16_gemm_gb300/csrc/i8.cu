@@ -4,69 +4,18 @@
 
 #include "gemm_i8.cuh"
 #include "gemm_i8_wide.cuh"
-#include "op_host.h"
+#include "launch_host.h"
 
 namespace {
 
 using tg::I8Params;
+using tg::launch;
+using tg::max_clusters;
+using tg::misaligned;
 
 constexpr int64_t kMaxK = 131071;  // 2^17 - 1: a sum of K products of -128 · -128 fits 32 bits
 
-bool misaligned(const void* p, unsigned bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
-}
-
-// One launch with dependent launch allowed, in clusters of `cluster` blocks.
-template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
-                   cudaStream_t s, Given... given) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
-    return TG_OK;
-}
-
 constexpr int kSmem = 226 * 1024;
-
-// Clusters of `size` blocks that the device holds at once, for a kernel opted into `smem`.
-template <typename Kernel>
-int max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
-    if (size == 1) return dev.num_sms;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(size);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
-}
 
 // What a device holds of a kernel that uses clusters, asked once.
 struct Limits {

@@ -12,15 +12,15 @@ namespace {
 using tg::allow_smem;
 using tg::check_matrix;
 using tg::elem_bytes;
+using tg::known_clusters;
+using tg::kRingBytes;
 using tg::launch;
 using tg::LayerNormGradParams;
 using tg::LayerNormParams;
-using tg::max_clusters;
 using tg::misaligned;
 using tg::wide;
 
 constexpr int64_t kMaxCols = 131071;   // codes of a row: whole sums of gemm_i8 fit 32 bits
-constexpr int kRingBytes = 214 * 1024;  // of shared memory, for rings
 constexpr int64_t kGradBlocks = 320;   // that share the column sums, at most
 
 tg::OpWorkspace g_workspace;  // column sums of the gradient, where the caller has none
@@ -255,7 +255,7 @@ tg_status_t backward(const tg_layer_norm_t* a, const tg_layer_norm_grad_t* b, vo
             const auto kernel = vec ? tg::tg_layer_norm_grad_rows<TX, TR, true, true>
                                     : tg::tg_layer_norm_grad_rows<TX, TR, false, true>;
             if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
-            most = max_clusters(kernel, split, 32 * warps, smem, dev);
+            most = known_clusters(kernel, split, 32 * warps, smem, dev);
             if (most < 1) return TG_ERR_LAUNCH;
         }
         if (most > kGradBlocks) most = kGradBlocks;

@@ -10,8 +10,8 @@ namespace {
 using tg::allow_smem;
 using tg::check_matrix;
 using tg::elem_bytes;
+using tg::known_clusters;
 using tg::launch;
-using tg::max_clusters;
 using tg::misaligned;
 using tg::narrow;
 using tg::NormGradParams;
@@ -227,7 +227,7 @@ static tg_status_t norm_residual_backward(const tg_norm_t* a, const tg_norm_grad
             const auto kernel = vec ? tg::tg_norm_grad_rows<TX, TR, true, true>
                                     : tg::tg_norm_grad_rows<TX, TR, false, true>;
             if (!allow_smem(kernel, dev.dev)) return TG_ERR_LAUNCH;
-            most = max_clusters(kernel, split, r.threads, r.smem, dev);
+            most = known_clusters(kernel, split, r.threads, r.smem, dev);
             if (most < 1) return TG_ERR_LAUNCH;
         }
         const int64_t wanted = ring ? (a->rows + r.groups - 1) / r.groups : a->rows;

@@ -6,10 +6,13 @@
 #include "gemm_w4.cuh"
 #include "gemm_w4_tc.cuh"
 #include "gemm_w4_wide.cuh"
-#include "op_host.h"
+#include "launch_host.h"
 
 namespace {
 
+using tg::launch;
+using tg::max_clusters;
+using tg::misaligned;
 using tg::W4Params;
 
 tg::OpWorkspace g_workspace;  // 16-bit weights of the dense path
@@ -17,10 +20,6 @@ tg::OpWorkspace g_workspace;  // 16-bit weights of the dense path
 // place is the same for every shape: each launch leaves them at zero for the stream's next.
 constexpr int64_t kCounterBytes = 64 * 1024;
 tg::OpWorkspace g_tc(kCounterBytes);
-
-bool misaligned(const void* p, unsigned bytes) {
-    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
-}
 
 template <typename T>
 tg_status_t launch_dense(int32_t in_dtype, const W4Params& p, const tg_epilogue_ex_t& x,
@@ -35,32 +34,6 @@ tg_status_t launch_dense(int32_t in_dtype, const W4Params& p, const tg_epilogue_
     tg::tg_w4_dequant<T><<<static_cast<unsigned>(grid), 256, 0, s>>>(p, static_cast<T*>(ws), ldo);
     if (cudaGetLastError() != cudaSuccess) return TG_ERR_LAUNCH;
     return tg_gemm_ex(in_dtype, p.A, ws, p.C, p.M, p.N, p.K, p.lda, ldo, p.ldc, &x, s);
-}
-
-// One launch with dependent launch allowed, in clusters of `cluster` blocks.
-template <typename... Args, typename... Given>
-tg_status_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster,
-                   cudaStream_t s, Given... given) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args>(given)...) != cudaSuccess) {
-        cudaGetLastError();
-        return TG_ERR_LAUNCH;
-    }
-    return TG_OK;
 }
 
 constexpr int kSmem = 226 * 1024;
@@ -82,30 +55,6 @@ int64_t w4_smem_bytes(tg::W4Launch* q) {
         }
     }
     return kSmem + 1;
-}
-
-// Clusters of `size` blocks that the device holds at once.
-template <typename Kernel>
-int max_clusters(Kernel kernel, int size, int threads, size_t smem, const tg::OpDevice& dev) {
-    if (size == 1) return dev.num_sms;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = static_cast<unsigned>(size);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(size * (dev.num_sms / size)));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return n;
 }
 
 // NT: tokens / 8.
