@@ -45,7 +45,7 @@ def check(tg, a, b, rows):
         assert torch.equal(got, want[:m]), (m, float((got - want[:m]).abs().max()))
 
 
-ROWS = (1, 8, 9, 16, 17, 32, 33, 48, 64, 65, 100, 129, 256, 300)
+ROWS = (1, 7, 8, 9, 12, 16, 17, 24, 32, 33, 48, 64, 65, 100, 129, 256, 300)
 
 
 @pytest.mark.parametrize("N,K", [(300, 28672), (300, 131071), (4096, 8192), (2500, 28672), (19456, 8192),
@@ -64,8 +64,10 @@ def test_halves_that_cancel(tg, N, K):
 
 
 @pytest.mark.parametrize("N,K", [(200, 131071), (1000, 28672), (640, 8192), (19456, 4096), (6000, 20000),
-                                 (128, 1032), (20000, 1160)])
+                                 (128, 1032), (20000, 1160), (600, 8192), (100, 9001), (3600, 8200)])
 def test_any_codes(tg, N, K):
+    """Few rows of long and of wide weights among them, whose sums are 32-bit numbers from the start:
+    no code may be lost, however small its part of a sum."""
     check(tg, ints(300, K, -128, 128, 3), ints(N, K, -128, 128, 4), ROWS)
 
 

@@ -663,15 +663,16 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
                 float t = (b3 ? f : e) + __shfl_xor_sync(0xffffffffu, b3 ? e : f, 8);  // sum lane / 8
 #pragma unroll
                 for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-                float mean, var, p1, p2;  // of the block: mean - m, Σ (v - mean)², Σ dn, Σ dn (v - mean)
+                // of the block: base and mean - base, Σ (v - mean)², Σ dn, Σ dn (v - mean)
+                float base, rest, var, p1, p2;
                 if (warps == 1) {
                     const float d1 = __shfl_sync(0xffffffffu, t, 0), d2 = __shfl_sync(0xffffffffu, t, 8);
-                    mean = d1 * here_inv;
-                    var = d2 - mean * d1;
+                    base = m;
+                    rest = d1 * here_inv;
+                    var = d2 - rest * d1;
                     p1 = __shfl_sync(0xffffffffu, t, 16);
-                    p2 = __shfl_sync(0xffffffffu, t, 24) - mean * p1;
-                    off = mean;
-                    if (MULTI) mean += m;
+                    p2 = __shfl_sync(0xffffffffu, t, 24) - rest * p1;
+                    off = rest;
                 } else {
                     float* r = &red[turn][0][group * warps];
                     if ((lane & 7) == 0) r[(1 + (lane >> 3)) * kLnGradWarps + warp] = t;
@@ -696,26 +697,29 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
                     var = __shfl_sync(0xffffffffu, z, 0);
                     p2 = __shfl_sync(0xffffffffu, z, 16);
                     off = shift - (m - m0);
-                    mean = m0 + shift;
+                    base = m0;
+                    rest = shift;
                 }
                 if constexpr (MULTI) {
-                    const float send[4] = {mean, var, p1, p2};
+                    // (the block's mean in two parts: far from zero it loses in one what counts)
+                    const float send[5] = {base, rest, var, p1, p2};
                     const float* got = peers.exchange(send);
                     const float from = got[0];
+                    auto above = [&](int b) { return got[8 * b] - from + got[8 * b + 1]; };  // from
                     auto columns = [&](int b) {
                         return static_cast<float>(min(static_cast<int>(p.cols) - b * part, part));
                     };
                     float shift = 0.0f;
-                    for (int b = 1; b < split; ++b) shift = fmaf(columns(b), got[8 * b] - from, shift);
+                    for (int b = 0; b < split; ++b) shift = fmaf(columns(b), above(b), shift);
                     shift *= inv;
                     var = p1 = p2 = 0.0f;
                     for (int b = 0; b < split; ++b) {
-                        const float g = got[8 * b] - from - shift;
-                        var += fmaf(columns(b) * g, g, got[8 * b + 1]);
-                        p1 += got[8 * b + 2];
-                        p2 += fmaf(g, got[8 * b + 2], got[8 * b + 3]);
+                        const float g = above(b) - shift;
+                        var += fmaf(columns(b) * g, g, got[8 * b + 2]);
+                        p1 += got[8 * b + 3];
+                        p2 += fmaf(g, got[8 * b + 3], got[8 * b + 4]);
                     }
-                    off += shift - (mean - from);
+                    off += shift - (base - from + rest);
                 }
                 s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
                 if (!(var == var)) s = var;  // (fmaxf would turn a NaN into 0)
