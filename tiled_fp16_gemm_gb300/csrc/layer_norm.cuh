@@ -172,6 +172,12 @@ __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
 // columns a block apart (addresses in registers, 80 us), runs of 4 or 2 neighbours instead of 8 (bf16
 // 57 and 63 us).
 
+// One over the deviation, from Σ (v - mean)².
+__device__ __forceinline__ float ln_scale_of(float squares, float inv, float eps) {
+    const float s = rsqrtf(fmaxf(squares, 0.0f) * inv + eps);
+    return squares == squares ? s : squares;  // (fmaxf turns a NaN into 0)
+}
+
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -393,10 +399,8 @@ __global__ void __launch_bounds__(SM, 1)
             var = ln_warp_sum(has ? fmaf(gu, fmaf(count, gu, 2.0f * s1), stat[2][lane]) : 0.0f);
             off = shift - (m - m0);
         }
-        const float s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
-        // (fmaxf would turn a NaN into 0)
-        const float ss = var == var ? s : var;
-        const F2 s2 = f2(ss, ss), o2 = f2(-off, -off);
+        const float s = ln_scale_of(var, inv, p.eps);
+        const F2 s2 = f2(s, s), o2 = f2(-off, -off);
         TX* h = static_cast<TX*>(p.h) + row * p.ldh + c.first;
         c.either([&](auto whole) {
             constexpr bool ALL = decltype(whole)::value;
@@ -721,8 +725,7 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
                     }
                     off += shift - (base - from + rest);
                 }
-                s = rsqrtf(fmaxf(var, 0.0f) * inv + p.eps);
-                if (!(var == var)) s = var;  // (fmaxf would turn a NaN into 0)
+                s = ln_scale_of(var, inv, p.eps);
                 m1 = p1 * inv;
                 m2 = p2 * inv * s;
             }
@@ -806,7 +809,8 @@ __global__ void __launch_bounds__(32 * kLnGradWarps, 1)
 
 // ------------------------------------------------------------------ any width and stride
 //
-// A row per block and turn; values are read again for each pass, from L2.
+// A row per block and turn; values are read again for each pass, from L2.  The second pass takes the
+// differences from the first one's mean, and with them what that lacks.
 
 template <typename TX, typename TR, int MODE>
 __global__ void __launch_bounds__(256) tg_layer_norm_simple(const LayerNormParams p) {
@@ -821,21 +825,24 @@ __global__ void __launch_bounds__(256) tg_layer_norm_simple(const LayerNormParam
             const float v = op_to_float(x[c]);
             return r != nullptr ? v + op_to_float(r[c]) : v;
         };
-        float mean = 0.0f, s = 1.0f;
+        float m = 0.0f, off = 0.0f, s = 1.0f;  // the mean is m + off
         if (MODE != kLnRaw) {
-            float a = 0.0f;
+            float a = 0.0f, b = 0.0f;
             for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) a += value(c);
-            mean = norm_block_sum(a, red) * inv;
+            m = norm_block_sum(a, red) * inv;
             a = 0.0f;
             for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
-                const float d = value(c) - mean;
-                a += d * d;
+                const float d = value(c) - m;
+                a += d;
+                b += d * d;
             }
-            s = rsqrtf(norm_block_sum(a, red) * inv + p.eps);
+            a = norm_block_sum(a, red);
+            off = a * inv;
+            s = ln_scale_of(norm_block_sum(b, red) - off * a, inv, p.eps);
         }
         auto normed = [&](float v, int64_t c) {
             if (MODE == kLnRaw) return v;
-            const float n = (v - mean) * s;
+            const float n = (v - m - off) * s;
             return fmaf(n, p.w != nullptr ? p.w[c] : 1.0f, p.b != nullptr ? p.b[c] : 0.0f);
         };
         float scale = 0.0f;
@@ -887,26 +894,30 @@ __global__ void __launch_bounds__(256) tg_layer_norm_grad_simple(const LayerNorm
             const float d = op_to_float(dh[c]);
             return p.w != nullptr ? d * p.w[c] : d;
         };
-        float mean = 0.0f, s = 0.0f, m1 = 0.0f, m2 = 0.0f;
+        float m = 0.0f, off = 0.0f, s = 0.0f, m1 = 0.0f, m2 = 0.0f;  // the mean is m + off
         if (dh != nullptr) {  // else nothing is taken of v, which need not be finite then
-            float a = 0.0f, b = 0.0f, d = 0.0f;
+            float a = 0.0f, a2 = 0.0f, b = 0.0f, d = 0.0f;
             for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) a += value(c);
-            mean = norm_block_sum(a, red) * inv;
+            m = norm_block_sum(a, red) * inv;
             a = 0.0f;
             for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
-                const float u = value(c) - mean, dn = dn_at(c);
-                a += u * u;
+                const float u = value(c) - m, dn = dn_at(c);
+                a += u;
+                a2 += u * u;
                 b += dn;
                 d += dn * u;
             }
-            s = rsqrtf(norm_block_sum(a, red) * inv + p.eps);
-            m1 = norm_block_sum(b, red) * inv;
-            m2 = norm_block_sum(d, red) * inv * s;
+            a = norm_block_sum(a, red);
+            off = a * inv;
+            s = ln_scale_of(norm_block_sum(a2, red) - off * a, inv, p.eps);
+            b = norm_block_sum(b, red);
+            m1 = b * inv;
+            m2 = (norm_block_sum(d, red) - off * b) * inv * s;
         }
         for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
             float d = dy != nullptr ? op_to_float(dy[c]) : 0.0f;
             if (dh != nullptr) {
-                const float n = (value(c) - mean) * s;
+                const float n = (value(c) - m - off) * s;
                 d += s * (dn_at(c) - m1 - n * m2);
                 if (ww != nullptr) ww[c] = (row == row0 ? 0.0f : ww[c]) + op_to_float(dh[c]) * n;
                 if (wb != nullptr) wb[c] = (row == row0 ? 0.0f : wb[c]) + op_to_float(dh[c]);
