@@ -33,6 +33,30 @@ const Limits& limits_of(Kernel kernel, int threads, int smem, const tg::OpDevice
     return lim;
 }
 
+int64_t chunks_of(int64_t K) { return (K + tg::kI8FewK - 1) / tg::kI8FewK; }
+
+// What a block of the kernel for few rows has in shared memory.
+struct FewRoom {
+    int64_t x_pitch;  // bytes of a token
+    int64_t fixed;    // bytes besides the sums
+    int64_t tiles;    // whose sums fit besides
+};
+FewRoom few_room(int64_t M, int64_t K, int cluster, int stages) {
+    FewRoom r;
+    const int64_t slice = (chunks_of(K) + cluster - 1) / cluster;
+    r.x_pitch = slice * tg::kI8FewK * (M > 8 ? 2 : 1) + 64;
+    r.fixed = 1024 + int64_t{tg::kI8FewWarps} * stages * tg::kI8FewStep + tg::kI8FewBars + M * r.x_pitch;
+    const int64_t room = kSmem - r.fixed - M * 16;
+    r.tiles = room < 0 ? 0 : room / (M * tg::kI8FewRows * 4);
+    return r;
+}
+// Whether a block, of a cluster of eight at most, has room for them.
+bool few_fits(int64_t M, int64_t K) {
+    for (int cluster = 1; cluster <= 8 && cluster <= chunks_of(K); cluster *= 2)
+        if (few_room(M, K, cluster, 2).tiles >= 1) return true;
+    return false;
+}
+
 // Few rows of A (NT: tokens / 8).
 struct FewPlan {
     tg::I8Few q;
@@ -56,22 +80,21 @@ FewPlan plan_few(const I8Params& p, const tg::OpDevice& dev) {
     q.p = p;
     const int64_t tiles = (p.N + tg::kI8FewRows - 1) / tg::kI8FewRows;
     q.tiles = static_cast<int32_t>(tiles);
-    q.chunks = static_cast<int32_t>((p.K + tg::kI8FewK - 1) / tg::kI8FewK);
+    q.chunks = static_cast<int32_t>(chunks_of(p.K));
     constexpr double round = NT <= 2 ? 0.73 : NT == 4 ? 0.8 : 1.4;
     for (int i = 0; i < 4; ++i) {
         q.cluster = 1 << i;
         if (q.cluster > q.chunks || lim.clusters[i] < 1) break;
         const int64_t slice = (q.chunks + q.cluster - 1) / q.cluster;
-        q.x_pitch = static_cast<int32_t>(slice * tg::kI8FewK * (NT > 1 ? 2 : 1) + 64);
         int64_t clusters = tiles < lim.clusters[i] ? tiles : lim.clusters[i];
         // (with few steps a shallow ring: then the next call's blocks find room beside this one's, and
         // B comes to L2 meanwhile; one row of 4096×4096 5.4 us, with three stages 6.0)
         const int64_t each = ((tiles + clusters - 1) / clusters * slice + tg::kI8FewWarps - 1) / tg::kI8FewWarps;
         for (q.stages = each <= 6 ? 2 : tg::kI8FewStages; q.stages >= 2; --q.stages) {
-            const int64_t fixed = 1024 + int64_t{tg::kI8FewWarps} * q.stages * tg::kI8FewStep + tg::kI8FewBars +
-                                  p.M * q.x_pitch;
+            const FewRoom of_block = few_room(p.M, p.K, q.cluster, q.stages);
+            q.x_pitch = static_cast<int32_t>(of_block.x_pitch);
             // (a block keeps the sums of its tiles: very many rows of B take several waves)
-            const int64_t room = (kSmem - fixed - p.M * 16) / (p.M * tg::kI8FewRows * 4);
+            const int64_t room = of_block.tiles;
             int64_t rounds = (tiles + clusters - 1) / clusters;
             if (room < 1 || (room < rounds && q.stages > 2)) continue;
             if (rounds > room) {
@@ -87,7 +110,7 @@ FewPlan plan_few(const I8Params& p, const tg::OpDevice& dev) {
             if (time < best.time && clusters * q.cluster <= tg::kOpMaxDim) {
                 best.time = time;
                 best.q = q;
-                best.smem = static_cast<size_t>(fixed + 4 * p.M * q.sums_pitch);
+                best.smem = static_cast<size_t>(of_block.fixed + 4 * p.M * q.sums_pitch);
                 best.grid = clusters * q.cluster;
             }
             break;
@@ -170,9 +193,24 @@ int64_t slot_bytes(int64_t M, int64_t K) {
     return int64_t{tg::kI8MaxClusters} * tg::kWideCluster * tile_tokens(M) * tg::kTcRows * 4 * (more_runs(K) ? 2 : 1);
 }
 constexpr int64_t kHeadBytes = tg::kI8CounterBytes + tg::kI8PeakBytes;
-int64_t workspace_bytes(int64_t M, int64_t, int64_t K) {
-    if (M <= 8 || K == 0) return 0;
+int64_t wide_bytes(int64_t M, int64_t K) {
     return kHeadBytes + slot_bytes(M, K) + slab_rows(M, K) * up(K, tg::kTcK) * 2;
+}
+
+// Whether the kernel for few rows is the faster one: up to 16 rows always, more of them with small
+// weights.  Measured, us, few / wide: 16384×8192 with 16 rows 28.7 / 30.9, 32 rows 48 / 31;
+// 4096×28672 with 16 rows 29.8 / 31.2; 9728×2560 with 32 rows 13.6 / 13.8, 9728×4096 18.0 / 17.4;
+// 4096×1024 with 48 rows 8.6 / 9.1, 64 rows 11.6 / 9.2; 2560×2560 with 48 rows 10.8 / 10.8;
+// 1024×1024 with 64 rows 9.0 / 9.0.
+bool prefer_few(int64_t M, int64_t N, int64_t K) {
+    const int64_t codes = N * K;
+    return M <= 16 || (M <= 32 && codes <= 30000000) || (M <= 48 && codes <= 5000000) ||
+           (M <= 64 && codes <= 1000000);
+}
+// None for the kernel for few rows.  (On a device that holds none of its clusters the other takes the
+// library's buffer.)
+int64_t workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    return M <= 8 || K == 0 || (prefer_few(M, N, K) && few_fits(M, K)) ? 0 : wide_bytes(M, K);
 }
 
 template <typename TC>
@@ -184,7 +222,7 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
     tg::OpWorkspace::Hold hold;  // until the last product is launched
     if (ws == nullptr) {
         const tg_status_t st = g_workspace.get(
-            dev.dev, s, static_cast<size_t>(workspace_bytes(whole.M, whole.N, whole.K)), &ws, &hold);
+            dev.dev, s, static_cast<size_t>(wide_bytes(whole.M, whole.K)), &ws, &hold);
         if (st != TG_OK) return st;
     }
     tg::I8Wide q;
@@ -241,17 +279,6 @@ tg_status_t launch_wide(const I8Params& whole, const tg::OpDevice& dev, void* ws
     return TG_OK;
 }
 
-// Whether the kernel for few rows is the faster one: up to 16 rows always, more of them with small
-// weights.  Measured, us, few / wide: 16384×8192 with 16 rows 28.7 / 30.9, 32 rows 48 / 31;
-// 4096×28672 with 16 rows 29.8 / 31.2; 9728×2560 with 32 rows 13.6 / 13.8, 9728×4096 18.0 / 17.4;
-// 4096×1024 with 48 rows 8.6 / 9.1, 64 rows 11.6 / 9.2; 2560×2560 with 48 rows 10.8 / 10.8;
-// 1024×1024 with 64 rows 9.0 / 9.0.
-bool prefer_few(const I8Params& p) {
-    const int64_t codes = p.N * p.K;
-    return p.M <= 16 || (p.M <= 32 && codes <= 30000000) || (p.M <= 48 && codes <= 5000000) ||
-           (p.M <= 64 && codes <= 1000000);
-}
-
 // Launches the kernel for few rows; false where no shape fits.
 template <typename TC, int NT>
 bool take_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_status_t* st) {
@@ -264,7 +291,7 @@ bool take_few(const I8Params& p, const tg::OpDevice& dev, cudaStream_t s, tg_sta
 template <typename TC>
 tg_status_t launch_type(const I8Params& p, const tg::OpDevice& dev, void* ws, cudaStream_t s) {
     tg_status_t st = TG_OK;
-    if (p.K > 0 && prefer_few(p)) {
+    if (p.K > 0 && prefer_few(p.M, p.N, p.K)) {
         if (p.M <= 8 ? take_few<TC, 1>(p, dev, s, &st)
             : p.M <= 16 ? take_few<TC, 2>(p, dev, s, &st)
             : p.M <= 32 ? take_few<TC, 4>(p, dev, s, &st)
@@ -302,6 +329,7 @@ tg_status_t gemm_i8(const int8_t* A, int64_t lda, const float* sa, const int8_t*
         if (misaligned(B, 16) || ldb % 16 != 0) return TG_ERR_MISALIGNED;
     }
     if (workspace != nullptr && bytes < workspace_bytes(M, N, K)) return TG_ERR_INVALID_VALUE;
+    if (K > 0 && bytes < wide_bytes(M, K)) workspace = nullptr;  // (none is needed)
     tg::OpDevice dev;
     tg_status_t st = tg::op_device(&dev);
     if (st != TG_OK) return st;
