@@ -53,7 +53,7 @@ __device__ __forceinline__ float i8_value(const I8Params& p, float sum, float sa
 // 2^24, which eight steps do not pass; then they go to the 32-bit sums.  (16 tokens on s8:
 // 16384×8192 in 40 us.  The tokens kept as bytes and decoded with each step's codes: 32 us.)
 //
-// Measured, bf16 results, random codes: 28672×4096 with 1 / 8 / 16 tokens 21.5 / 23.0 / 26.8 us (5.5
+// Measured, bf16 results, random codes: 28672×4096 with 1 / 8 / 16 tokens 20.8 / 23.0 / 26.8 us (5.7
 // TB/s with one), 16384×8192 24.3 / 25.5 / 28.9, 4096×28672 23.1 / 24.4 / 30.0 (16 tokens' fp16 takes
 // clusters of eight, which hold 120 of the 152 SMs), 4096×4096 5.7 / 6.2 / 8.1, 1024×1024 3.1 / 3.8 / 3.9.
 // Bound by memory, with some 3 us before the first codes and behind the last.  Three stages of a

@@ -160,7 +160,7 @@ __device__ __forceinline__ uint32_t ln_block_max(uint32_t v, uint32_t* red) {
 //   Σ (v - mu)² = Σ_u (Σd² + 2 g_u Σd + n_u g_u²),   g_u = m_u - mu
 // so neither a mean far from zero nor warps with different means cost digits.
 //
-// Measured: 8192×4096 bf16 on an fp32 stream 60 us (6.7 TB/s), bf16 47 us, its codes 59 and 49 us; rows of
+// Measured, calls back to back on inputs in turn: 8192×4096 bf16 on an fp32 stream 60 us (6.7 TB/s), bf16 47 us, its codes 59 and 49 us; rows of
 // x as codes 17 us; 600×16384 bf16 16.1 us; 8192×1536 19 us; unaligned, 1021×5119 13 us, 4096×767 10 us;
 // one row of 4096 2.1 us.  Bound by memory on the fp32 stream; else by the way of a row from its loads to
 // its stores, with five rows of 4096 on an SM (96 registers).  The weights' reads, from L1, are some 4 us
@@ -476,8 +476,9 @@ __global__ void __launch_bounds__(SM, 1)
 // MULTI: the `split` blocks of a cluster share their rows, `part` columns each, and exchange
 // their means and sums: for rows of more columns than a block's threads have in registers.
 //
-// Measured: 8192×4096 bf16 67 us (6.0 TB/s), on an fp32 stream 107 us; 8192×1024 24 us, 2048×8192 40
-// us, 600×16384 34 us; unaligned, 2050×1537 on an fp32 stream 22 us, 1021×5119 27 us; 256×1024 5.9 us.
+// Measured, in bf16 with a residual: 8192×4096 66 us (6.1 TB/s), on an fp32 stream 107 us; 8192×1024 23
+// us, 2048×8192 40 us, 600×16384 34 us; unaligned, 2050×1537 on an fp32 stream 21 us, 1021×5119 27 us;
+// 256×1024 5.9 us (in fp16 without a residual 5.1).
 // The column sums (a block's share, the second launch) are 2 to 5 us of each.  Aligned rows are bound
 // by memory, unaligned ones by the issue of single-value accesses, rows that blocks share by their
 // exchanges.  (The groups' sums joined by the first group alone, one sum after the other: 2 us more.)
