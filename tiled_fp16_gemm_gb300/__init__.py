@@ -1160,7 +1160,8 @@ def layer_norm_backward(dy, dh, x, residual=None, *, weight=None, bias=None, eps
 def gemm_i8(a, b, ascale, bscale, relu: bool = False, out=None, stream=None, *, bias=None,
             residual=None, out_dtype=None):
     """C = out(act(ascale[m] · bscale[n] · (a @ b.T) + bias) + residual) of 8-bit integers
-    with a scale per row of a (token) and per row of b (channel).
+    with a scale per row of a (token) and per row of b (channel).  The sums a @ b.T are
+    exact; scales, bias and residual are applied in fp32, and C is rounded once.
 
     a: CUDA int8 tensor M×K (unit column stride), for instance the codes of ``quantize_rows``
     or ``layer_norm_i8``.  b: CUDA int8 tensor N×K, the [out][in] orientation of a weight,
